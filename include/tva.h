@@ -242,6 +242,86 @@ tva_status commit_accepted_kv(int batch, int num_kv_heads, int head_dim, tva_dty
                               const void* tree_v, const int32_t* dst_row, void* k_cache, void* v_cache,
                               int32_t* dev_status, void* stream);
 
+/* Tree-verification attention under a sliding window with sinks, over a ragged batch
+ * (LongSpec's draft layers attend through a window of 512, "Memory-Efficient
+ * Architecture", and its Anchor-Offset Indices keep the first four positions as sinks;
+ * the pages give no interface).  A node's position is P_b plus its number of proper
+ * ancestors; prefix row s stands at position s.  Node i at position t sees the key at
+ * position s - a prefix row, or an ancestor or itself - when t - s < window or s < sinks.
+ *   window   >= 1: a node always sees itself (else TVA_ERR_INVALID_ARG)
+ *   sinks    >= 0
+ * Everything else, and the layout of every buffer, is as for tree_verify_attn_varlen;
+ * lse covers the keys that the row sees.  The work and the bytes read grow with
+ * min(P_b, window + sinks), not with P_b.  A K / V row of the cache that no node of its
+ * sequence sees may hold anything, NaN included; a V row that some node of the sequence
+ * sees must be finite (one weight of a product is zero for the nodes that do not see it). */
+tva_status tree_verify_attn_window_varlen(const tva_params* p, int window, int sinks, const void* q,
+                                          const void* k_cache, const void* v_cache, const void* tree_k,
+                                          const void* tree_v, const int32_t* parent, void* out, float* lse,
+                                          void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                          void* stream);
+
+/* 4-bit cache.  One cache row of one KV head is a record of tva_kv4_record_bytes(d) bytes
+ * (144 at d = 128, 80 at d = 64, against 512 and 256 in 16 bits); a cache is
+ * [kv_capacity, Hkv, record], 16-byte aligned.  A record is
+ *   d/2 bytes of K codes, d/2 of V codes, d/16 K scales, d/16 V scales, zeros up to a
+ *   multiple of 16 bytes.
+ * The little-endian 32-bit code word i holds elements 8i .. 8i+7: element 8i + 2j in bits
+ * 4j .. 4j+3, element 8i + 2j + 1 in bits 16+4j .. 16+4j+3 (j = 0 .. 3).  A code n (1 ..
+ * 15 as written here) stands for (n - 8) * scale.  Scale byte b belongs to 16 consecutive
+ * elements and is an unsigned float of 5 exponent bits (bias 15, subnormals) and 3
+ * mantissa bits, 0 .. 2560: shifted left by 7 it is the same value in float16.  Every
+ * value that a record can stand for is exact in bfloat16, float16 and float32.
+ * Rounding: a block's scale is its largest magnitude / 7 rounded to the nearest scale
+ * (ties to the even byte; 2560 at most); a value's code is 8 + value / scale rounded to
+ * the nearest whole number (ties to even), limited to 8 - 7 .. 8 + 7; all exactly, as
+ * real numbers.  A value is therefore off by at most half its scale, except that
+ * magnitudes beyond 7.5 * 2560 (and infinities) saturate at 7 * 2560, that a block whose
+ * largest magnitude is below 7 * 2^-18 becomes 0, and that NaN becomes 0. */
+
+/* Bytes of one record, or 0 if head_dim is not 64 or 128. */
+size_t tva_kv4_record_bytes(int head_dim);
+
+/* Quantises rows into the 4-bit cache.
+ *   k, v     [num_rows, Hkv, d] of `dtype` (bf16, fp16 or fp32)
+ *   slot     [num_rows] device int32: the cache row of each; a negative one (padding) is
+ *            skipped, one >= kv_capacity is skipped and TVA_ERR_INVALID_ARG goes to
+ *            *dev_status.  Slots are distinct (else which row's codes and scales the
+ *            record ends up with, or a mix of them, is unspecified)
+ * No other cache row is written.  k, v and kv4_cache are 16-byte aligned; k and v must not
+ * overlap the cache.  num_rows = 0 does nothing. */
+tva_status append_kv4(int num_rows, int num_kv_heads, int head_dim, tva_dtype dtype, long long kv_capacity,
+                      const void* k, const void* v, const int32_t* slot, void* kv4_cache, int32_t* dev_status,
+                      void* stream);
+
+/* The values that cache rows stand for, exactly: k, v [num_rows, Hkv, d] of `dtype` from
+ * rows slot[0 .. num_rows - 1], or from rows 0 .. num_rows - 1 when slot is null.  A row
+ * whose slot is negative reads as zeros, as does one >= kv_capacity, for which
+ * TVA_ERR_INVALID_ARG goes to *dev_status; slots may repeat. */
+tva_status read_kv4(int num_rows, int num_kv_heads, int head_dim, tva_dtype dtype, long long kv_capacity,
+                    const void* kv4_cache, const int32_t* slot, void* k, void* v, int32_t* dev_status, void* stream);
+
+/* commit_accepted_kv into a 4-bit cache: row j < accept_len[b] of the path is quantised
+ * into cache row dst_row[b] + j.  Arguments, bounds and errors as for commit_accepted_kv
+ * (a head_dim or dtype that is not supported is TVA_ERR_UNSUPPORTED). */
+tva_status commit_accepted_kv4(int batch, int num_kv_heads, int head_dim, tva_dtype dtype, int node_capacity,
+                               int max_nodes, long long kv_capacity, const int32_t* cu_nodes,
+                               const int32_t* accept_len, const int32_t* accept_path, const void* tree_k,
+                               const void* tree_v, const int32_t* dst_row, void* kv4_cache, int32_t* dev_status,
+                               void* stream);
+
+/* Tree-verification attention whose prefix cache is held in 4 bits: tree_verify_attn_varlen
+ * (window = 0; sinks then has no effect) or tree_verify_attn_window_varlen (window >= 1)
+ * with K / V row j of sequence b in records cu_prefix[b] + j of kv4_cache [kv_capacity,
+ * Hkv, record].  q, tree_k, tree_v and out are bf16 or fp16 (TVA_FP32 is
+ * TVA_ERR_UNSUPPORTED); the tree's own K / V stay in 16 bits until they are committed.
+ * The records' values are used exactly; the rest of the arithmetic is that of the 16-bit
+ * form.  The workspace is that of tva_workspace_size(p). */
+tva_status tree_verify_attn_kv4_varlen(const tva_params* p, int window, int sinks, const void* q,
+                                       const void* kv4_cache, const void* tree_k, const void* tree_v,
+                                       const int32_t* parent, void* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, int32_t* dev_status, void* stream);
+
 /* Stochastic verification of draft chains by modified rejection sampling ("Faster
  * decoding", "Modified rejection sampling keeps the target distribution"): left to
  * right, draft token x at a position is accepted with probability min(1, p(x)/q(x));

@@ -17,6 +17,8 @@ definition.
 * :mod:`oracle.expected_tokens` - expected tokens per verification cycle.
 * :mod:`oracle.kv_commit` - committing the accepted path's K/V into the cache.
 * :mod:`oracle.rejection_sampling` - stochastic verification of a draft chain.
+* :mod:`oracle.window_attention` - tree attention under a sliding window with sinks.
+* :mod:`oracle.kv4_cache` - the 4-bit K/V record: rounding, layout, values.
 * :mod:`oracle.gdn_tree` - tree verification for Gated DeltaNet layers.
 
 Every function is pinned by ``tests/test_oracle_*.py`` against facts fixed by the pages
@@ -29,6 +31,8 @@ from .acceptance import accept_longest_path
 from .expected_tokens import expected_tokens, survival_from_conditional, iid_expected_tokens
 from .kv_commit import commit_accepted_kv
 from .rejection_sampling import verify_chain_sampling, quantised_draw
+from .window_attention import tree_verify_window_attention, tree_verify_window_rows, window_visible
+from .kv4_cache import SCALES, kv4_pack, kv4_quantise, kv4_record_bytes, kv4_unpack, kv4_values
 from .gdn_tree import gdn_tree_outputs, gdn_path_state
 
 __all__ = [
@@ -44,6 +48,15 @@ __all__ = [
     "commit_accepted_kv",
     "verify_chain_sampling",
     "quantised_draw",
+    "tree_verify_window_attention",
+    "tree_verify_window_rows",
+    "window_visible",
+    "SCALES",
+    "kv4_pack",
+    "kv4_quantise",
+    "kv4_record_bytes",
+    "kv4_unpack",
+    "kv4_values",
     "gdn_tree_outputs",
     "gdn_path_state",
 ]

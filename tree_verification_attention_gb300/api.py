@@ -18,7 +18,8 @@ __all__ = [
     "TvaError", "Params", "load_library", "workspace_size", "num_workers",
     "tree_verify_attn_varlen", "tree_verify_attn_partials", "tree_verify_attn_combine",
     "tree_verify_attn", "read_device_status", "release", "diag_set_wait_limit", "diag_use_cta_pair", "accept_longest_path",
-    "status_string", "STATUS",
+    "tree_verify_attn_window_varlen", "tree_verify_attn_kv4_varlen", "kv4_record_bytes", "alloc_kv4_cache", "append_kv4",
+    "read_kv4", "commit_accepted_kv4", "status_string", "STATUS",
 ]
 
 STATUS = {0: "TVA_OK", 1: "TVA_ERR_INVALID_ARG", 2: "TVA_ERR_UNSUPPORTED", 3: "TVA_ERR_BAD_TREE",
@@ -78,6 +79,12 @@ def load_library(path: str | None = None):
         "verify_chain_sampling": (_I, [_I, _I, _I, ctypes.c_longlong, ctypes.c_longlong, _P, _P, _P, _P, _P, _P,
                                        _P, _P, _P, _P]),
         "gdn_tree_verify": (_I, [_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+        "tree_verify_attn_window_varlen": (_I, [PP, _I, _I] + [_P] * 9 + [_SZ, _P, _P]),
+        "tree_verify_attn_kv4_varlen": (_I, [PP, _I, _I] + [_P] * 8 + [_SZ, _P, _P]),
+        "tva_kv4_record_bytes": (_SZ, [_I]),
+        "append_kv4": (_I, [_I, _I, _I, _I, ctypes.c_longlong] + [_P] * 6),
+        "read_kv4": (_I, [_I, _I, _I, _I, ctypes.c_longlong] + [_P] * 6),
+        "commit_accepted_kv4": (_I, [_I, _I, _I, _I, _I, _I, ctypes.c_longlong] + [_P] * 9),
         "tva_status_string": (ctypes.c_char_p, [_I]),
         "tva_last_error": (ctypes.c_char_p, []),
     }
@@ -386,4 +393,175 @@ def tree_verify_attn_varlen_noalloc(q, k_cache, v_cache, tree_k, tree_v, parent,
     if code != 0:
         detail = lib.tva_last_error().decode()
         raise TvaError(code, "tree_verify_attn_varlen_noalloc" + (f" [{detail}]" if detail else ""))
+    return out, lse
+
+
+def _device_status(dev_status, device):
+    if dev_status is None:
+        return torch.zeros(1, dtype=torch.int32, device=device)
+    return _dev(dev_status, "dev_status", torch.int32)
+
+
+def _one_device(*tensors):
+    """The kernels run on the current device's stream: every tensor has to be there."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != here:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+
+
+def _window_outputs(q, out, lse):
+    N, Hq, _ = q.shape
+    out = torch.empty_like(q) if out is None else _dev(out, "out", q.dtype)
+    lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device) if lse is None else _dev(lse, "lse", torch.float32)
+    if out.shape != q.shape or lse.shape != (N, Hq):
+        raise ValueError("out must have q's shape and lse [N, Hq]")
+    return out, lse
+
+
+def _check_heads(q, tree_k, params):
+    if q.dim() != 3 or tree_k.dim() != 3 or tree_k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [N, Hq, d] and tree_k [N, Hkv, d]")
+    if params.num_kv_heads != tree_k.shape[1] or params.num_q_heads != q.shape[1] or params.head_dim != q.shape[2]:
+        raise ValueError("params do not describe these tensors")
+
+
+def tree_verify_attn_window_varlen(q, k_cache, v_cache, tree_k, tree_v, parent, cu_prefix, cu_nodes,
+                                   max_prefix_len, max_nodes, window, sinks=0, out=None, lse=None, workspace=None,
+                                   dev_status=None, softmax_scale=0.0, stream=None, params=None):
+    """tree_verify_attn_varlen under a sliding window: a node at position t (prefix length
+    plus proper ancestors) sees the key at position s when ``t - s < window`` or
+    ``s < sinks``.  ``window`` >= 1.  Returns (out [N, Hq, d], lse [N, Hq] float32)."""
+    _attn_inputs(q, k_cache, v_cache, tree_k, tree_v, parent, cu_prefix, cu_nodes)
+    _one_device(q, k_cache, v_cache, tree_k, tree_v, parent, cu_prefix, cu_nodes, out, lse, workspace, dev_status)
+    p = params or make_params(q, k_cache, cu_prefix, cu_nodes, tree_k.shape[1], max_prefix_len, max_nodes,
+                              softmax_scale)
+    _check_heads(q, tree_k, p)
+    if k_cache.shape[1:] != tree_k.shape[1:]:
+        raise ValueError("k_cache must be [rows, Hkv, d]")
+    out, lse = _window_outputs(q, out, lse)
+    if workspace is None:
+        workspace = alloc_workspace(p, q.device)
+    dev_status = _device_status(dev_status, q.device)
+    code = load_library().tree_verify_attn_window_varlen(
+        ctypes.byref(p), int(window), int(sinks), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(tree_k), _ptr(tree_v),
+        _ptr(parent), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream))
+    _check(code, "tree_verify_attn_window_varlen")
+    return out, lse
+
+
+def kv4_record_bytes(head_dim: int) -> int:
+    """Bytes that one row of one KV head takes in a 4-bit cache (K and V together)."""
+    n = int(load_library().tva_kv4_record_bytes(int(head_dim)))
+    if n == 0:
+        raise TvaError(2, "tva_kv4_record_bytes")
+    return n
+
+
+def alloc_kv4_cache(rows, num_kv_heads, head_dim, device="cuda") -> torch.Tensor:
+    """A 4-bit cache [rows, Hkv, record] uint8 of zeros (whose values are all 0)."""
+    return torch.zeros((rows, num_kv_heads, kv4_record_bytes(head_dim)), dtype=torch.uint8, device=device)
+
+
+def _kv4(kv4_cache, num_kv_heads, head_dim):
+    _dev(kv4_cache, "kv4_cache", torch.uint8)
+    if kv4_cache.dim() != 3 or kv4_cache.shape[1] != num_kv_heads or kv4_cache.shape[2] != kv4_record_bytes(head_dim):
+        raise ValueError(f"kv4_cache must be [rows, {num_kv_heads}, {kv4_record_bytes(head_dim)}] uint8")
+    return kv4_cache
+
+
+def _kv4_rows(k, v):
+    _dev(k, "k")
+    if k.dtype not in DTYPES:
+        raise ValueError(f"unsupported dtype {k.dtype}")
+    _dev(v, "v", k.dtype)
+    if k.dim() != 3 or k.shape != v.shape:
+        raise ValueError("k and v must be [rows, Hkv, d], alike")
+
+
+def append_kv4(k, v, slot, kv4_cache, dev_status=None, stream=None):
+    """Quantises k, v [n, Hkv, d] into rows slot[i] (int32; negative: skipped) of the 4-bit
+    cache, in place.  Returns dev_status (int32 [1], 0 = ok)."""
+    _kv4_rows(k, v)
+    _dev(slot, "slot", torch.int32)
+    n, Hkv, d = k.shape
+    if slot.shape != (n,):
+        raise ValueError("slot must hold one row number per row of k")
+    _kv4(kv4_cache, Hkv, d)
+    _one_device(k, v, slot, kv4_cache, dev_status)
+    dev_status = _device_status(dev_status, k.device)
+    code = load_library().append_kv4(n, Hkv, d, DTYPES[k.dtype], kv4_cache.shape[0], _ptr(k), _ptr(v), _ptr(slot),
+                                     _ptr(kv4_cache), _ptr(dev_status), _stream(stream))
+    _check(code, "append_kv4")
+    return dev_status
+
+
+def read_kv4(kv4_cache, head_dim, slot=None, dtype=torch.bfloat16, k=None, v=None, dev_status=None, stream=None):
+    """(k, v) [n, Hkv, head_dim] of ``dtype``: the values that rows slot[i] (int32; negative:
+    zeros) of the 4-bit cache stand for, or all rows in order when ``slot`` is None."""
+    if dtype not in DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    _kv4(kv4_cache, kv4_cache.shape[1] if kv4_cache.dim() == 3 else 0, head_dim)
+    if slot is not None:
+        _dev(slot, "slot", torch.int32)
+        if slot.dim() != 1:
+            raise ValueError("slot must be one-dimensional")
+    shape = (kv4_cache.shape[0] if slot is None else slot.shape[0], kv4_cache.shape[1], int(head_dim))
+    k = torch.empty(shape, dtype=dtype, device=kv4_cache.device) if k is None else _dev(k, "k", dtype)
+    v = torch.empty(shape, dtype=dtype, device=kv4_cache.device) if v is None else _dev(v, "v", dtype)
+    if tuple(k.shape) != shape or tuple(v.shape) != shape:
+        raise ValueError(f"k and v must be {list(shape)}")
+    _one_device(kv4_cache, slot, k, v, dev_status)
+    dev_status = _device_status(dev_status, kv4_cache.device)
+    code = load_library().read_kv4(shape[0], shape[1], shape[2], DTYPES[dtype], kv4_cache.shape[0], _ptr(kv4_cache),
+                                   _ptr(slot), _ptr(k), _ptr(v), _ptr(dev_status), _stream(stream))
+    _check(code, "read_kv4")
+    return k, v
+
+
+def commit_accepted_kv4(cu_nodes, accept_len, accept_path, tree_k, tree_v, dst_row, kv4_cache, max_nodes=None,
+                        dev_status=None, stream=None):
+    """commit_accepted_kv into a 4-bit cache [rows, Hkv, record], in place.  Returns
+    dev_status (int32 [1], 0 = ok)."""
+    for name, t in (("cu_nodes", cu_nodes), ("accept_len", accept_len), ("accept_path", accept_path),
+                    ("dst_row", dst_row)):
+        _dev(t, name, torch.int32)
+    _kv4_rows(tree_k, tree_v)
+    B = cu_nodes.numel() - 1
+    N, Hkv, d = tree_k.shape
+    if accept_len.numel() != B or dst_row.numel() != B or accept_path.numel() != N:
+        raise ValueError("accept_len and dst_row must hold B entries and accept_path one per node")
+    _kv4(kv4_cache, Hkv, d)
+    _one_device(cu_nodes, accept_len, accept_path, tree_k, tree_v, dst_row, kv4_cache, dev_status)
+    if max_nodes is None:
+        max_nodes = int((cu_nodes[1:] - cu_nodes[:-1]).max().item()) if B > 0 else 1
+    dev_status = _device_status(dev_status, tree_k.device)
+    code = load_library().commit_accepted_kv4(
+        B, Hkv, d, DTYPES[tree_k.dtype], N, max(1, int(max_nodes)), kv4_cache.shape[0], _ptr(cu_nodes),
+        _ptr(accept_len), _ptr(accept_path), _ptr(tree_k), _ptr(tree_v), _ptr(dst_row), _ptr(kv4_cache),
+        _ptr(dev_status), _stream(stream))
+    _check(code, "commit_accepted_kv4")
+    return dev_status
+
+
+def tree_verify_attn_kv4_varlen(q, kv4_cache, tree_k, tree_v, parent, cu_prefix, cu_nodes, max_prefix_len,
+                                max_nodes, window=0, sinks=0, out=None, lse=None, workspace=None, dev_status=None,
+                                softmax_scale=0.0, stream=None, params=None):
+    """Tree-verification attention whose prefix rows are records of a 4-bit cache; q, tree_k,
+    tree_v bf16 or fp16.  ``window`` 0: the whole prefix, else as in
+    tree_verify_attn_window_varlen.  Returns (out [N, Hq, d], lse [N, Hq] float32)."""
+    _attn_inputs(q, tree_k, tree_v, tree_k, tree_v, parent, cu_prefix, cu_nodes)
+    p = params or make_params(q, kv4_cache, cu_prefix, cu_nodes, tree_k.shape[1], max_prefix_len, max_nodes,
+                              softmax_scale)
+    _check_heads(q, tree_k, p)
+    _kv4(kv4_cache, tree_k.shape[1], q.shape[2])
+    _one_device(q, kv4_cache, tree_k, tree_v, parent, cu_prefix, cu_nodes, out, lse, workspace, dev_status)
+    out, lse = _window_outputs(q, out, lse)
+    if workspace is None:
+        workspace = alloc_workspace(p, q.device)
+    dev_status = _device_status(dev_status, q.device)
+    code = load_library().tree_verify_attn_kv4_varlen(
+        ctypes.byref(p), int(window), int(sinks), _ptr(q), _ptr(kv4_cache), _ptr(tree_k), _ptr(tree_v), _ptr(parent),
+        _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream))
+    _check(code, "tree_verify_attn_kv4_varlen")
     return out, lse

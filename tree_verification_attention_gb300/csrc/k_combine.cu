@@ -244,7 +244,7 @@ cudaError_t launch_typed(const CombineArgs& a, cudaStream_t s) {
 // workers at most (stream-K), or over the teams that cover its KV head (shared mode).  Smaller sequences shrink the chunk and can raise the count; the
 // kernel loops over any number, this only sizes its first round of loads.
 int expected_partials(const Problem& pr) {
-  const long long tiles = (pr.max_prefix + kKeyTile - 1) / kKeyTile + 1;
+  const long long tiles = (walk_prefix_bound(pr) + kKeyTile - 1) / kKeyTile + 1;
   if (pr.share == 0 && pr.align > 0) return (int)std::min<long long>(pr.align, tiles);
   if (pr.share > 0) {  // a head's columns spread over ceil(tiles / columns per team) + 1 teams
     const long long Q = pr.U / pr.share, C = (long long)pr.Hkv * tiles;

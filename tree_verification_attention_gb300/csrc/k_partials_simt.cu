@@ -13,6 +13,7 @@
 //
 // This path carries the float32 dtype (head_dim 64 or 128).  bfloat16 inputs go to
 // the tensor-core kernel.
+#include "kv4.cuh"
 #include "tva_internal.h"
 
 namespace tva {
@@ -27,6 +28,7 @@ template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
 template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) {
   return __bfloat162float(v);
 }
+template <> __device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
 
 // Four consecutive elements of a row (16-byte aligned for float: rows are D floats and
 // the base pointers are 16-byte aligned).
@@ -39,13 +41,22 @@ __device__ __forceinline__ float4 load4(const T* p) {
   }
 }
 
+// Four consecutive values (dd a multiple of 4) of the K (half 0) or V part of a 4-bit record.
+template <int D>
+__device__ __forceinline__ float4 load4_kv4(const uint8_t* rec, int half, int dd) {
+  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(rec + half * (D / 2)) + dd / 8) >> (dd & 4 ? 8 : 0);
+  const float s = kv4_scale_value(__ldg(rec + D + half * (D / 16) + dd / 16));
+  auto value = [&](int e) { return (float)((int)((w >> kv4_shift(e)) & 15u) - 8) * s; };
+  return make_float4(value(0), value(1), value(2), value(3));
+}
+
 template <int D>
 constexpr size_t simt_smem_bytes() {
   return sizeof(float) * (kRB * (D + 1) + kKT * (D + 1) + kKT * D + kRB * (kKT + 1)) +
          sizeof(uint32_t) * kMaxNodes * 4;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kWin, bool kKv4>
 __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs a) {
   extern __shared__ float smem[];
   float* qs = smem;                          // [kRB][D+1]
@@ -55,6 +66,7 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
   uint32_t* masks = reinterpret_cast<uint32_t*>(ps + kRB * (kKT + 1));  // [128][4]
   __shared__ int tree_bad;
   __shared__ int par_s[kMaxNodes];           // parent ids of the current tree
+  __shared__ int low_s[kWin ? kMaxNodes : 1];  // kWin: lowest prefix key each node sees through its window
 
   __shared__ int cu_buf[512];
   Problem pr = a.pr;
@@ -80,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
     const bool slot_ok = slot < a.slots;  // cannot fail for a consistent layout
     if (!slot_ok && tid == 0) set_status(a.status, kStatusInvalidArg);
 
-    if (has_tree) {
+    if (has_tree || kWin) {
       __syncthreads();
       if (tid == 0) tree_bad = 0;
       __syncthreads();
@@ -88,7 +100,13 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
       __syncthreads();
       for (int i = tid; i < s.m; i += kThreads) {
         uint32_t bits[4];
-        if (!ancestor_bits_shared(par_s, i, bits)) tree_bad = 1;
+        if constexpr (kWin) {
+          int depth;
+          if (!window_ancestors(par_s, i, pr.window, pr.sinks, s.len, bits, depth)) tree_bad = 1;
+          low_s[i] = window_low(pr, s, depth);
+        } else {
+          if (!ancestor_bits_shared(par_s, i, bits)) tree_bad = 1;
+        }
         masks[i * 4 + 0] = bits[0]; masks[i * 4 + 1] = bits[1];
         masks[i * 4 + 2] = bits[2]; masks[i * 4 + 3] = bits[3];
       }
@@ -129,10 +147,14 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
 
       for (int tile = tile0; tile < tile1; ++tile) {
         const bool is_tree = tile == 0;
-        const int nkeys = is_tree ? s.m : min(kKeyTile, s.P - (tile - 1) * kKeyTile);
+        const int key0 = kWin && !is_tree ? tile_key0(s, tile) : (tile - 1) * kKeyTile;
+        const int nkeys = is_tree ? s.m
+                          : kWin  ? tile_keys(pr, s, tile)
+                                  : min(kKeyTile, s.P - (tile - 1) * kKeyTile);
+        const int low = kWin && !is_tree ? low_s[my_node] : 0;  // my_node < m
         const T* kb = static_cast<const T*>(is_tree ? a.tree_k : a.k_cache);
         const T* vb = static_cast<const T*>(is_tree ? a.tree_v : a.v_cache);
-        const size_t first = is_tree ? (size_t)s.n0 : (size_t)s.p0 + (size_t)(tile - 1) * kKeyTile;
+        const size_t first = is_tree ? (size_t)s.n0 : (size_t)s.p0 + (size_t)key0;
         kb += first * kv_stride + (size_t)L.g * D;
         vb += first * kv_stride + (size_t)L.g * D;
         // The sub-tile's K / V are loaded into registers one sub-tile ahead: the loads
@@ -144,6 +166,13 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
           for (int i = 0; i < kN; ++i) {
             const int idx = (tid + i * kThreads) * 4, key = idx / D, dd = idx % D;
             const bool valid = k0 + key < nkeys;
+            if (kKv4 && !is_tree) {
+              const uint8_t* rec = static_cast<const uint8_t*>(a.k_cache) +
+                                   ((first + k0 + key) * pr.Hkv + L.g) * kv4_record_bytes(D);
+              kr[i] = valid ? load4_kv4<D>(rec, 0, dd) : make_float4(0.f, 0.f, 0.f, 0.f);
+              vr[i] = valid ? load4_kv4<D>(rec, 1, dd) : make_float4(0.f, 0.f, 0.f, 0.f);
+              continue;
+            }
             kr[i] = valid ? load4(kb + (size_t)(k0 + key) * kv_stride + dd) : make_float4(0.f, 0.f, 0.f, 0.f);
             vr[i] = valid ? load4(vb + (size_t)(k0 + key) * kv_stride + dd) : make_float4(0.f, 0.f, 0.f, 0.f);
           }
@@ -173,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
           for (int k = 0; k < 4; ++k) {
             const int key = k0 + kg * 4 + k;
             bool vis = row_ok && key < nkeys;
+            if (kWin && !is_tree) vis = vis && (key0 + key >= low || key0 + key < pr.sinks);
             if (is_tree && vis) vis = (masks[my_node * 4 + (key >> 5)] >> (key & 31)) & 1u;
             sc[k] = vis ? sc[k] * a.scale_log2 : -INFINITY;
             mx = fmaxf(mx, sc[k]);
@@ -205,7 +235,8 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
         }
       }
       if (row_ok && slot_ok) {
-        const float inv = 1.f / l_run;
+        // under a window a row may see no key of the segment: its partial is 0, log 0
+        const float inv = kWin && l_run == 0.f ? 0.f : 1.f / l_run;
         const int rr = my_row - row_begin, MT = mtile_rows(pr.G);
         const int pp = rr / MT * 128 + rr % MT;  // padded row (see o_part_offset)
         const int RGP = padded_group_rows(pr.RG, pr.G);
@@ -222,14 +253,14 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kWin, bool kKv4>
 cudaError_t launch_simt_typed(const PartialArgs& a, cudaStream_t s) {
   constexpr size_t smem = simt_smem_bytes<D>();
-  cudaError_t e = check_cuda(cudaFuncSetAttribute(partials_simt_kernel<T, D>,
+  cudaError_t e = check_cuda(cudaFuncSetAttribute(partials_simt_kernel<T, D, kWin, kKv4>,
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
                              "cudaFuncSetAttribute(partials_simt_kernel)");
   if (e != cudaSuccess) return e;
-  partials_simt_kernel<T, D><<<a.pr.U, kThreads, smem, s>>>(a);
+  partials_simt_kernel<T, D, kWin, kKv4><<<a.pr.U, kThreads, smem, s>>>(a);
   return check_cuda(cudaGetLastError(), "launch partials_simt_kernel");
 }
 
@@ -242,7 +273,20 @@ cudaError_t launch_partials_simt(const PartialArgs& a, int dtype, cudaStream_t s
     record_error("launch_partials_simt", 0, "float32 only");
     return cudaErrorInvalidValue;
   }
-  return a.pr.d == 64 ? launch_simt_typed<float, 64>(a, s) : launch_simt_typed<float, 128>(a, s);
+  if (a.pr.window > 0)
+    return a.pr.d == 64 ? launch_simt_typed<float, 64, true, false>(a, s) : launch_simt_typed<float, 128, true, false>(a, s);
+  return a.pr.d == 64 ? launch_simt_typed<float, 64, false, false>(a, s) : launch_simt_typed<float, 128, false, false>(a, s);
+}
+
+template <typename T>
+cudaError_t launch_kv4_typed(const PartialArgs& a, cudaStream_t s) {
+  if (a.pr.window > 0)
+    return a.pr.d == 64 ? launch_simt_typed<T, 64, true, true>(a, s) : launch_simt_typed<T, 128, true, true>(a, s);
+  return a.pr.d == 64 ? launch_simt_typed<T, 64, false, true>(a, s) : launch_simt_typed<T, 128, false, true>(a, s);
+}
+
+cudaError_t launch_partials_kv4(const PartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
+  return bf16 ? launch_kv4_typed<__nv_bfloat16>(a, s) : launch_kv4_typed<__half>(a, s);
 }
 
 }  // namespace tva

@@ -29,6 +29,8 @@
 // so each stream's softmax overlaps the other stream's MMAs, and the commit that
 // publishes S_w(j+1) also covers PV_w(j): a stream may rescale its O right after its
 // S is ready.
+// With a window (kWin; tva_common.cuh, SeqInfo) the walk covers only the key tiles that
+// some node sees; a tile that a window's lower edge crosses is masked per row.
 // TMEM columns: S/P buffers at 0 and 128, O accumulators at 256 and 384 (512 total).
 //
 // Every wait is bounded (2 s by default; the main-loop limit is a launch argument): on
@@ -86,7 +88,7 @@ __device__ __forceinline__ int q_buffer(int W, int sg) { return W == 1 ? (sg & 1
 // Earlier segments that used the same buffer.
 __device__ __forceinline__ int q_use(int W, int sg) { return W == 1 ? (sg >> 1) : sg; }
 
-template <int D, bool kBF16, bool kShare>
+template <int D, bool kBF16, bool kShare, bool kWin>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     partials_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
@@ -224,10 +226,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           const int tile = S.tile0 + k;
           const bool tree = tile == 0;
           const CUtensorMap* m = tree ? (is_v ? &tm_tv : &tm_tk) : (is_v ? &tm_v : &tm_k);
-          int z = tree ? L.s.n0 : L.s.p0 + (tile - 1) * kKeyTile;
+          int z = tree ? L.s.n0 : L.s.p0 + (kWin ? tile_key0(L.s, tile) : (tile - 1) * kKeyTile);
           // a tile starts inside its sequence's rows (loads past a tensor's end read zeros)
           if (!TVA_CHECK(z >= 0 && (tree ? z < pr.node_capacity && L.s.m > 0
-                                         : z < L.s.p0 + L.s.P && z < pr.kv_capacity), a.status))
+                                         : z < L.s.p0 + L.s.len && z < pr.kv_capacity), a.status))
             z = 0;
           mbar_expect_tx_elect(KV_FULL + 8 * stage, C::kTileBytes);
           for (int h = 0; h < C::kHalves; ++h)
@@ -394,6 +396,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const float sl2 = a.scale_log2;
     const int RG = pr.RG;
     int cnt = 0, of0 = 0, of1 = 0, sg = 0, trees = 0;
+    int ring = 0;  // kWin: ring index of the segment's first tile, as the producer counts
     bool ok = true;
     long long t = t_begin;
     Segment S;
@@ -407,15 +410,32 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       // row's ancestor bits.  They depend only on the parent ids, so they are found here,
       // while the first K tile is still on its way: one parent load per thread, shared
       // through shared memory, then the walk up from the row's node.
+      // Under a window every tile may need the row's depth, so every segment finds it.
       uint32_t anc[4] = {0u, 0u, 0u, 0u};
-      if (S.tile0 == 0 && (W == 2 || w == 0)) {
+      int low = 0;  // kWin: the lowest prefix key this row sees through its window
+      if (kWin || (S.tile0 == 0 && (W == 2 || w == 0))) {
         int* ps = par_s + w * 128;
+        // kWin: PAR_READY's even phases complete when the parents are in place, its odd
+        // ones when every row has read them.  Nothing else keeps a row of stream 1 from
+        // overwriting them for its next segment too early (W = 1: it waits for no O_FULL).
+        if (kWin && trees > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(PAR_READY + 8 * w, 1, abort_flag, wait_ns));
+          if (!ok) break;
+        }
         if (r < L.s.m) ps[r] = __ldg(a.parent + L.s.n0 + r);
         mbar_arrive(PAR_READY + 8 * w);
-        ok = __all_sync(0xffffffffu, mbar_wait(PAR_READY + 8 * w, trees & 1, abort_flag, wait_ns));
+        ok = __all_sync(0xffffffffu, mbar_wait(PAR_READY + 8 * w, kWin ? 0 : trees & 1, abort_flag, wait_ns));
         ++trees;
         if (!ok) break;
-        if (row_ok && !ancestor_bits_shared(ps, node, anc)) set_status(a.status, kStatusBadTree);
+        if constexpr (kWin) {
+          int depth = 0;
+          if (row_ok && !window_ancestors(ps, node, pr.window, pr.sinks, L.s.len, anc, depth))
+            set_status(a.status, kStatusBadTree);
+          low = window_low(pr, L.s, depth);
+          mbar_arrive(PAR_READY + 8 * w);
+        } else {
+          if (row_ok && !ancestor_bits_shared(ps, node, anc)) set_status(a.status, kStatusBadTree);
+        }
       }
       const int n_mine = (W == 2) ? n : (n - w + 1) / 2;
       float m_run = -INFINITY, l_run = 0.f;
@@ -427,8 +447,33 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (!ok) break;
         tc_fence_after();
         // keys of this tile: [0, lim) exist; the tree tile also needs the ancestor bit
-        const int lim = is_tree ? L.s.m : min(kKeyTile, L.s.P - (tile - 1) * kKeyTile);
-        if (is_tree || lim < kKeyTile) {
+        const int key0 = kWin && !is_tree ? tile_key0(L.s, tile) : 0;
+        const int lim = is_tree ? L.s.m
+                        : kWin  ? tile_keys(pr, L.s, tile)
+                                : min(kKeyTile, L.s.P - (tile - 1) * kKeyTile);
+        if constexpr (kWin) {
+          // Rows of V past the keys that exist, or that no node sees, may hold anything (an
+          // evicted or unwritten cache row: infinities, NaN), and a weight of zero would
+          // not hide them: they are zeroed in shared memory before this stream's P is
+          // published.  The stage cannot be refilled meanwhile: its release waits for the
+          // product that waits for P.  With W = 2 both streams write the same zeros.
+          if (lim < kKeyTile) {
+            const int vi = ring + (W == 2 ? 2 * k + 1 : (k <= n - 2 ? 2 + 2 * k : 2 * n - 1));
+            ok = __all_sync(0xffffffffu, mbar_wait(KV_FULL + 8 * (vi % C::kStages), (vi / C::kStages) & 1,
+                                                   abort_flag, wait_ns));
+            if (!ok) break;
+            if (r >= lim) {
+#pragma unroll
+              for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  *reinterpret_cast<uint4*>(smem + C::kQBytes + (vi % C::kStages) * C::kTileBytes + h * kHalfBytes +
+                                            r * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_async_shared();  // the MMA reads V through the asynchronous proxy
+          }
+        }
+        if (is_tree || lim < kKeyTile || (kWin && window_cuts(pr, L.s, key0, lim))) {
           // Rare tiles (the last, partial prefix tile; the tree tile): rewrite the logits
           // the row does not see to -inf in TMEM, 32 columns at a time, so the two
           // passes below carry no masking code.
@@ -439,6 +484,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             tmem_wait_ld32(sv);
             const int rem = lim - 32 * ck;
             uint32_t vw = rem >= 32 ? 0xffffffffu : (rem <= 0 ? 0u : (1u << rem) - 1u);
+            if constexpr (kWin) {
+              if (!is_tree) vw = window_bits(key0 + 32 * ck, rem, low, pr.sinks);
+            }
             if (is_tree) {
               const uint32_t aw = ck == 0 ? anc[0] : ck == 1 ? anc[1] : ck == 2 ? anc[2] : anc[3];
               vw &= row_ok ? aw : 0u;
@@ -549,7 +597,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (!ok) break;
         (w == 0 ? of0 : of1)++;
         tc_fence_after();
-        const float inv = 1.f / l_run;
+        // under a window a row may see no key of the segment: its partial is 0, log 0
+        const float inv = kWin && l_run == 0.f ? 0.f : 1.f / l_run;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 64) {
           // 64 columns of the row's O per TMEM round trip (one wait covers all loads in
@@ -601,7 +650,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const float a0 = (m_run == -INFINITY) ? 0.f : ex2(m_run - mm);
         const float a1 = (!has1 || m1 == -INFINITY) ? 0.f : ex2(m1 - mm);
         const float lt = a0 * l_run + a1 * l1;
-        const float inv = 1.f / lt;
+        const float inv = kWin && lt == 0.f ? 0.f : 1.f / lt;
         const float w0 = a0 * inv, w1 = a1 * inv;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -626,6 +675,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         tc_fence_before();
         mbar_arrive(O_FREE);
       }
+      ring += 2 * n;
       ++sg;
     }
   }
@@ -688,7 +738,7 @@ void tc_wait_settings(uint64_t* wait_ns, int* stall) {
 
 namespace {
 
-template <int D, bool kBF16, bool kShare>
+template <int D, bool kBF16, bool kShare, bool kWin>
 cudaError_t launch_tc_typed(const PartialArgs& a, int W, int npt, cudaStream_t s) {
   constexpr CUtensorMapDataType type = kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const Problem& pr = a.pr;
@@ -702,17 +752,17 @@ cudaError_t launch_tc_typed(const PartialArgs& a, int W, int npt, cudaStream_t s
       !make_map(&mtv, type, a.tree_v, D, pr.Hkv, pr.node_capacity, 1, kKeyTile))
     return cudaErrorInvalidValue;
   constexpr int smem = Cfg<D>::kSmemBytes;
-  cudaError_t e = check_cuda(cudaFuncSetAttribute(partials_tc_kernel<D, kBF16, kShare>,
+  cudaError_t e = check_cuda(cudaFuncSetAttribute(partials_tc_kernel<D, kBF16, kShare, kWin>,
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                              "cudaFuncSetAttribute(partials_tc_kernel)");
   if (e != cudaSuccess) return e;
   TcArgs ta{a, W, npt, 0, 0};
   tc_wait_settings(&ta.wait_ns, &ta.stall);
-  e = launch_pdl(partials_tc_kernel<D, kBF16, kShare>, dim3(pr.U), dim3(kThreadsTc), (size_t)smem, s, mq, mk, mv, mtk,
+  e = launch_pdl(partials_tc_kernel<D, kBF16, kShare, kWin>, dim3(pr.U), dim3(kThreadsTc), (size_t)smem, s, mq, mk, mv, mtk,
                  mtv, ta);
   if (e != cudaSuccess) {
     cudaFuncAttributes fa{};
-    cudaFuncGetAttributes(&fa, partials_tc_kernel<D, kBF16, kShare>);
+    cudaFuncGetAttributes(&fa, partials_tc_kernel<D, kBF16, kShare, kWin>);
     char what[160];
     snprintf(what, sizeof(what), "%s; kernel regs %d, max threads %d, smem %d+%d", cudaGetErrorString(e),
              fa.numRegs, fa.maxThreadsPerBlock, (int)fa.sharedSizeBytes, smem);
@@ -728,15 +778,19 @@ void set_tc_wait_limit(unsigned long long ns, int stall) {
   g_force_stall.store(stall != 0 ? 1 : 0, std::memory_order_relaxed);
 }
 
-template <bool kShare>
+template <bool kShare, bool kWin>
 cudaError_t launch_tc_mode(const PartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
   if (bf16)
-    return a.pr.d == 64 ? launch_tc_typed<64, true, kShare>(a, W, npt, s) : launch_tc_typed<128, true, kShare>(a, W, npt, s);
-  return a.pr.d == 64 ? launch_tc_typed<64, false, kShare>(a, W, npt, s) : launch_tc_typed<128, false, kShare>(a, W, npt, s);
+    return a.pr.d == 64 ? launch_tc_typed<64, true, kShare, kWin>(a, W, npt, s)
+                        : launch_tc_typed<128, true, kShare, kWin>(a, W, npt, s);
+  return a.pr.d == 64 ? launch_tc_typed<64, false, kShare, kWin>(a, W, npt, s)
+                      : launch_tc_typed<128, false, kShare, kWin>(a, W, npt, s);
 }
 
 cudaError_t launch_partials_tc(const PartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
-  return a.pr.share != 0 ? launch_tc_mode<true>(a, bf16, W, npt, s) : launch_tc_mode<false>(a, bf16, W, npt, s);
+  if (a.pr.window > 0)
+    return a.pr.share != 0 ? launch_tc_mode<true, true>(a, bf16, W, npt, s) : launch_tc_mode<false, true>(a, bf16, W, npt, s);
+  return a.pr.share != 0 ? launch_tc_mode<true, false>(a, bf16, W, npt, s) : launch_tc_mode<false, false>(a, bf16, W, npt, s);
 }
 
 }  // namespace tva

@@ -63,12 +63,22 @@ struct Problem {
   // range crosses into another row group (stream-K ranges do, and such a worker pays a
   // second segment - epilogue, Q copy, tree tile - in the middle of its stream).
   int align;
+  // 0: every node sees the whole prefix.  W >= 1: a node at position t (the prefix length
+  // plus its number of proper ancestors) sees the key at position s when t - s < W or
+  // s < sinks; the walk then covers only the prefix keys that some node sees (SeqInfo).
+  int window, sinks;
 };
 
 struct SeqInfo {
-  int p0, P;   // first k_cache row, prefix length
+  int p0, P;   // first k_cache row; keys that the walk covers (the prefix length without a window)
   int n0, m;   // first node row, tree size
   bool ok;     // false: bounds violated (sequence treated as empty)
+  // Windowed sequences: prefix length, sink tiles, first key of the window.  A root (position
+  // len) sees keys [0, sinks) and [len - W + 1, len) and every deeper node a subset of them.
+  // If those ranges leave a gap, the walk's tiles are `ns` tiles from key 0 (the last one
+  // may be partial), then tiles from key w0; the keys between are never read.  Otherwise
+  // ns = w0 = 0 and the tiles run over the whole prefix.
+  int len, ns, w0;
 };
 
 __device__ __forceinline__ void set_status(int32_t* st, int code) {
@@ -105,7 +115,58 @@ __device__ __forceinline__ SeqInfo seq_info(const Problem& pr, int b) {
   s.ok = s.p0 >= 0 && s.P >= 0 && s.P <= pr.max_prefix && s.p0 + s.P <= pr.kv_capacity &&
          s.n0 >= 0 && s.m >= 0 && s.m <= pr.max_nodes && s.n0 + s.m <= pr.node_capacity;
   if (!s.ok) { s.P = 0; s.m = 0; }
+  s.len = s.P;
+  s.ns = s.w0 = 0;
+  if (pr.window > 0) {
+    const int lo = s.P > pr.window - 1 ? s.P - (pr.window - 1) : 0;
+    const int sk = pr.sinks < s.P ? pr.sinks : s.P;
+    if (lo > sk) {
+      s.ns = (sk + kKeyTile - 1) / kKeyTile;
+      s.w0 = lo;
+      s.P = s.ns * kKeyTile + (s.len - lo);
+    }
+  }
   return s;
+}
+
+// Windowed walk: first key (relative to the sequence) of prefix tile `tile` >= 1, and how
+// many keys from there on some node sees (1 .. 128; the rest of the tile is never used).
+__device__ __forceinline__ int tile_key0(const SeqInfo& s, int tile) {
+  const int k = tile - 1;
+  return k < s.ns ? k * kKeyTile : s.w0 + (k - s.ns) * kKeyTile;
+}
+__device__ __forceinline__ int tile_keys(const Problem& pr, const SeqInfo& s, int tile) {
+  const int end = tile - 1 < s.ns ? (pr.sinks < s.len ? pr.sinks : s.len) : s.len;
+  const int n = end - tile_key0(s, tile);
+  return n < kKeyTile ? n : kKeyTile;
+}
+// The lowest prefix key that a node `depth` levels below the roots sees through the window
+// (it sees every key from there on, and the sinks).
+__device__ __forceinline__ int window_low(const Problem& pr, const SeqInfo& s, int depth) {
+  const int low = s.len + depth - (pr.window - 1);
+  return low > 0 ? low : 0;
+}
+// Whether some row may not see some of the tile's keys: they start below the deepest
+// possible node's window (depth <= m - 1) and are not all sinks.
+__device__ __forceinline__ bool window_cuts(const Problem& pr, const SeqInfo& s, int key0, int keys) {
+  return key0 < window_low(pr, s, s.m - 1) && key0 + keys > pr.sinks;
+}
+// Bits first .. 31 (all when first <= 0) and bits 0 .. count - 1 of a 32-key mask word.
+__device__ __forceinline__ uint32_t bits_from(int first) {
+  return first <= 0 ? 0xffffffffu : (first >= 32 ? 0u : 0xffffffffu << first);
+}
+__device__ __forceinline__ uint32_t bits_below(int count) { return ~bits_from(count); }
+// The keys of a 32-key chunk starting at key c0 that a row with window_low `low` sees, the
+// first `keys` (counted from c0) being real.
+__device__ __forceinline__ uint32_t window_bits(int c0, int keys, int low, int sinks) {
+  return bits_below(keys) & (bits_from(low - c0) | bits_below(sinks - c0));
+}
+// The longest walk of a sequence within the stated bound (sizes launches only).
+__host__ __device__ __forceinline__ long long walk_prefix_bound(const Problem& pr) {
+  if (pr.window <= 0) return pr.max_prefix;
+  const long long a = (long long)pr.max_prefix + kKeyTile - 1;
+  const long long b = ((long long)pr.sinks + kKeyTile - 1) / kKeyTile * kKeyTile + pr.window - 1;
+  return a < b ? a : b;
 }
 
 // Copies cu_prefix / cu_nodes into `buf` (2 * (B + 1) ints of shared memory) when they
@@ -398,6 +459,24 @@ __device__ __forceinline__ bool ancestor_bits_shared(const int* par, int i, uint
     if (p < 0) return true;
     bits[p >> 5] |= 1u << (p & 31);
     j = p;
+  }
+  return true;
+}
+
+// The same under a window: also the node's depth (its number of proper ancestors), and the
+// bits of only those ancestors at distance < window or at a position below `sinks` (the
+// node at depth e stands at position len + e).
+__device__ __forceinline__ bool window_ancestors(const int* par, int i, int window, int sinks, int len,
+                                                 uint32_t bits[4], int& depth) {
+  depth = 0;
+  if (!ancestor_bits_shared(par, i, bits)) return false;
+  for (int j = par[i]; j >= 0; j = par[j]) ++depth;
+  if (depth >= window) {  // some ancestors are further away than the window reaches
+    int j = i;
+    for (int dist = 0; dist <= depth; ++dist) {
+      if (dist >= window && len + depth - dist >= sinks) bits[j >> 5] &= ~(1u << (j & 31));
+      j = par[j];
+    }
   }
   return true;
 }

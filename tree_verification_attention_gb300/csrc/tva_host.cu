@@ -7,6 +7,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "kv4.cuh"
 #include "tva.h"
 #include "tva_internal.h"
 
@@ -84,7 +85,7 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // the single-sequence form.
 tva_status make_layout(int B, int Hq, int Hkv, int d, int dtype, int max_prefix, int max_nodes,
                        int kv_cap, int node_cap, const int32_t* cu_prefix, const int32_t* cu_nodes,
-                       int single_prefix, int single_nodes, Layout* L) {
+                       int single_prefix, int single_nodes, Layout* L, bool allow_pair = true) {
   tva_status st = check_shape(B, Hq, Hkv, d, dtype, max_prefix, max_nodes, kv_cap, node_cap);
   if (st != TVA_OK) return st;
   int sms = 0;
@@ -115,9 +116,10 @@ tva_status make_layout(int B, int Hq, int Hkv, int d, int dtype, int max_prefix,
   // workers: the fp32 kernel runs several CTAs per SM; the tensor-core kernel one CTA per
   // SM, the CTA-pair kernel (selected by tva_diag_use_cta_pair; two M-tiles per row group,
   // head_dim 128) one pair per two SMs
-  L->pair = g_use_cta_pair.load(std::memory_order_relaxed) != 0 && dtype != TVA_FP32 && W == 2 && d == 128;
+  L->pair = allow_pair && g_use_cta_pair.load(std::memory_order_relaxed) != 0 && dtype != TVA_FP32 && W == 2 && d == 128;
   pr.U = dtype == TVA_FP32 ? sms * tva::simt_workers_per_sm() : (L->pair ? sms / 2 : sms);
   pr.max_prefix = max_prefix; pr.max_nodes = max_nodes;
+  pr.window = pr.sinks = 0;
   pr.kv_capacity = kv_cap; pr.node_capacity = node_cap;
   const int mp_max = (max_nodes + W * npt - 1) / (W * npt);  // row groups per KV head
   const long long groups = (long long)B * Hkv * mp_max;
@@ -147,10 +149,9 @@ float scale_log2(float softmax_scale, int d) {
   return s * 1.44269504088896340736f;
 }
 
-tva_status run_partials(const Layout& L, int dtype, float softmax_scale, const void* q,
-                        const void* k_cache, const void* v_cache, const void* tree_k,
-                        const void* tree_v, const int32_t* parent, void* workspace,
-                        int32_t* dev_status, cudaStream_t s) {
+tva::PartialArgs partial_args(const Layout& L, float softmax_scale, const void* q, const void* k_cache,
+                              const void* v_cache, const void* tree_k, const void* tree_v, const int32_t* parent,
+                              void* workspace, int32_t* dev_status) {
   tva::PartialArgs a;
   a.pr = L.pr;
   a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.tree_k = tree_k; a.tree_v = tree_v;
@@ -160,6 +161,15 @@ tva_status run_partials(const Layout& L, int dtype, float softmax_scale, const v
   a.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.o_bytes);
   a.slots = L.slots;
   a.status = dev_status;
+  return a;
+}
+
+tva_status run_partials(const Layout& L, int dtype, float softmax_scale, const void* q,
+                        const void* k_cache, const void* v_cache, const void* tree_k,
+                        const void* tree_v, const int32_t* parent, void* workspace,
+                        int32_t* dev_status, cudaStream_t s) {
+  const tva::PartialArgs a =
+      partial_args(L, softmax_scale, q, k_cache, v_cache, tree_k, tree_v, parent, workspace, dev_status);
   const cudaError_t e = dtype == TVA_FP32 ? tva::launch_partials_simt(a, dtype, s)
                         : L.pair           ? tva::launch_partials_pair(a, dtype == TVA_BF16, L.npt, s)
                                            : tva::launch_partials_tc(a, dtype == TVA_BF16, L.W, L.npt, s);
@@ -206,6 +216,50 @@ tva_status check_io_ptrs(const void* q, const void* k_cache, const void* v_cache
 tva_status check_workspace(const Layout& L, const void* ws, size_t bytes) {
   if (ws == nullptr || bytes < L.total) return TVA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return TVA_ERR_WORKSPACE;
+  return TVA_OK;
+}
+
+// The checks and the layout that the windowed and the 4-bit-cache forms share; p's window
+// is set in the layout's problem (0: the whole prefix).
+tva_status check_varlen_window(const tva_params* p, int window, int sinks, const void* q, const void* k_cache,
+                               const void* v_cache, const void* tree_k, const void* tree_v, const int32_t* parent,
+                               const void* out, const float* lse, const void* workspace, size_t workspace_bytes,
+                               const int32_t* dev_status, Layout* L) {
+  if (out == nullptr || lse == nullptr || !aligned16(out)) return TVA_ERR_INVALID_ARG;
+  if (p == nullptr || p->cu_prefix == nullptr || p->cu_nodes == nullptr || dev_status == nullptr)
+    return TVA_ERR_INVALID_ARG;
+  if (window < 0 || sinks < 0) return TVA_ERR_INVALID_ARG;
+  tva_status st = check_shape(p->batch, p->num_q_heads, p->num_kv_heads, p->head_dim, (int)p->dtype,
+                              p->max_prefix_len, p->max_nodes, p->kv_capacity, p->node_capacity);
+  if (st != TVA_OK) return st;
+  st = check_io_ptrs(q, k_cache, v_cache, tree_k, tree_v, parent, p->kv_capacity);
+  if (st != TVA_OK) return st;
+  st = make_layout(p->batch, p->num_q_heads, p->num_kv_heads, p->head_dim, (int)p->dtype, p->max_prefix_len,
+                   p->max_nodes, p->kv_capacity, p->node_capacity, p->cu_prefix, p->cu_nodes, 0, 0, L, false);
+  if (st != TVA_OK) return st;
+  L->pr.window = window;
+  L->pr.sinks = sinks;
+  return check_workspace(*L, workspace, workspace_bytes);
+}
+
+bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(x), b0 = reinterpret_cast<uintptr_t>(y);
+  return nx > 0 && ny > 0 && a0 < b0 + ny && b0 < a0 + nx;
+}
+
+// The checks that append_kv4 and read_kv4 share: shapes, pointers, and that the rows do
+// not overlap the cache (neither side has a defined order).
+tva_status check_kv4_rows(int num_rows, int Hkv, int d, int dtype, long long kv_capacity, const void* k, const void* v,
+                          const void* cache, const int32_t* dev_status) {
+  if (num_rows < 0 || Hkv < 1 || kv_capacity < 0 || kv_capacity > (1LL << 31) - 1 || !dev_status)
+    return TVA_ERR_INVALID_ARG;
+  if ((num_rows > 0 && (!k || !v)) || (kv_capacity > 0 && !cache)) return TVA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return TVA_ERR_UNSUPPORTED;
+  if (dtype != TVA_BF16 && dtype != TVA_FP32 && dtype != TVA_FP16) return TVA_ERR_UNSUPPORTED;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(cache)) return TVA_ERR_INVALID_ARG;
+  const size_t rows = (size_t)num_rows * Hkv * d * (dtype == TVA_FP32 ? 4 : 2);
+  const size_t held = (size_t)kv_capacity * Hkv * tva::kv4_record_bytes(d);
+  if (overlap(k, rows, cache, held) || overlap(v, rows, cache, held)) return TVA_ERR_INVALID_ARG;
   return TVA_OK;
 }
 
@@ -436,6 +490,86 @@ tva_status commit_accepted_kv(int batch, int num_kv_heads, int head_dim, tva_dty
   a.status = dev_status;
   return tva::launch_commit(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TVA_OK
                                                                                             : TVA_ERR_CUDA;
+}
+
+tva_status tree_verify_attn_window_varlen(const tva_params* p, int window, int sinks, const void* q,
+                                          const void* k_cache, const void* v_cache, const void* tree_k,
+                                          const void* tree_v, const int32_t* parent, void* out, float* lse,
+                                          void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                          void* stream) {
+  if (window < 1) return TVA_ERR_INVALID_ARG;
+  Layout L;
+  const tva_status st = check_varlen_window(p, window, sinks, q, k_cache, v_cache, tree_k, tree_v, parent, out, lse,
+                                            workspace, workspace_bytes, dev_status, &L);
+  if (st != TVA_OK) return st;
+  return run_attention(L, (int)p->dtype, p->softmax_scale, q, k_cache, v_cache, tree_k, tree_v, parent, workspace,
+                       out, lse, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+tva_status tree_verify_attn_kv4_varlen(const tva_params* p, int window, int sinks, const void* q,
+                                       const void* kv4_cache, const void* tree_k, const void* tree_v,
+                                       const int32_t* parent, void* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  if (p != nullptr && p->dtype == TVA_FP32) return TVA_ERR_UNSUPPORTED;
+  Layout L;
+  const tva_status st = check_varlen_window(p, window, sinks, q, kv4_cache, kv4_cache, tree_k, tree_v, parent, out,
+                                            lse, workspace, workspace_bytes, dev_status, &L);
+  if (st != TVA_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const tva::PartialArgs a = partial_args(L, p->softmax_scale, q, kv4_cache, kv4_cache, tree_k, tree_v, parent,
+                                          workspace, dev_status);
+  if (tva::launch_partials_kv4(a, p->dtype == TVA_BF16, L.W, L.npt, s) != cudaSuccess) return TVA_ERR_CUDA;
+  return run_combine(L, (int)p->dtype, workspace, out, lse, dev_status, s);
+}
+
+size_t tva_kv4_record_bytes(int head_dim) {
+  return head_dim == 64 || head_dim == 128 ? (size_t)tva::kv4_record_bytes(head_dim) : 0;
+}
+
+tva_status append_kv4(int num_rows, int num_kv_heads, int head_dim, tva_dtype dtype, long long kv_capacity,
+                      const void* k, const void* v, const int32_t* slot, void* kv4_cache, int32_t* dev_status,
+                      void* stream) {
+  const tva_status st = check_kv4_rows(num_rows, num_kv_heads, head_dim, (int)dtype, kv_capacity, k, v, kv4_cache,
+                                       dev_status);
+  if (st != TVA_OK) return st;
+  if (num_rows == 0) return TVA_OK;
+  if (slot == nullptr) return TVA_ERR_INVALID_ARG;
+  const tva::Kv4RowArgs a{num_rows, num_kv_heads, head_dim, kv_capacity, slot, k, v,
+                          static_cast<uint8_t*>(kv4_cache), dev_status};
+  return tva::launch_append_kv4(a, (int)dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TVA_OK
+                                                                                                 : TVA_ERR_CUDA;
+}
+
+tva_status read_kv4(int num_rows, int num_kv_heads, int head_dim, tva_dtype dtype, long long kv_capacity,
+                    const void* kv4_cache, const int32_t* slot, void* k, void* v, int32_t* dev_status, void* stream) {
+  const tva_status st = check_kv4_rows(num_rows, num_kv_heads, head_dim, (int)dtype, kv_capacity, k, v, kv4_cache,
+                                       dev_status);
+  if (st != TVA_OK) return st;
+  if (num_rows == 0) return TVA_OK;
+  const size_t rows = (size_t)num_rows * num_kv_heads * head_dim * (dtype == TVA_FP32 ? 4 : 2);
+  if (overlap(k, rows, v, rows)) return TVA_ERR_INVALID_ARG;
+  const tva::Kv4RowArgs a{num_rows, num_kv_heads, head_dim, kv_capacity, slot, k, v,
+                          static_cast<uint8_t*>(const_cast<void*>(kv4_cache)), dev_status};
+  return tva::launch_read_kv4(a, (int)dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TVA_OK : TVA_ERR_CUDA;
+}
+
+tva_status commit_accepted_kv4(int batch, int num_kv_heads, int head_dim, tva_dtype dtype, int node_capacity,
+                               int max_nodes, long long kv_capacity, const int32_t* cu_nodes,
+                               const int32_t* accept_len, const int32_t* accept_path, const void* tree_k,
+                               const void* tree_v, const int32_t* dst_row, void* kv4_cache, int32_t* dev_status,
+                               void* stream) {
+  if (batch < 1 || node_capacity < 0 || max_nodes < 1 || max_nodes > tva::kMaxNodes || !cu_nodes || !accept_len ||
+      !accept_path || !dst_row || !tree_k || !tree_v)
+    return TVA_ERR_INVALID_ARG;
+  const tva_status st = check_kv4_rows(node_capacity, num_kv_heads, head_dim, (int)dtype, kv_capacity, tree_k, tree_v,
+                                       kv4_cache, dev_status);
+  if (st != TVA_OK) return st;
+  tva::CommitArgs a{};
+  a.B = batch; a.node_capacity = node_capacity; a.max_nodes = max_nodes; a.kv_capacity = kv_capacity;
+  a.cu_nodes = cu_nodes; a.accept_len = accept_len; a.accept_path = accept_path;
+  a.tree_k = tree_k; a.tree_v = tree_v; a.dst_row = dst_row; a.k_cache = kv4_cache; a.status = dev_status;
+  return tva::launch_commit_kv4(a, num_kv_heads, head_dim, (int)dtype, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess ? TVA_OK : TVA_ERR_CUDA;
 }
 
 tva_status verify_chain_sampling(int batch, int vocab, int max_draft, long long p_rows, long long q_rows,

@@ -66,6 +66,17 @@ struct CommitArgs {
   int32_t* status;
 };
 
+// Rows into (append) or out of (read) the 4-bit cache.
+struct Kv4RowArgs {
+  int rows, Hkv, d;
+  long long kv_capacity;
+  const int32_t* slot;      // [rows] cache row of each; read: null for rows 0, 1, ...
+  const void* k;            // [rows, Hkv, d] (read: written)
+  const void* v;
+  uint8_t* cache;           // [kv_capacity, Hkv, record]
+  int32_t* status;
+};
+
 struct SamplingArgs {
   int B, V, max_draft;
   long long p_rows, q_rows;
@@ -124,6 +135,8 @@ int simt_workers_per_sm();
 cudaError_t launch_partials_simt(const PartialArgs& a, int dtype, cudaStream_t s);
 // bf16 (bf16 = true) or fp16, head_dim 64 or 128; W M-tiles of npt nodes per row group
 cudaError_t launch_partials_tc(const PartialArgs& a, bool bf16, int W, int npt, cudaStream_t s);
+// The same over a 4-bit prefix cache (a.k_cache: the records; a.v_cache unused).
+cudaError_t launch_partials_kv4(const PartialArgs& a, bool bf16, int W, int npt, cudaStream_t s);
 // Row groups of two M-tiles at head_dim 128 on CTA pairs (a.pr.U = pairs); bf16 or fp16.
 cudaError_t launch_partials_pair(const PartialArgs& a, bool bf16, int npt, cudaStream_t s);
 // 3-D 16-bit tensor map over [rows][heads][d] with a box of {64, box_heads, box_rows}
@@ -138,6 +151,10 @@ void set_tc_wait_limit(unsigned long long ns, int stall);
 cudaError_t launch_combine(const CombineArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s);
 cudaError_t launch_commit(const CommitArgs& a, cudaStream_t s);
+cudaError_t launch_append_kv4(const Kv4RowArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_read_kv4(const Kv4RowArgs& a, int dtype, cudaStream_t s);
+// CommitArgs with k_cache the 4-bit cache (v_cache unused).
+cudaError_t launch_commit_kv4(const CommitArgs& a, int Hkv, int d, int dtype, cudaStream_t s);
 cudaError_t launch_sampling(const SamplingArgs& a, cudaStream_t s);
 cudaError_t launch_gdn(const GdnArgs& a, cudaStream_t s);
 
