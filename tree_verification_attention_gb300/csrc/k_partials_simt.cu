@@ -13,7 +13,6 @@
 //
 // This path carries the float32 dtype (head_dim 64 or 128).  bfloat16 inputs go to
 // the tensor-core kernel.
-#include "kv4.cuh"
 #include "tva_internal.h"
 
 namespace tva {
@@ -28,7 +27,6 @@ template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
 template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) {
   return __bfloat162float(v);
 }
-template <> __device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
 
 // Four consecutive elements of a row (16-byte aligned for float: rows are D floats and
 // the base pointers are 16-byte aligned).
@@ -41,22 +39,13 @@ __device__ __forceinline__ float4 load4(const T* p) {
   }
 }
 
-// Four consecutive values (dd a multiple of 4) of the K (half 0) or V part of a 4-bit record.
-template <int D>
-__device__ __forceinline__ float4 load4_kv4(const uint8_t* rec, int half, int dd) {
-  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(rec + half * (D / 2)) + dd / 8) >> (dd & 4 ? 8 : 0);
-  const float s = kv4_scale_value(__ldg(rec + D + half * (D / 16) + dd / 16));
-  auto value = [&](int e) { return (float)((int)((w >> kv4_shift(e)) & 15u) - 8) * s; };
-  return make_float4(value(0), value(1), value(2), value(3));
-}
-
 template <int D>
 constexpr size_t simt_smem_bytes() {
   return sizeof(float) * (kRB * (D + 1) + kKT * (D + 1) + kKT * D + kRB * (kKT + 1)) +
          sizeof(uint32_t) * kMaxNodes * 4;
 }
 
-template <typename T, int D, bool kWin, bool kKv4>
+template <typename T, int D, bool kWin>
 __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs a) {
   extern __shared__ float smem[];
   float* qs = smem;                          // [kRB][D+1]
@@ -166,13 +155,6 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
           for (int i = 0; i < kN; ++i) {
             const int idx = (tid + i * kThreads) * 4, key = idx / D, dd = idx % D;
             const bool valid = k0 + key < nkeys;
-            if (kKv4 && !is_tree) {
-              const uint8_t* rec = static_cast<const uint8_t*>(a.k_cache) +
-                                   ((first + k0 + key) * pr.Hkv + L.g) * kv4_record_bytes(D);
-              kr[i] = valid ? load4_kv4<D>(rec, 0, dd) : make_float4(0.f, 0.f, 0.f, 0.f);
-              vr[i] = valid ? load4_kv4<D>(rec, 1, dd) : make_float4(0.f, 0.f, 0.f, 0.f);
-              continue;
-            }
             kr[i] = valid ? load4(kb + (size_t)(k0 + key) * kv_stride + dd) : make_float4(0.f, 0.f, 0.f, 0.f);
             vr[i] = valid ? load4(vb + (size_t)(k0 + key) * kv_stride + dd) : make_float4(0.f, 0.f, 0.f, 0.f);
           }
@@ -253,14 +235,14 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
   }
 }
 
-template <typename T, int D, bool kWin, bool kKv4>
+template <typename T, int D, bool kWin>
 cudaError_t launch_simt_typed(const PartialArgs& a, cudaStream_t s) {
   constexpr size_t smem = simt_smem_bytes<D>();
-  cudaError_t e = check_cuda(cudaFuncSetAttribute(partials_simt_kernel<T, D, kWin, kKv4>,
+  cudaError_t e = check_cuda(cudaFuncSetAttribute(partials_simt_kernel<T, D, kWin>,
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
                              "cudaFuncSetAttribute(partials_simt_kernel)");
   if (e != cudaSuccess) return e;
-  partials_simt_kernel<T, D, kWin, kKv4><<<a.pr.U, kThreads, smem, s>>>(a);
+  partials_simt_kernel<T, D, kWin><<<a.pr.U, kThreads, smem, s>>>(a);
   return check_cuda(cudaGetLastError(), "launch partials_simt_kernel");
 }
 
@@ -274,19 +256,8 @@ cudaError_t launch_partials_simt(const PartialArgs& a, int dtype, cudaStream_t s
     return cudaErrorInvalidValue;
   }
   if (a.pr.window > 0)
-    return a.pr.d == 64 ? launch_simt_typed<float, 64, true, false>(a, s) : launch_simt_typed<float, 128, true, false>(a, s);
-  return a.pr.d == 64 ? launch_simt_typed<float, 64, false, false>(a, s) : launch_simt_typed<float, 128, false, false>(a, s);
-}
-
-template <typename T>
-cudaError_t launch_kv4_typed(const PartialArgs& a, cudaStream_t s) {
-  if (a.pr.window > 0)
-    return a.pr.d == 64 ? launch_simt_typed<T, 64, true, true>(a, s) : launch_simt_typed<T, 128, true, true>(a, s);
-  return a.pr.d == 64 ? launch_simt_typed<T, 64, false, true>(a, s) : launch_simt_typed<T, 128, false, true>(a, s);
-}
-
-cudaError_t launch_partials_kv4(const PartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
-  return bf16 ? launch_kv4_typed<__nv_bfloat16>(a, s) : launch_kv4_typed<__half>(a, s);
+    return a.pr.d == 64 ? launch_simt_typed<float, 64, true>(a, s) : launch_simt_typed<float, 128, true>(a, s);
+  return a.pr.d == 64 ? launch_simt_typed<float, 64, false>(a, s) : launch_simt_typed<float, 128, false>(a, s);
 }
 
 }  // namespace tva

@@ -730,6 +730,26 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, int d,
   return true;
 }
 
+bool make_record_map(CUtensorMap* m, const void* base, int record, int heads, long long rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) {
+    record_error("cudaGetDriverEntryPointByVersion(cuTensorMapEncodeTiled)", 0, "entry point not found");
+    return false;
+  }
+  cuuint64_t dims[3] = {(cuuint64_t)record, (cuuint64_t)heads, (cuuint64_t)(rows > 0 ? rows : 1)};
+  cuuint64_t strides[2] = {(cuuint64_t)record, (cuuint64_t)heads * record};
+  cuuint32_t box[3] = {(cuuint32_t)record, 1, kKeyTile};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    record_error("cuTensorMapEncodeTiled", (int)r, "tensor map rejected");
+    return false;
+  }
+  return true;
+}
+
 void tc_wait_settings(uint64_t* wait_ns, int* stall) {
   const unsigned long long lim = g_wait_limit_ns.load(std::memory_order_relaxed);
   *wait_ns = lim > 0 ? (uint64_t)lim : kDrainNs;

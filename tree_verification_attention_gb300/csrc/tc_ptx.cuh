@@ -24,6 +24,13 @@ __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Registers per thread of a warpgroup (all of its four warps execute it): give some back to
+// the block, or take some of what others have given back (waits until they are there).
+template <int kRegs>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+template <int kRegs>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+
 // Named CTA barrier `id` (1..15) over `count` threads (a multiple of 32, whole warps):
 // arrive without waiting, or arrive and wait for the others.
 __device__ __forceinline__ void bar_arrive(int id, int count) {

@@ -143,6 +143,8 @@ cudaError_t launch_partials_pair(const PartialArgs& a, bool bf16, int npt, cudaS
 // (128-byte swizzle); false (and tva_last_error) if the driver rejects it.
 bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, int d, int heads, long long rows,
               int box_heads, int box_rows);
+// 3-D byte map over [rows][heads][record] with a box of {record, 1, 128}, not swizzled.
+bool make_record_map(CUtensorMap* m, const void* base, int record, int heads, long long rows);
 // Main-loop wait limit and test stall for the tensor-core partials kernels.
 void tc_wait_settings(uint64_t* wait_ns, int* stall);
 // Main-loop wait limit of the tensor-core partials kernel for later launches (0: the
