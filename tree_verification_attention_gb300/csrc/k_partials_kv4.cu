@@ -7,16 +7,19 @@
 // type - exactly: a value has at most 7 significant bits - on their way to the tensor
 // cores: DRAM and L2 carry 144 bytes a row and head (d = 128) instead of 512.
 //
-// How (one CTA per SM, 512 threads in four warpgroups with registers of their own):
-//   warp 12 (producer): TMA of Q, of the tree tile's K / V (16-bit, into the ring) and of
+// How (one CTA per SM, 640 threads in five warpgroups with registers of their own):
+//   warp 16 (producer): TMA of Q, of the tree tile's K / V (16-bit, into the ring) and of
 //           the raw 128-record tiles (a box of records, 18 KB at d = 128) into a ring.
-//   warps 8-11 (widening): thread r widens record r of a tile: 16 bytes of codes become 64
-//           bytes of a K or V tile in the 128-byte-swizzled ring that the MMAs read.
-//           A shift and one and-or put two codes n into the mantissas of 128 + n (fp16:
-//           16 + n), one fused multiply-add takes the offset off and applies the scale:
-//           1.4 instructions a value.  Rows past a tile's last key are written as zeros,
-//           so nothing a record of another sequence holds can reach a product.
-//   warp 13 (MMA), warps 0-7 (softmax): as in k_partials_tc.cu, two streams of 4 warps.
+//   warps 8-11 and 12-15 (widening K, widening V): thread r widens record r of a tile: 16
+//           bytes of codes become 64 bytes of a K or V tile in the 128-byte-swizzled ring
+//           that the MMAs read.  A shift and one and-or put two codes n into the mantissas
+//           of 128 + n (fp16: 16 + n), one fused multiply-add takes the offset off and
+//           applies the scale.  Rows past a tile's last key are written as zeros, so nothing
+//           that a record of another sequence holds can reach a product.  K and V have a
+//           warpgroup each because a tile's widening is a chain of about 1300 clocks however
+//           few rows the tree has: one warpgroup for both took 3000 a tile, more than
+//           everything else when the tree has one M-tile.
+//   warp 17 (MMA), warps 0-7 (softmax): as in k_partials_tc.cu, two streams of 4 warps.
 //           A warp whose 32 rows are all padding leaves its logits alone.
 // TMEM columns: S/P buffers at 0 and 128, O accumulators at 256 and 384 (512 total).
 // A window (pr.window > 0) is handled as there too, at run time: it only adds masks to the
@@ -38,16 +41,17 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreadsKv4 = 512;
-constexpr int kWidenWarp = 8;     // .. 11
-constexpr int kProducerWarp = 12;
-constexpr int kMmaWarp = 13;
+
+constexpr int kWidenWarp = 8;     // 8-11: K, 12-15: V
+constexpr int kProducerWarp = 16;
+constexpr int kMmaWarp = kProducerWarp + 1;
+constexpr int kThreadsKv4 = 640;
 constexpr int kHalfBytes = 128 * 128;  // 128 rows of 64 16-bit values (one swizzle span)
-// Registers per thread of the four warpgroups (two of softmax, widening, the rest).  They
-// share what the block is launched with, 512 x 128 (checked before the first launch): a
-// split above that would wait forever.
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 184, kWidenRegs = 72, kOtherRegs = 72;
-static_assert(2 * kSoftmaxRegs + kWidenRegs + kOtherRegs <= 4 * kLaunchRegs, "register split");
+// Registers per thread of the five warpgroups (two of softmax, K, V, the rest).  They share
+// what the block is launched with, 640 x 96 (checked before the first launch): a split above
+// that would wait forever.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 152, kWidenRegs = 56, kOtherRegs = 64;
+static_assert(2 * kSoftmaxRegs + 2 * kWidenRegs + kOtherRegs <= 5 * kLaunchRegs, "register split");
 
 template <int D>
 struct Cfg {
@@ -104,17 +108,18 @@ __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
   return r;
 }
 
-// A block's scale as a pair, and the pair that takes the codes' offset off.  Every step is
-// exact: the scale has 4 significant bits; 136 = 8 x 17 times it at most 9 - 1 = 8 (17 x 15
-// = 255), 24 = 8 x 3 times it 6.
+// Byte i of `scales` - a block's scale - as a pair, and the pair that takes the codes'
+// offset off.  Every step is exact: the scale has 4 significant bits; 136 = 8 x 17 times it
+// at most 8 (17 x 15 = 255), 24 = 8 x 3 times it 6.
 template <bool kBF16>
-__device__ __forceinline__ void widen_scale(uint32_t byte, uint32_t& s, uint32_t& c) {
+__device__ __forceinline__ void widen_scale(uint32_t scales, int i, uint32_t& s, uint32_t& c) {
+  const uint32_t b = __byte_perm(scales, 0u, 0x4040u + 0x0101u * i);  // the byte in both halves
   if constexpr (kBF16) {
-    s = bf2_mul(byte * 0x00100010u, 0x77807780u);  // exponent bias 15 -> 127: times 2^112
-    c = bf2_mul(s, 0xc308c308u);                   // -136
+    s = bf2_mul(b << 4, 0x77807780u);  // exponent bias 15 -> 127: times 2^112
+    c = bf2_mul(s, 0xc308c308u);       // -136
   } else {
-    s = byte * 0x00800080u;
-    c = h2_mul(s, 0xce00ce00u);                    // -24
+    s = b << 7;
+    c = h2_mul(s, 0xce00ce00u);        // -24
   }
 }
 
@@ -134,6 +139,38 @@ __device__ __forceinline__ uint4 widen8(uint32_t w, uint32_t s, uint32_t c) {
     o.w = h2_fma(((w >> 6) & 0x03c003c0u) | 0x4c004c00u, s, c);
   }
   return o;
+}
+
+// One row's K or V values (codes at `codes`, scales at `scales`, both shared
+// addresses) into a swizzled tile, from 16-byte chunk `chunk0` of the row on; the row starts
+// at `row`, with the swizzle's row term already in it.  All loads come first.
+template <int D, bool kBF16>
+__device__ __forceinline__ void widen_row(uint32_t codes, uint32_t scales, uint32_t row) {
+  constexpr int kVals = D;
+  uint4 code[kVals / 32];
+  uint32_t sc = 0u, sc1 = 0u, s[kVals / 16], c[kVals / 16];
+#pragma unroll
+  for (int q = 0; q < kVals / 32; ++q) code[q] = ld_shared_v4(codes + 16 * q);
+  if constexpr (kVals == 32) {
+    sc = ld_shared_u16(scales);
+  } else {
+    sc = ld_shared(scales);
+    if constexpr (kVals == 128) sc1 = ld_shared(scales + 4);
+  }
+#pragma unroll
+  for (int b = 0; b < kVals / 16; ++b) widen_scale<kBF16>(b < 4 ? sc : sc1, b & 3, s[b], c[b]);
+#pragma unroll
+  for (int i = 0; i < (kVals < 64 ? kVals / 8 : 8); ++i) {  // chunk i of a span (of both when a thread has both)
+    const uint32_t at = row ^ (uint32_t)(i << 4);
+    const uint4 v = code[i >> 2];
+    const uint32_t w = (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+    st_shared_v4_at<0>(at, widen8<kBF16>(w, s[i >> 1], c[i >> 1]));
+    if constexpr (kVals == 128) {
+      const uint4 v1 = code[2 + (i >> 2)];
+      const uint32_t w1 = (i & 3) == 0 ? v1.x : (i & 3) == 1 ? v1.y : (i & 3) == 2 ? v1.z : v1.w;
+      st_shared_v4_at<kHalfBytes>(at, widen8<kBF16>(w1, s[4 + (i >> 1)], c[4 + (i >> 1)]));
+    }
+  }
 }
 
 // The 128 logits of this thread's row.
@@ -210,7 +247,7 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
     }
     for (int s = 0; s < C::kRaws; ++s) {
       mbar_init(RAW_FULL + 8 * s, 1);
-      mbar_init(RAW_EMPTY + 8 * s, 4);
+      mbar_init(RAW_EMPTY + 8 * s, 8);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(Q_FULL + 8 * w, 1);
@@ -456,73 +493,54 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
   } else if (warp >= kWidenWarp) {
     // ------------------------------------------------------------------ widening
     reg_dec<kWidenRegs>();
+    const bool is_v = warp >= kWidenWarp + 4;
     const int r = threadIdx.x & 127;  // the tile's row (key) of this thread
-    int ring = 0, raw = 0, trees = 0;
+    const uint32_t row_s = kv_s + r * 128 + ((r & 7) << 4);  // 16-byte chunk c of a span is at c ^ (row mod 8)
+    const uint32_t codes = raw_s + r * kv4_record_bytes(D) + (is_v ? D / 2 : 0);
+    const uint32_t scales = raw_s + r * kv4_record_bytes(D) + D + (is_v ? D / 16 : 0);
+    const uint32_t tree_bar = is_v ? 8 : 0;
+    uint32_t raw = 0, raw_ph = 0;
+    int ring = 0, trees = 0;
     bool ok = true;
     long long t = t_begin;
     Segment S;
     while (ok && next_segment(pr, u, t, t_end, S, kShare)) {
       const int n = S.n;
-      const bool tree = S.tile0 == 0;
-      // K (or V) of the segment's tile k into its ring stage
-      auto fill = [&](int k, bool is_v) -> bool {
+#pragma unroll 1
+      for (int k = 0; k < n; ++k) {
         const int idx = ring + (is_v ? ring_v(W, k, n) : ring_k(W, k));
-        const int stage = idx % C::kStages, use = idx / C::kStages;
-        uint8_t* dst = smem + C::kQBytes + stage * C::kTileBytes + r * 128;
+        const uint32_t stage = (uint32_t)idx % C::kStages, use = (uint32_t)idx / C::kStages;
         const int tile = S.tile0 + k;
+        int lim;  // rows from here on are written as zeros
         if (tile == 0) {
           // fetched by the producer; rows past the tree are another sequence's, or nothing's
-          if (!warp_wait(TREE_FULL + (is_v ? 8 : 0), trees & 1, abort_flag, wait_ns)) return false;
-          mbar_arrive_elect(TREE_EMPTY + (is_v ? 8 : 0));
-          if (r >= S.L.s.m) {
-#pragma unroll
-            for (int h = 0; h < C::kHalves; ++h)
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                *reinterpret_cast<uint4*>(dst + h * kHalfBytes + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
+          if (!(ok = warp_wait(TREE_FULL + tree_bar, trees & 1, abort_flag, wait_ns))) break;
+          mbar_arrive_elect(TREE_EMPTY + tree_bar);
+          lim = S.L.s.m;
         } else {
-          const int ri = raw + k - (tree ? 1 : 0);
-          if (use > 0 && !warp_wait(KV_EMPTY + 8 * stage, (use - 1) & 1, abort_flag, wait_ns)) return false;
-          if (!warp_wait(RAW_FULL + 8 * (ri % C::kRaws), (ri / C::kRaws) & 1, abort_flag, wait_ns)) return false;
-          const uint8_t* rec = smem + C::kRawOff + (ri % C::kRaws) * C::kRawBytes + r * kv4_record_bytes(D);
-          const bool real = r < tile_keys(pr, S.L.s, tile);
-          const uint8_t* scales = rec + D + (is_v ? D / 16 : 0);
+          // a wait for the phase before a fresh barrier's first returns at once
+          if (!(ok = warp_wait(KV_EMPTY + 8 * stage, (use & 1u) ^ 1u, abort_flag, wait_ns))) break;
+          if (!(ok = warp_wait(RAW_FULL + 8 * raw, raw_ph, abort_flag, wait_ns))) break;
+          lim = tile_keys(pr, S.L.s, tile);
+          if (r < lim)
+            widen_row<D, kBF16>(codes + raw * C::kRawBytes, scales + raw * C::kRawBytes, row_s + stage * C::kTileBytes);
+          __syncwarp();
+          mbar_arrive_elect(RAW_EMPTY + 8 * raw);
+          raw = raw + 1 == C::kRaws ? 0 : raw + 1;
+          raw_ph ^= raw == 0 ? 1u : 0u;
+        }
+        if (r >= lim) {
+          const uint32_t dst = kv_s + stage * C::kTileBytes + r * 128;
 #pragma unroll
-          for (int q = 0; q < D / 32; ++q) {  // 32 values: 16 bytes of codes, two scales
-            const uint4 w = *reinterpret_cast<const uint4*>(rec + (is_v ? D / 2 : 0) + q * 16);
-            const uint32_t sb = *reinterpret_cast<const uint16_t*>(scales + 2 * q);
-            uint32_t s0, c0, s1, c1;
-            widen_scale<kBF16>(sb & 0xffu, s0, c0);
-            widen_scale<kBF16>(sb >> 8, s1, c1);
-            uint4 o[4] = {widen8<kBF16>(w.x, s0, c0), widen8<kBF16>(w.y, s0, c0), widen8<kBF16>(w.z, s1, c1),
-                          widen8<kBF16>(w.w, s1, c1)};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int chunk = (4 * q + i) & 7;  // 16-byte chunk of the row's 128-byte span, swizzled by the row
-              *reinterpret_cast<uint4*>(dst + (q >> 1) * kHalfBytes + ((chunk ^ (r & 7)) << 4)) =
-                  real ? o[i] : make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
-          if (is_v) {
-            __syncwarp();
-            mbar_arrive_elect(RAW_EMPTY + 8 * (ri % C::kRaws));
-          }
+          for (int c = 0; c < 8 * C::kHalves; ++c)
+            st_shared_v4(dst + (c >> 3) * kHalfBytes + (c & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
         }
         fence_async_shared();  // the MMAs read the stage through the asynchronous proxy
         __syncwarp();
         mbar_arrive_elect(KV_FULL + 8 * stage);
-        return true;
-      };
-      if (W == 2) {
-        for (int k = 0; k < n && ok; ++k) ok = fill(k, false) && fill(k, true);
-      } else {
-        ok = fill(0, false) && (n < 2 || fill(1, false));
-        for (int j = 0; j < n && ok; ++j) ok = fill(j, true) && (j + 2 >= n || fill(j + 2, false));
       }
       ring += 2 * n;
-      raw += n - (tree ? 1 : 0);
-      if (tree) ++trees;
+      if (S.tile0 == 0) ++trees;
     }
   } else {
     // ------------------------------------------------------------------ softmax
@@ -611,15 +629,17 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
           }
           tmem_wait_st();
         }
-        // The row's 128 logits are read once (one TMEM round trip) and kept in registers for
-        // both passes: the maximum, then p = 2^(s * scale - m).
-        uint32_t s[128];
-        load_row(tl + s_col, s);
+        // pass 1: row maximum; pass 2: p = 2^(s * scale - m).  Each reads the row's 128 logits
+        // in one TMEM round trip (keeping them for both costs more registers than there are).
         float mx0 = -INFINITY, mx1 = -INFINITY;
+        {
+          uint32_t s[128];
+          load_row(tl + s_col, s);
 #pragma unroll
-        for (int c = 0; c < 128; c += 4) {
-          mx0 = max3(mx0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-          mx1 = max3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+          for (int c = 0; c < 128; c += 4) {
+            mx0 = max3(mx0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            mx1 = max3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+          }
         }
         const float m_new = fmaxf(m_run, fmaxf(mx0, mx1) * sl2);
         if (i == 0) {
@@ -642,7 +662,6 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
               tmem_st32(tl + o_col + c0, o);
             }
             tmem_wait_st();
-            load_row(tl + s_col, s);  // again, so that they need no registers beside O's
           }
         }
         const float nb = (m_run == -INFINITY) ? 0.f : -m_run;
@@ -650,6 +669,8 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
         // row sum (of the unrounded p, in fp32) run on packed fp32 pairs.
         const uint64_t sl2x2 = f2_pack(sl2, sl2), nbx2 = f2_pack(nb, nb);
         uint64_t lsx2 = f2_pack(0.f, 0.f);
+        uint32_t s[128];
+        load_row(tl + s_col, s);
 #pragma unroll
         for (int c = 0; c < 64; ++c) {
           float x0, x1;
