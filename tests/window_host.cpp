@@ -6,6 +6,7 @@
 //   - a row's mask (window_bits, over every tile) is exactly the keys it sees, and a tile
 //     that window_cuts leaves unmasked is seen whole by every row;
 //   - window_ancestors finds each node's depth and visible ancestors;
+//   - units and row groups found by bisection (stage_sums) are those found by walking;
 //   - the walk is no longer than walk_prefix_bound says, and every worker range covers
 //     the tiles once (total_units).
 // Prints "ok <problems>" or the first violation, and exits non-zero on a violation.
@@ -106,6 +107,24 @@ bool check(int P, const std::vector<int>& parent, int window, int sinks) {
     while (tva::next_segment(pr, u, t, t1, S, false)) covered += S.n;
   }
   if (covered != tva::total_units(pr)) return fail("units covered", covered, tva::total_units(pr));
+  // the same walk with the staged running sums
+  int buf[16];
+  tva::Problem sums = pr;
+  tva::stage_sums(sums, buf, 16);
+  if (sums.unit_start == nullptr) return fail("no sums", 0, 0);
+  if (tva::total_units(sums) != tva::total_units(pr)) return fail("total", tva::total_units(sums), 0);
+  for (long long t = 0; t < tva::total_units(pr); ++t) {
+    const tva::Loc a = tva::locate_unit(pr, t), b = tva::locate_unit(sums, t);
+    if (a.b != b.b || a.g != b.g || a.mp != b.mp || a.tile != b.tile || a.q != b.q || a.start != b.start)
+      return fail("unit found by bisection", t, b.b);
+  }
+  for (long long q = 0;; ++q) {
+    const tva::GroupLoc a = tva::locate_group(pr, q), b = tva::locate_group(sums, q);
+    if (a.found != b.found || a.T != b.T) return fail("row group found by bisection", q, b.found);
+    if (!a.found) break;
+    if (a.b != b.b || a.g != b.g || a.mp != b.mp || a.start != b.start || a.tiles != b.tiles)
+      return fail("row group by bisection", q, b.b);
+  }
   return true;
 }
 

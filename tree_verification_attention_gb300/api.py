@@ -396,34 +396,81 @@ def tree_verify_attn_varlen_noalloc(q, k_cache, v_cache, tree_k, tree_v, parent,
     return out, lse
 
 
-def _device_status(dev_status, device):
+# The calls below cost the host about as much as a small call costs the GPU, so their checks
+# are few and cheap: one pass over the tensors, pointers as plain integers.
+
+def _check_all(*named):
+    """Each (name, tensor, dtype): contiguous, of that type, on the current device (whose
+    stream the kernels run on).  Returns that device's index."""
+    here = named[0][1].get_device()
+    for name, t, dtype in named:
+        if t.get_device() != here or here < 0 or t.dtype is not dtype or not t.is_contiguous():
+            _dev(t, name, dtype)
+            raise ValueError(f"{name} is on {t.device}, {named[0][0]} on {named[0][1].device}")
+    if torch.cuda.current_device() != here:
+        raise ValueError(f"the tensors are on cuda:{here}, the current device is cuda:{torch.cuda.current_device()}")
+    return here
+
+
+def _raw_stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+def _status_word(dev_status, device):
     if dev_status is None:
         return torch.zeros(1, dtype=torch.int32, device=device)
-    return _dev(dev_status, "dev_status", torch.int32)
+    if dev_status.get_device() != device.index or dev_status.dtype is not torch.int32:
+        raise ValueError("dev_status must be int32, on the tensors' device")
+    return dev_status
 
 
-def _one_device(*tensors):
-    """The kernels run on the current device's stream: every tensor has to be there."""
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != here:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
-
-
-def _window_outputs(q, out, lse):
-    N, Hq, _ = q.shape
-    out = torch.empty_like(q) if out is None else _dev(out, "out", q.dtype)
-    lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device) if lse is None else _dev(lse, "lse", torch.float32)
-    if out.shape != q.shape or lse.shape != (N, Hq):
-        raise ValueError("out must have q's shape and lse [N, Hq]")
-    return out, lse
-
-
-def _check_heads(q, tree_k, params):
-    if q.dim() != 3 or tree_k.dim() != 3 or tree_k.shape[2] != q.shape[2]:
-        raise ValueError("q must be [N, Hq, d] and tree_k [N, Hkv, d]")
-    if params.num_kv_heads != tree_k.shape[1] or params.num_q_heads != q.shape[1] or params.head_dim != q.shape[2]:
+def _window_attention(name, window, sinks, q, cache, tree_k, tree_v, parent, cu_prefix, cu_nodes, max_prefix_len,
+                      max_nodes, out, lse, workspace, dev_status, softmax_scale, stream, params):
+    """The checks and the call that the windowed and the 4-bit-cache forms share; ``cache``
+    holds (name, tensor, dtype, row shape) of each cache tensor."""
+    dt, i32 = q.dtype, torch.int32
+    if dt not in DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
+    here = _check_all(("q", q, dt), ("tree_k", tree_k, dt), ("tree_v", tree_v, dt), ("parent", parent, i32),
+                      ("cu_prefix", cu_prefix, i32), ("cu_nodes", cu_nodes, i32), *(c[:3] for c in cache))
+    if q.dim() != 3 or tree_k.dim() != 3 or tree_k.shape != tree_v.shape:
+        raise ValueError("q must be [N, Hq, d], tree_k and tree_v [N, Hkv, d]")
+    N, Hq, d = q.shape
+    Nk, Hkv, dk = tree_k.shape
+    if Nk != N or dk != d or parent.shape[0] != N:
+        raise ValueError("q, tree_k and parent must have one row per tree node")
+    rows = cache[0][1].shape[0]
+    for label, t, _, row in cache:
+        if t.dim() != 3 or t.shape[0] != rows or t.shape[1] != Hkv or t.shape[2] != row:
+            raise ValueError(f"{label} must be [rows, {Hkv}, {row}]")
+    p = params
+    if p is None:
+        p = make_params(q, cache[0][1], cu_prefix, cu_nodes, Hkv, max_prefix_len, max_nodes, softmax_scale)
+    elif (p.num_q_heads != Hq or p.num_kv_heads != Hkv or p.head_dim != d or p.dtype != DTYPES[dt]
+          or p.node_capacity > N or p.kv_capacity > rows or p.cu_prefix != cu_prefix.data_ptr()
+          or p.cu_nodes != cu_nodes.data_ptr()):
         raise ValueError("params do not describe these tensors")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.get_device() != here or out.dtype is not dt or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be like q")
+    if lse is None:
+        lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
+    elif (lse.get_device() != here or lse.dtype is not torch.float32 or lse.shape != (N, Hq)
+          or not lse.is_contiguous()):
+        raise ValueError("lse must be [N, Hq] float32")
+    if workspace is None:
+        workspace = alloc_workspace(p, q.device)
+    elif workspace.get_device() != here or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8, on the tensors' device")
+    dev_status = _status_word(dev_status, q.device)
+    code = getattr(load_library(), name)(
+        ctypes.byref(p), int(window), int(sinks), q.data_ptr(), *(c[1].data_ptr() for c in cache), tree_k.data_ptr(),
+        tree_v.data_ptr(), parent.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        dev_status.data_ptr(), _raw_stream(stream, here))
+    if code:
+        _check(code, name)
+    return out, lse
 
 
 def tree_verify_attn_window_varlen(q, k_cache, v_cache, tree_k, tree_v, parent, cu_prefix, cu_nodes,
@@ -432,116 +479,11 @@ def tree_verify_attn_window_varlen(q, k_cache, v_cache, tree_k, tree_v, parent, 
     """tree_verify_attn_varlen under a sliding window: a node at position t (prefix length
     plus proper ancestors) sees the key at position s when ``t - s < window`` or
     ``s < sinks``.  ``window`` >= 1.  Returns (out [N, Hq, d], lse [N, Hq] float32)."""
-    _attn_inputs(q, k_cache, v_cache, tree_k, tree_v, parent, cu_prefix, cu_nodes)
-    _one_device(q, k_cache, v_cache, tree_k, tree_v, parent, cu_prefix, cu_nodes, out, lse, workspace, dev_status)
-    p = params or make_params(q, k_cache, cu_prefix, cu_nodes, tree_k.shape[1], max_prefix_len, max_nodes,
-                              softmax_scale)
-    _check_heads(q, tree_k, p)
-    if k_cache.shape[1:] != tree_k.shape[1:]:
-        raise ValueError("k_cache must be [rows, Hkv, d]")
-    out, lse = _window_outputs(q, out, lse)
-    if workspace is None:
-        workspace = alloc_workspace(p, q.device)
-    dev_status = _device_status(dev_status, q.device)
-    code = load_library().tree_verify_attn_window_varlen(
-        ctypes.byref(p), int(window), int(sinks), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(tree_k), _ptr(tree_v),
-        _ptr(parent), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream))
-    _check(code, "tree_verify_attn_window_varlen")
-    return out, lse
-
-
-def kv4_record_bytes(head_dim: int) -> int:
-    """Bytes that one row of one KV head takes in a 4-bit cache (K and V together)."""
-    n = int(load_library().tva_kv4_record_bytes(int(head_dim)))
-    if n == 0:
-        raise TvaError(2, "tva_kv4_record_bytes")
-    return n
-
-
-def alloc_kv4_cache(rows, num_kv_heads, head_dim, device="cuda") -> torch.Tensor:
-    """A 4-bit cache [rows, Hkv, record] uint8 of zeros (whose values are all 0)."""
-    return torch.zeros((rows, num_kv_heads, kv4_record_bytes(head_dim)), dtype=torch.uint8, device=device)
-
-
-def _kv4(kv4_cache, num_kv_heads, head_dim):
-    _dev(kv4_cache, "kv4_cache", torch.uint8)
-    if kv4_cache.dim() != 3 or kv4_cache.shape[1] != num_kv_heads or kv4_cache.shape[2] != kv4_record_bytes(head_dim):
-        raise ValueError(f"kv4_cache must be [rows, {num_kv_heads}, {kv4_record_bytes(head_dim)}] uint8")
-    return kv4_cache
-
-
-def _kv4_rows(k, v):
-    _dev(k, "k")
-    if k.dtype not in DTYPES:
-        raise ValueError(f"unsupported dtype {k.dtype}")
-    _dev(v, "v", k.dtype)
-    if k.dim() != 3 or k.shape != v.shape:
-        raise ValueError("k and v must be [rows, Hkv, d], alike")
-
-
-def append_kv4(k, v, slot, kv4_cache, dev_status=None, stream=None):
-    """Quantises k, v [n, Hkv, d] into rows slot[i] (int32; negative: skipped) of the 4-bit
-    cache, in place.  Returns dev_status (int32 [1], 0 = ok)."""
-    _kv4_rows(k, v)
-    _dev(slot, "slot", torch.int32)
-    n, Hkv, d = k.shape
-    if slot.shape != (n,):
-        raise ValueError("slot must hold one row number per row of k")
-    _kv4(kv4_cache, Hkv, d)
-    _one_device(k, v, slot, kv4_cache, dev_status)
-    dev_status = _device_status(dev_status, k.device)
-    code = load_library().append_kv4(n, Hkv, d, DTYPES[k.dtype], kv4_cache.shape[0], _ptr(k), _ptr(v), _ptr(slot),
-                                     _ptr(kv4_cache), _ptr(dev_status), _stream(stream))
-    _check(code, "append_kv4")
-    return dev_status
-
-
-def read_kv4(kv4_cache, head_dim, slot=None, dtype=torch.bfloat16, k=None, v=None, dev_status=None, stream=None):
-    """(k, v) [n, Hkv, head_dim] of ``dtype``: the values that rows slot[i] (int32; negative:
-    zeros) of the 4-bit cache stand for, or all rows in order when ``slot`` is None."""
-    if dtype not in DTYPES:
-        raise ValueError(f"unsupported dtype {dtype}")
-    _kv4(kv4_cache, kv4_cache.shape[1] if kv4_cache.dim() == 3 else 0, head_dim)
-    if slot is not None:
-        _dev(slot, "slot", torch.int32)
-        if slot.dim() != 1:
-            raise ValueError("slot must be one-dimensional")
-    shape = (kv4_cache.shape[0] if slot is None else slot.shape[0], kv4_cache.shape[1], int(head_dim))
-    k = torch.empty(shape, dtype=dtype, device=kv4_cache.device) if k is None else _dev(k, "k", dtype)
-    v = torch.empty(shape, dtype=dtype, device=kv4_cache.device) if v is None else _dev(v, "v", dtype)
-    if tuple(k.shape) != shape or tuple(v.shape) != shape:
-        raise ValueError(f"k and v must be {list(shape)}")
-    _one_device(kv4_cache, slot, k, v, dev_status)
-    dev_status = _device_status(dev_status, kv4_cache.device)
-    code = load_library().read_kv4(shape[0], shape[1], shape[2], DTYPES[dtype], kv4_cache.shape[0], _ptr(kv4_cache),
-                                   _ptr(slot), _ptr(k), _ptr(v), _ptr(dev_status), _stream(stream))
-    _check(code, "read_kv4")
-    return k, v
-
-
-def commit_accepted_kv4(cu_nodes, accept_len, accept_path, tree_k, tree_v, dst_row, kv4_cache, max_nodes=None,
-                        dev_status=None, stream=None):
-    """commit_accepted_kv into a 4-bit cache [rows, Hkv, record], in place.  Returns
-    dev_status (int32 [1], 0 = ok)."""
-    for name, t in (("cu_nodes", cu_nodes), ("accept_len", accept_len), ("accept_path", accept_path),
-                    ("dst_row", dst_row)):
-        _dev(t, name, torch.int32)
-    _kv4_rows(tree_k, tree_v)
-    B = cu_nodes.numel() - 1
-    N, Hkv, d = tree_k.shape
-    if accept_len.numel() != B or dst_row.numel() != B or accept_path.numel() != N:
-        raise ValueError("accept_len and dst_row must hold B entries and accept_path one per node")
-    _kv4(kv4_cache, Hkv, d)
-    _one_device(cu_nodes, accept_len, accept_path, tree_k, tree_v, dst_row, kv4_cache, dev_status)
-    if max_nodes is None:
-        max_nodes = int((cu_nodes[1:] - cu_nodes[:-1]).max().item()) if B > 0 else 1
-    dev_status = _device_status(dev_status, tree_k.device)
-    code = load_library().commit_accepted_kv4(
-        B, Hkv, d, DTYPES[tree_k.dtype], N, max(1, int(max_nodes)), kv4_cache.shape[0], _ptr(cu_nodes),
-        _ptr(accept_len), _ptr(accept_path), _ptr(tree_k), _ptr(tree_v), _ptr(dst_row), _ptr(kv4_cache),
-        _ptr(dev_status), _stream(stream))
-    _check(code, "commit_accepted_kv4")
-    return dev_status
+    d = q.shape[-1]
+    return _window_attention("tree_verify_attn_window_varlen", window, sinks, q,
+                             (("k_cache", k_cache, q.dtype, d), ("v_cache", v_cache, q.dtype, d)), tree_k, tree_v,
+                             parent, cu_prefix, cu_nodes, max_prefix_len, max_nodes, out, lse, workspace, dev_status,
+                             softmax_scale, stream, params)
 
 
 def tree_verify_attn_kv4_varlen(q, kv4_cache, tree_k, tree_v, parent, cu_prefix, cu_nodes, max_prefix_len,
@@ -550,18 +492,115 @@ def tree_verify_attn_kv4_varlen(q, kv4_cache, tree_k, tree_v, parent, cu_prefix,
     """Tree-verification attention whose prefix rows are records of a 4-bit cache; q, tree_k,
     tree_v bf16 or fp16.  ``window`` 0: the whole prefix, else as in
     tree_verify_attn_window_varlen.  Returns (out [N, Hq, d], lse [N, Hq] float32)."""
-    _attn_inputs(q, tree_k, tree_v, tree_k, tree_v, parent, cu_prefix, cu_nodes)
-    p = params or make_params(q, kv4_cache, cu_prefix, cu_nodes, tree_k.shape[1], max_prefix_len, max_nodes,
-                              softmax_scale)
-    _check_heads(q, tree_k, p)
-    _kv4(kv4_cache, tree_k.shape[1], q.shape[2])
-    _one_device(q, kv4_cache, tree_k, tree_v, parent, cu_prefix, cu_nodes, out, lse, workspace, dev_status)
-    out, lse = _window_outputs(q, out, lse)
-    if workspace is None:
-        workspace = alloc_workspace(p, q.device)
-    dev_status = _device_status(dev_status, q.device)
-    code = load_library().tree_verify_attn_kv4_varlen(
-        ctypes.byref(p), int(window), int(sinks), _ptr(q), _ptr(kv4_cache), _ptr(tree_k), _ptr(tree_v), _ptr(parent),
-        _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream))
-    _check(code, "tree_verify_attn_kv4_varlen")
-    return out, lse
+    return _window_attention("tree_verify_attn_kv4_varlen", window, sinks, q,
+                             (("kv4_cache", kv4_cache, torch.uint8, kv4_record_bytes(q.shape[-1])),), tree_k, tree_v,
+                             parent, cu_prefix, cu_nodes, max_prefix_len, max_nodes, out, lse, workspace, dev_status,
+                             softmax_scale, stream, params)
+
+
+_record_bytes = {}
+
+
+def kv4_record_bytes(head_dim: int) -> int:
+    """Bytes that one row of one KV head takes in a 4-bit cache (K and V together)."""
+    n = _record_bytes.get(head_dim)
+    if n is None:
+        n = int(load_library().tva_kv4_record_bytes(int(head_dim)))
+        if n == 0:
+            raise TvaError(2, "tva_kv4_record_bytes")
+        _record_bytes[head_dim] = n
+    return n
+
+
+def alloc_kv4_cache(rows, num_kv_heads, head_dim, device="cuda") -> torch.Tensor:
+    """A 4-bit cache [rows, Hkv, record] uint8 of zeros (whose values are all 0)."""
+    return torch.zeros((rows, num_kv_heads, kv4_record_bytes(head_dim)), dtype=torch.uint8, device=device)
+
+
+def _check_records(kv4_cache, num_kv_heads, head_dim):
+    record = kv4_record_bytes(head_dim)
+    if kv4_cache.dim() != 3 or kv4_cache.shape[1] != num_kv_heads or kv4_cache.shape[2] != record:
+        raise ValueError(f"kv4_cache must be [rows, {num_kv_heads}, {record}] uint8")
+
+
+def _check_rows(k, v):
+    if k.dtype not in DTYPES:
+        raise ValueError(f"unsupported dtype {k.dtype}")
+    if k.dim() != 3 or k.shape != v.shape:
+        raise ValueError("k and v must be [rows, Hkv, d], alike")
+
+
+def append_kv4(k, v, slot, kv4_cache, dev_status=None, stream=None):
+    """Quantises k, v [n, Hkv, d] into rows slot[i] (int32; negative: skipped) of the 4-bit
+    cache, in place.  Returns dev_status (int32 [1], 0 = ok)."""
+    _check_rows(k, v)
+    here = _check_all(("k", k, k.dtype), ("v", v, k.dtype), ("slot", slot, torch.int32),
+                      ("kv4_cache", kv4_cache, torch.uint8))
+    n, Hkv, d = k.shape
+    if slot.shape != (n,):
+        raise ValueError("slot must hold one row number per row of k")
+    _check_records(kv4_cache, Hkv, d)
+    dev_status = _status_word(dev_status, k.device)
+    code = load_library().append_kv4(n, Hkv, d, DTYPES[k.dtype], kv4_cache.shape[0], k.data_ptr(), v.data_ptr(),
+                                     slot.data_ptr(), kv4_cache.data_ptr(), dev_status.data_ptr(),
+                                     _raw_stream(stream, here))
+    if code:
+        _check(code, "append_kv4")
+    return dev_status
+
+
+def read_kv4(kv4_cache, head_dim, slot=None, dtype=torch.bfloat16, k=None, v=None, dev_status=None, stream=None):
+    """(k, v) [n, Hkv, head_dim] of ``dtype``: the values that rows slot[i] (int32; negative:
+    zeros) of the 4-bit cache stand for, or all rows in order when ``slot`` is None."""
+    if dtype not in DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    here = _check_all(("kv4_cache", kv4_cache, torch.uint8))
+    _check_records(kv4_cache, kv4_cache.shape[1] if kv4_cache.dim() == 3 else 0, head_dim)
+    rows, Hkv, _ = kv4_cache.shape
+    n = rows
+    if slot is not None:
+        _check_all(("slot", slot, torch.int32))
+        if slot.dim() != 1:
+            raise ValueError("slot must be one-dimensional")
+        n = slot.shape[0]
+    shape = (n, Hkv, int(head_dim))
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=kv4_cache.device)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=kv4_cache.device)
+    _check_all(("k", k, dtype), ("v", v, dtype))
+    if k.shape != shape or v.shape != shape:
+        raise ValueError(f"k and v must be {list(shape)}")
+    dev_status = _status_word(dev_status, kv4_cache.device)
+    code = load_library().read_kv4(n, Hkv, shape[2], DTYPES[dtype], rows, kv4_cache.data_ptr(),
+                                   None if slot is None else slot.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                   dev_status.data_ptr(), _raw_stream(stream, here))
+    if code:
+        _check(code, "read_kv4")
+    return k, v
+
+
+def commit_accepted_kv4(cu_nodes, accept_len, accept_path, tree_k, tree_v, dst_row, kv4_cache, max_nodes=None,
+                        dev_status=None, stream=None):
+    """commit_accepted_kv into a 4-bit cache [rows, Hkv, record], in place.  Returns
+    dev_status (int32 [1], 0 = ok)."""
+    _check_rows(tree_k, tree_v)
+    dt, i32 = tree_k.dtype, torch.int32
+    here = _check_all(("cu_nodes", cu_nodes, i32), ("accept_len", accept_len, i32), ("accept_path", accept_path, i32),
+                      ("dst_row", dst_row, i32), ("tree_k", tree_k, dt), ("tree_v", tree_v, dt),
+                      ("kv4_cache", kv4_cache, torch.uint8))
+    B = cu_nodes.shape[0] - 1
+    N, Hkv, d = tree_k.shape
+    if accept_len.shape[0] != B or dst_row.shape[0] != B or accept_path.shape[0] != N:
+        raise ValueError("accept_len and dst_row must hold B entries and accept_path one per node")
+    _check_records(kv4_cache, Hkv, d)
+    if max_nodes is None:
+        max_nodes = int((cu_nodes[1:] - cu_nodes[:-1]).max().item()) if B > 0 else 1
+    dev_status = _status_word(dev_status, tree_k.device)
+    code = load_library().commit_accepted_kv4(
+        B, Hkv, d, DTYPES[dt], N, max(1, int(max_nodes)), kv4_cache.shape[0], cu_nodes.data_ptr(),
+        accept_len.data_ptr(), accept_path.data_ptr(), tree_k.data_ptr(), tree_v.data_ptr(), dst_row.data_ptr(),
+        kv4_cache.data_ptr(), dev_status.data_ptr(), _raw_stream(stream, here))
+    if code:
+        _check(code, "commit_accepted_kv4")
+    return dev_status

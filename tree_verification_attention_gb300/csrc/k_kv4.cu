@@ -9,7 +9,11 @@
 // A thread quantises one block of 16 values: it loads them, finds the scale, and stores
 // eight bytes of codes; four threads put their scale bytes together into one word.  The
 // blocks of a row are numbered K before V and head by head, so neighbouring threads load
-// neighbouring 32 (fp32: 64) bytes.
+// neighbouring 32 (fp32: 64) bytes.  A thread block takes a few whole rows, so that the
+// numbers of its items stay small and dividing them by a row's items is one multiplication.
+// All three are bound by memory: what they read and write, once.
+#include <type_traits>
+
 #include "kv4.cuh"
 #include "tc_ptx.cuh"
 #include "tva_internal.h"
@@ -18,29 +22,91 @@ namespace tva {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kItemsPerBlock = 2048;
+
+// t / d for t < 2^16, d <= 2^16 as a multiplication: with m = ceil(2^32 / d) the error of
+// t m / 2^32 is below t / 2^32 < 1 / d.
+__host__ __device__ inline uint32_t small_inverse(uint32_t d) { return (uint32_t)(((1ull << 32) + d - 1) / d); }
+__device__ __forceinline__ int small_div(int t, uint32_t inverse) { return (int)__umulhi((uint32_t)t, inverse); }
 
 template <typename T> __device__ __forceinline__ float to_f(T v) { return (float)v; }
 
-// Quantises the 16 values at `src` (aligned to their size) into codes and a scale byte.
+// The general form: any values of any type.
 template <typename T>
-__device__ __forceinline__ int quantise16(const T* src, uint32_t code[2]) {
-  alignas(16) T x[16];
-  const uint4* s4 = reinterpret_cast<const uint4*>(src);
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T); ++i) reinterpret_cast<uint4*>(x)[i] = __ldg(s4 + i);
+__device__ __noinline__ int quantise16_any(const T* x, uint32_t code[2]) {
   float amax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(to_f(x[i])));
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(to_f(x[i])));  // (a NaN is passed over)
   const int byte = kv4_scale_byte(amax);
   const float s = kv4_scale_value(byte), inv = byte > 0 ? 1.0f / s : 0.0f;
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    uint32_t c = 0u;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) c |= (uint32_t)(kv4_round(to_f(x[8 * w + e]), s, inv) + 8) << kv4_shift(e);
-    code[w] = c;
-  }
+  code[0] = code[1] = 0u;
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i) code[i >> 3] |= (uint32_t)(kv4_round(to_f(x[i]), s, inv) + 8) << kv4_shift(i & 7);
   return byte;
+}
+
+// The two values of a packed 16-bit pair.
+template <typename T> __device__ __forceinline__ float2 pair_f(uint32_t w);
+template <> __device__ __forceinline__ float2 pair_f<__nv_bfloat16>(uint32_t w) {
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+template <> __device__ __forceinline__ float2 pair_f<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Quantises the 16 values at `src` (16-byte aligned) into codes and a scale byte.
+//
+// 16-bit values with a normal scale below the largest take a short way.  A quotient x / s
+// (11 significant bits over 4, below 7.5) that is not halfway between two whole numbers is
+// at least 2^-8 / 30 > 2^-13 away from it, so it may be rounded to a multiple of 2^-15
+// first - which one fused multiply-add onto 384 does, taking up the errors of 1 / s as
+// well - and that exactly representable value to the nearest whole number by a second
+// addition, onto 3 * 2^22, whose low bits are then the code.  No limit is needed: the scale
+// is at least 16/17 of amax / 7, so |x / s| <= 7.4375.
+template <typename T>
+__device__ __forceinline__ int quantise16(const T* src, uint32_t code[2]) {
+  if constexpr (sizeof(T) == 4) {
+    alignas(16) T x[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      reinterpret_cast<uint4*>(x)[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+    const int byte = kv4_scale_byte(amax);
+    const float s = kv4_scale_value(byte), inv = byte > 0 ? 1.0f / s : 0.0f;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      uint32_t c = 0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c |= (uint32_t)(kv4_round(x[8 * w + e], s, inv) + 8) << kv4_shift(e);
+      code[w] = c;
+    }
+    return byte;
+  } else {
+    constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    const uint4 lo = __ldg(reinterpret_cast<const uint4*>(src)), hi = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    uint32_t m = w[0] & 0x7fff7fffu;  // the order of magnitudes is that of their bits
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    m = max(m & 0xffffu, m >> 16);
+    const int byte = kv4_scale_byte(pair_f<T>(m).x);
+    if (m >= kInf || byte < 8 || byte >= kKv4MaxScale) return quantise16_any(src, code);
+    const float inv = __fdividef(1.0f, kv4_scale_value(byte));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t c = 0u - 0x4b400000u * 0x11111111u;  // what the eight sums' exponent bits add up to
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 p = pair_f<T>(w[4 * h + e / 2]);
+        const float z = fmaf(e & 1 ? p.y : p.x, inv, 384.0f);
+        c += __float_as_uint(z + 12582536.0f) << kv4_shift(e);  // 3 * 2^22 - 384 + 8
+      }
+      code[h] = c;
+    }
+    return byte;
+  }
 }
 
 // One block (half 0: K, 1: V; block `blk` of head `head`) of a row into its record.  Called
@@ -52,6 +118,7 @@ __device__ __forceinline__ void store_block(const T* src, uint8_t* rec, int d, i
   *reinterpret_cast<uint2*>(rec + half * (d / 2) + blk * 8) = make_uint2(code[0], code[1]);
   const int lane = threadIdx.x & 31;
   const uint32_t group = 0xfu << (lane & ~3);
+  __syncwarp(group);
   uint32_t w = (uint32_t)byte << (8 * (lane & 3));
   w |= __shfl_xor_sync(group, w, 1);
   w |= __shfl_xor_sync(group, w, 2);
@@ -65,35 +132,38 @@ __device__ __forceinline__ void store_block(const T* src, uint8_t* rec, int d, i
 template <typename T>
 __device__ __forceinline__ void quantise_item(const T* k, const T* v, uint8_t* cache, long long src_row,
                                               long long dst_row, int Hkv, int d, int t) {
-  const int nb = d / 16, per = Hkv * nb;
+  const int shift = d == 128 ? 3 : 2;  // d / 16 blocks a head
+  const int per = Hkv << shift;
   const int half = t >= per ? 1 : 0;
   const int in_row = t - half * per;
-  const int head = in_row / nb, blk = in_row % nb;
+  const int head = in_row >> shift, blk = in_row & ((1 << shift) - 1);
   const T* src = (half ? v : k) + src_row * (long long)Hkv * d + in_row * 16;
   uint8_t* rec = cache + (dst_row * Hkv + head) * (long long)kv4_record_bytes(d);
   store_block<T>(src, rec, d, half, blk);
 }
 
+// rows_per_block whole rows a block; `inverse` is small_inverse(items of a row).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) append_kernel(Kv4RowArgs a) {
+__global__ void __launch_bounds__(kThreads) append_kernel(Kv4RowArgs a, int rows_per_block, uint32_t inverse) {
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   const int per_row = 2 * a.Hkv * (a.d / 16);
-  const long long total = (long long)a.rows * per_row;
-  for (long long e = (long long)blockIdx.x * kThreads + threadIdx.x; e < total; e += (long long)gridDim.x * kThreads) {
-    const long long row = e / per_row;
-    const int t = (int)(e - row * per_row);
-    const long long slot = __ldg(a.slot + row);
+  const long long row0 = (long long)blockIdx.x * rows_per_block;
+  const int rows = (int)min((long long)rows_per_block, a.rows - row0);
+  for (int e = threadIdx.x; e < rows * per_row; e += kThreads) {
+    const int i = rows_per_block > 1 ? small_div(e, inverse) : 0;
+    const int t = e - i * per_row;
+    const long long slot = __ldg(a.slot + row0 + i);
     if (slot < 0) continue;
     if (slot >= a.kv_capacity) {
       if (t == 0) set_status(a.status, kStatusInvalidArg);
       continue;
     }
-    quantise_item<T>(static_cast<const T*>(a.k), static_cast<const T*>(a.v), a.cache, row, slot, a.Hkv, a.d, t);
+    quantise_item<T>(static_cast<const T*>(a.k), static_cast<const T*>(a.v), a.cache, row0 + i, slot, a.Hkv, a.d, t);
   }
 }
 
-constexpr int kRowsPerBlock = 8;
+constexpr int kRowsPerBlock = 2;  // of the commit: few rows, so many small blocks
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) commit_kv4_kernel(CommitArgs a, int Hkv, int d) {
@@ -120,11 +190,10 @@ __global__ void __launch_bounds__(kThreads) commit_kv4_kernel(CommitArgs a, int 
   }
   const int j0 = y * kRowsPerBlock, j1 = min(L, j0 + kRowsPerBlock);
   const int per_row = 2 * Hkv * (d / 16);
-  for (int e = threadIdx.x; e < (j1 - j0) * per_row; e += kThreads) {
-    const int j = j0 + e / per_row;
-    quantise_item<T>(static_cast<const T*>(a.tree_k), static_cast<const T*>(a.tree_v),
-                     static_cast<uint8_t*>(a.k_cache), (long long)n0 + s_path[j], dst + j, Hkv, d, e % per_row);
-  }
+  for (int j = j0; j < j1; ++j)
+    for (int t = threadIdx.x; t < per_row; t += kThreads)
+      quantise_item<T>(static_cast<const T*>(a.tree_k), static_cast<const T*>(a.tree_v),
+                       static_cast<uint8_t*>(a.k_cache), (long long)n0 + s_path[j], dst + j, Hkv, d, t);
 }
 
 // Eight values of code word `w` at scale byte `byte`.
@@ -149,16 +218,19 @@ __device__ __forceinline__ void store8(__half* dst, const float x[8]) {  // exac
 
 // A thread reads one code word (8 values), numbered as the destination's elements.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) read_kernel(Kv4RowArgs a) {
+__global__ void __launch_bounds__(kThreads) read_kernel(Kv4RowArgs a, int rows_per_block, uint32_t inverse) {
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  const int words = a.d / 8, per_half = a.Hkv * words;
-  const long long total = (long long)a.rows * per_half * 2;
-  for (long long e = (long long)blockIdx.x * kThreads + threadIdx.x; e < total; e += (long long)gridDim.x * kThreads) {
-    const long long row = e / (2 * per_half);
-    const int t = (int)(e - row * 2 * per_half);
+  const int shift = a.d == 128 ? 4 : 3;  // d / 8 words a head
+  const int per_half = a.Hkv << shift, per_row = 2 * per_half;
+  const long long row0 = (long long)blockIdx.x * rows_per_block;
+  const int rows = (int)min((long long)rows_per_block, a.rows - row0);
+  for (int e = threadIdx.x; e < rows * per_row; e += kThreads) {
+    const int r = rows_per_block > 1 ? small_div(e, inverse) : 0;
+    const int t = e - r * per_row;
+    const long long row = row0 + r;
     const int half = t >= per_half ? 1 : 0, in_row = t - half * per_half;
-    const int head = in_row / words, i = in_row % words;
+    const int head = in_row >> shift, i = in_row & ((1 << shift) - 1);
     const long long slot = a.slot != nullptr ? (long long)__ldg(a.slot + row) : row;
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (slot >= a.kv_capacity) {
@@ -173,22 +245,25 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Kv4RowArgs a) {
   }
 }
 
-unsigned blocks_for(long long items) {
-  const long long b = (items + kThreads - 1) / kThreads;
-  return (unsigned)(b < 1 ? 1 : (b < 152 * 64 ? b : 152 * 64));
+// Rows a block and blocks for rows of `per_row` items; more than 2^16 items a row (never
+// numbered by small_div then) get a block each.
+template <typename K>
+cudaError_t launch_rows(K kernel, const Kv4RowArgs& a, int per_row, cudaStream_t s, const char* what) {
+  const int rows_per_block = per_row >= kItemsPerBlock ? 1 : kItemsPerBlock / per_row;
+  const long long blocks = ((long long)a.rows + rows_per_block - 1) / rows_per_block;
+  return check_cuda(launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, rows_per_block,
+                               small_inverse((uint32_t)per_row)),
+                    what);
 }
 
 template <typename T>
 cudaError_t run_append(const Kv4RowArgs& a, cudaStream_t s) {
-  const long long items = (long long)a.rows * 2 * a.Hkv * (a.d / 16);
-  return check_cuda(launch_pdl(append_kernel<T>, dim3(blocks_for(items)), dim3(kThreads), 0, s, a),
-                    "launch append_kernel");
+  return launch_rows(append_kernel<T>, a, 2 * a.Hkv * (a.d / 16), s, "launch append_kernel");
 }
 
 template <typename T>
 cudaError_t run_read(const Kv4RowArgs& a, cudaStream_t s) {
-  const long long items = (long long)a.rows * 2 * a.Hkv * (a.d / 8);
-  return check_cuda(launch_pdl(read_kernel<T>, dim3(blocks_for(items)), dim3(kThreads), 0, s, a), "launch read_kernel");
+  return launch_rows(read_kernel<T>, a, 2 * a.Hkv * (a.d / 8), s, "launch read_kernel");
 }
 
 template <typename T>

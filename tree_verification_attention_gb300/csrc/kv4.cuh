@@ -55,11 +55,10 @@ __device__ __forceinline__ float kv4_scale_value(int byte) {
 // residual x - q s (exact there) says which side of the border x is on.  NaN gives 0, and
 // so does every x at scale 0.
 __device__ __forceinline__ int kv4_round(float x, float s, float inv) {
-  if (s == 0.0f) return 0;
-  x = x == x ? x : 0.0f;
-  float q = rintf(x * inv);
-  const float r = fabsf(fmaf(-q, s, x)), h = 0.5f * s;
-  if (r > h || (r == h && fmodf(q, 2.0f) != 0.0f)) q += copysignf(1.0f, fmaf(-q, s, x));
+  if (s == 0.0f || x != x) return 0;
+  float q = fminf(fmaxf(rintf(x * inv), -8.0f), 8.0f);
+  const float r = fmaf(-q, s, x), h = 0.5f * s;
+  if (fabsf(r) > h || (fabsf(r) == h && ((int)q & 1))) q += copysignf(1.0f, r);
   return (int)fminf(fmaxf(q, -7.0f), 7.0f);
 }
 

@@ -67,6 +67,11 @@ struct Problem {
   // plus its number of proper ancestors) sees the key at position s when t - s < W or
   // s < sinks; the walk then covers only the prefix keys that some node sees (SeqInfo).
   int window, sinks;
+  // Null, or (staged in shared memory) B + 1 running sums over the sequences: units and row
+  // groups before sequence b.  With them a unit or row group is found by bisection; without
+  // them by walking the sequences, which at 32 of them cost about 2 us a time.
+  const int32_t* unit_start;
+  const int32_t* group_start;
 };
 
 struct SeqInfo {
@@ -169,45 +174,6 @@ __host__ __device__ __forceinline__ long long walk_prefix_bound(const Problem& p
   return a < b ? a : b;
 }
 
-// Copies cu_prefix / cu_nodes into `buf` (2 * (B + 1) ints of shared memory) when they
-// fit in `cap` ints, and points `pr` at the copies, so that the sequence walks below
-// cost shared-memory loads instead of one round of global loads per sequence.  Every
-// thread of the block must call it; it ends with a block barrier.
-__device__ __forceinline__ void stage_cu(Problem& pr, int* buf, int cap) {
-  const bool fits = pr.cu_prefix != nullptr && 2 * (pr.B + 1) <= cap;
-  if (fits) {
-    for (int i = threadIdx.x; i <= pr.B; i += blockDim.x) {
-      buf[i] = __ldg(pr.cu_prefix + i);
-      buf[pr.B + 1 + i] = __ldg(pr.cu_nodes + i);
-    }
-  }
-  __syncthreads();
-  if (fits) {
-    pr.cu_prefix = buf;
-    pr.cu_nodes = buf + pr.B + 1;
-  }
-}
-
-// Same, but the resulting problem description is also placed in shared memory (`dst`),
-// so that kernels short of registers can read its fields from there.
-__device__ __forceinline__ void stage_problem(const Problem& src, Problem* dst, int* buf, int cap) {
-  const bool fits = src.cu_prefix != nullptr && 2 * (src.B + 1) <= cap;
-  if (fits) {
-    for (int i = threadIdx.x; i <= src.B; i += blockDim.x) {
-      buf[i] = __ldg(src.cu_prefix + i);
-      buf[src.B + 1 + i] = __ldg(src.cu_nodes + i);
-    }
-  }
-  if (threadIdx.x == 0) {
-    *dst = src;
-    if (fits) {
-      dst->cu_prefix = buf;
-      dst->cu_nodes = buf + src.B + 1;
-    }
-  }
-  __syncthreads();
-}
-
 // Reports (once, from one thread) a cu_* entry outside the stated bounds.  The
 // offending sequence is treated as empty by every kernel.
 __device__ __forceinline__ void validate_sequences(const Problem& pr, int32_t* status) {
@@ -224,8 +190,107 @@ __device__ __forceinline__ int seq_groups(const Problem& pr, int m) {
   return (m * pr.G + pr.RG - 1) / pr.RG;
 }
 
+// Fills pr.unit_start / group_start (4 (B + 1) ints of `buf` hold the cu_* copies and the
+// sums) when they fit and the units can be counted in 32 bits.  Every thread of the block
+// must call it, after the cu_* copies are in place; it ends with a block barrier.
+__device__ __forceinline__ void stage_sums(Problem& pr, int* buf, int cap) {
+  constexpr int kOwn = 4;  // entries per thread
+  const int n = pr.B + 1;
+  if (4 * n > cap || n > kOwn * (int)blockDim.x) return;  // uniform over the block
+  int* units = buf + 2 * n;
+  int* groups = buf + 3 * n;
+  for (int b = threadIdx.x; b < pr.B; b += blockDim.x) {
+    const SeqInfo s = seq_info(pr, b);
+    const long long g = (long long)pr.Hkv * seq_groups(pr, s.m), u = g * seq_tiles(s.P);
+    units[b] = u < (1LL << 30) ? (int)u : -1;  // -1: too many to count here
+    groups[b] = (int)g;
+  }
+  __syncthreads();
+  long long us[kOwn];
+  int gs[kOwn];
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int b = threadIdx.x + i * blockDim.x;
+    us[i] = 0;
+    gs[i] = 0;
+    if (b < n)
+      for (int c = 0; c < b; ++c) {
+        us[i] = us[i] < 0 || units[c] < 0 ? -1 : us[i] + units[c];
+        gs[i] += groups[c];
+      }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int b = threadIdx.x + i * blockDim.x;
+    if (b < n) {
+      units[b] = us[i] <= 0x7fffffffLL ? (int)us[i] : -1;
+      groups[b] = gs[i];
+    }
+  }
+  __syncthreads();
+  if (units[pr.B] >= 0) {
+    pr.unit_start = units;
+    pr.group_start = groups;
+  }
+}
+
+// The last b with start[b] <= x (start has n + 1 ascending entries, start[0] <= x < start[n]):
+// the one sequence that x falls into.
+__device__ __forceinline__ int find_sequence(const int32_t* start, int n, long long x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Copies cu_prefix / cu_nodes into `buf` (2 * (B + 1) ints of shared memory) when they
+// fit in `cap` ints, and points `pr` at the copies, so that the sequence walks below
+// cost shared-memory loads instead of one round of global loads per sequence.  Every
+// thread of the block must call it; it ends with a block barrier.
+__device__ __forceinline__ void stage_cu(Problem& pr, int* buf, int cap) {
+  const bool fits = pr.cu_prefix != nullptr && 2 * (pr.B + 1) <= cap;
+  if (fits) {
+    for (int i = threadIdx.x; i <= pr.B; i += blockDim.x) {
+      buf[i] = __ldg(pr.cu_prefix + i);
+      buf[pr.B + 1 + i] = __ldg(pr.cu_nodes + i);
+    }
+  }
+  __syncthreads();
+  if (fits) {
+    pr.cu_prefix = buf;
+    pr.cu_nodes = buf + pr.B + 1;
+    stage_sums(pr, buf, cap);
+  }
+}
+
+// Same, but the resulting problem description is also placed in shared memory (`dst`),
+// so that kernels short of registers can read its fields from there.
+__device__ __forceinline__ void stage_problem(const Problem& src, Problem* dst, int* buf, int cap) {
+  const bool fits = src.cu_prefix != nullptr && 2 * (src.B + 1) <= cap;
+  if (fits) {
+    for (int i = threadIdx.x; i <= src.B; i += blockDim.x) {
+      buf[i] = __ldg(src.cu_prefix + i);
+      buf[src.B + 1 + i] = __ldg(src.cu_nodes + i);
+    }
+  }
+  Problem pr = src;
+  if (fits) {
+    __syncthreads();
+    pr.cu_prefix = buf;
+    pr.cu_nodes = buf + src.B + 1;
+    stage_sums(pr, buf, cap);
+  }
+  if (threadIdx.x == 0) *dst = pr;
+  __syncthreads();
+}
+
 // Total units T and the chunk size c = ceil(T / U).
 __device__ __forceinline__ long long total_units(const Problem& pr) {
+  if (pr.unit_start != nullptr) return pr.unit_start[pr.B];
   long long T = 0;
   for (int b = 0; b < pr.B; ++b) {
     SeqInfo s = seq_info(pr, b);
@@ -253,8 +318,13 @@ struct Loc {
 __device__ __forceinline__ Loc locate_unit(const Problem& pr, long long t) {
   Loc L;
   long long acc = 0;
-  int qacc = 0;
-  for (int b = 0; b < pr.B; ++b) {
+  int qacc = 0, b = 0;
+  if (pr.unit_start != nullptr) {
+    b = find_sequence(pr.unit_start, pr.B, t);
+    acc = pr.unit_start[b];
+    qacc = pr.group_start[b];
+  }
+  for (; b < pr.B; ++b) {
     SeqInfo s = seq_info(pr, b);
     int MP = seq_groups(pr, s.m);
     int tiles = seq_tiles(s.P);
@@ -423,7 +493,15 @@ __device__ __forceinline__ GroupLoc locate_group(const Problem& pr, long long qg
   R.b = R.g = R.mp = R.tiles = 0;
   R.start = 0;
   long long acc = 0, qacc = 0;
-  for (int b = 0; b < pr.B; ++b) {
+  int first = 0;
+  if (pr.unit_start != nullptr) {
+    R.T = pr.unit_start[pr.B];
+    if (qg >= pr.group_start[pr.B]) return R;
+    first = find_sequence(pr.group_start, pr.B, qg);
+    acc = pr.unit_start[first];
+    qacc = pr.group_start[first];
+  }
+  for (int b = first; b < pr.B; ++b) {
     const SeqInfo s = seq_info(pr, b);
     const int MP = seq_groups(pr, s.m);
     const int tiles = seq_tiles(s.P);
@@ -433,6 +511,7 @@ __device__ __forceinline__ GroupLoc locate_group(const Problem& pr, long long qg
       R.s = s; R.b = b; R.g = (int)(gi / MP); R.mp = (int)(gi % MP); R.tiles = tiles;
       R.start = acc + gi * tiles;
       R.found = true;
+      if (pr.unit_start != nullptr) return R;
     }
     acc += nq * tiles;
     qacc += nq;

@@ -120,6 +120,7 @@ tva_status make_layout(int B, int Hq, int Hkv, int d, int dtype, int max_prefix,
   pr.U = dtype == TVA_FP32 ? sms * tva::simt_workers_per_sm() : (L->pair ? sms / 2 : sms);
   pr.max_prefix = max_prefix; pr.max_nodes = max_nodes;
   pr.window = pr.sinks = 0;
+  pr.unit_start = pr.group_start = nullptr;
   pr.kv_capacity = kv_cap; pr.node_capacity = node_cap;
   const int mp_max = (max_nodes + W * npt - 1) / (W * npt);  // row groups per KV head
   const long long groups = (long long)B * Hkv * mp_max;
@@ -251,7 +252,7 @@ bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
 // not overlap the cache (neither side has a defined order).
 tva_status check_kv4_rows(int num_rows, int Hkv, int d, int dtype, long long kv_capacity, const void* k, const void* v,
                           const void* cache, const int32_t* dev_status) {
-  if (num_rows < 0 || Hkv < 1 || kv_capacity < 0 || kv_capacity > (1LL << 31) - 1 || !dev_status)
+  if (num_rows < 0 || Hkv < 1 || Hkv > 65536 || kv_capacity < 0 || kv_capacity > (1LL << 31) - 1 || !dev_status)
     return TVA_ERR_INVALID_ARG;
   if ((num_rows > 0 && (!k || !v)) || (kv_capacity > 0 && !cache)) return TVA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return TVA_ERR_UNSUPPORTED;
