@@ -249,7 +249,11 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Kv4RowArgs a, int rows_p
 // numbered by small_div then) get a block each.
 template <typename K>
 cudaError_t launch_rows(K kernel, const Kv4RowArgs& a, int per_row, cudaStream_t s, const char* what) {
-  const int rows_per_block = per_row >= kItemsPerBlock ? 1 : kItemsPerBlock / per_row;
+  // about 2048 items a block, but no fewer than 8 blocks an SM's worth while the rows last
+  // (each block then holds a thread's worth of items or a row)
+  const long long spread = a.rows / (152 * 8) + 1, least = (kThreads + per_row - 1) / per_row;
+  const long long most = per_row >= kItemsPerBlock ? 1 : kItemsPerBlock / per_row;
+  const int rows_per_block = (int)(spread < least ? least : spread < most ? spread : most);
   const long long blocks = ((long long)a.rows + rows_per_block - 1) / rows_per_block;
   return check_cuda(launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, rows_per_block,
                                small_inverse((uint32_t)per_row)),

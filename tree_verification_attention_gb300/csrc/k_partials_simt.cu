@@ -41,18 +41,20 @@ __device__ __forceinline__ float4 load4(const T* p) {
 
 template <int D>
 constexpr size_t simt_smem_bytes() {
-  return sizeof(float) * (kRB * (D + 1) + kKT * (D + 1) + kKT * D + kRB * (kKT + 1)) +
-         sizeof(uint32_t) * kMaxNodes * 4;
+  return sizeof(float) * (kRB * D + kKT * D + kKT * D + kRB * (kKT + 4)) + sizeof(uint32_t) * kMaxNodes * 4;
 }
 
 template <typename T, int D, bool kWin>
 __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs a) {
   extern __shared__ float smem[];
-  float* qs = smem;                          // [kRB][D+1]
-  float* ks = qs + kRB * (D + 1);            // [kKT][D+1]
-  float* vs = ks + kKT * (D + 1);            // [kKT][D]
-  float* ps = vs + kKT * D;                  // [kRB][kKT+1]
-  uint32_t* masks = reinterpret_cast<uint32_t*>(ps + kRB * (kKT + 1));  // [128][4]
+  // All shared-memory reads of the two products are 16 bytes wide (with single values they
+  // bound the kernel).  Chunk c (4 floats) of row r of qs is at c ^ (r mod 8), of key r of ks
+  // at c ^ (r / 4 mod 8): the rows that a warp reads together are then in different banks.
+  float* qs = smem;                          // [kRB][D]
+  float* ks = qs + kRB * D;                  // [kKT][D]
+  float* vs = ks + kKT * D;                  // [kKT][D]
+  float* ps = vs + kKT * D;                  // [kRB][kKT+4]
+  uint32_t* masks = reinterpret_cast<uint32_t*>(ps + kRB * (kKT + 4));  // [128][4]
   __shared__ int tree_bad;
   __shared__ int par_s[kMaxNodes];           // parent ids of the current tree
   __shared__ int low_s[kWin ? kMaxNodes : 1];  // kWin: lowest prefix key each node sees through its window
@@ -122,8 +124,7 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
           const int idx = (tid + i * kThreads) * 4, r = idx / D, dd = idx % D;
-          float* dst = qs + r * (D + 1) + dd;
-          dst[0] = qv[i].x; dst[1] = qv[i].y; dst[2] = qv[i].z; dst[3] = qv[i].w;
+          *reinterpret_cast<float4*>(qs + r * D + (dd ^ ((r & 7) * 4))) = qv[i];
         }
       }
       const int my_row = rb + r_loc;
@@ -165,8 +166,7 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
 #pragma unroll
           for (int i = 0; i < kN; ++i) {
             const int idx = (tid + i * kThreads) * 4, key = idx / D, dd = idx % D;
-            float* kd = ks + key * (D + 1) + dd;
-            kd[0] = kr[i].x; kd[1] = kr[i].y; kd[2] = kr[i].z; kd[3] = kr[i].w;
+            *reinterpret_cast<float4*>(ks + key * D + (dd ^ (((key >> 2) & 7) * 4))) = kr[i];
             *reinterpret_cast<float4*>(vs + key * D + dd) = vr[i];
           }
           if (k0 + kKT < nkeys) fetch(k0 + kKT);
@@ -174,10 +174,17 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
           float sc[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) sc[k] = 0.f;
-          for (int dd = 0; dd < D; ++dd) {
-            const float qv = qs[r_loc * (D + 1) + dd];
+#pragma unroll 4
+          for (int dd = 0; dd < D; dd += 4) {
+            const float4 qv = *reinterpret_cast<const float4*>(qs + r_loc * D + (dd ^ ((r_loc & 7) * 4)));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sc[k] = fmaf(qv, ks[(kg * 4 + k) * (D + 1) + dd], sc[k]);
+            for (int k = 0; k < 4; ++k) {
+              const float4 kv = *reinterpret_cast<const float4*>(ks + (kg * 4 + k) * D + (dd ^ (kg * 4)));
+              sc[k] = fmaf(qv.x, kv.x, sc[k]);
+              sc[k] = fmaf(qv.y, kv.y, sc[k]);
+              sc[k] = fmaf(qv.z, kv.z, sc[k]);
+              sc[k] = fmaf(qv.w, kv.w, sc[k]);
+            }
           }
           float mx = -INFINITY;
 #pragma unroll
@@ -198,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float p = (sc[k] == -INFINITY) ? 0.f : exp2f(sc[k] - m_new);
-            ps[r_loc * (kKT + 1) + kg * 4 + k] = p;
+            ps[r_loc * (kKT + 4) + kg * 4 + k] = p;
             psum += p;
           }
           psum += __shfl_xor_sync(0xffffffffu, psum, 4);
@@ -209,10 +216,20 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < D / 8; ++k) o[k] *= alpha;
-          for (int j = 0; j < kKT; ++j) {
-            const float pj = ps[r_loc * (kKT + 1) + j];
+#pragma unroll 2
+          for (int j = 0; j < kKT; j += 4) {  // this thread's columns: 4 kg .. 4 kg + 3 of every 32
+            const float4 pv = *reinterpret_cast<const float4*>(ps + r_loc * (kKT + 4) + j);
+            const float pj[4] = {pv.x, pv.y, pv.z, pv.w};
 #pragma unroll
-            for (int k = 0; k < D / 8; ++k) o[k] = fmaf(pj, vs[j * D + kg + 8 * k], o[k]);
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k) {
+                const float4 v = *reinterpret_cast<const float4*>(vs + (j + e) * D + 32 * k + 4 * kg);
+                o[4 * k] = fmaf(pj[e], v.x, o[4 * k]);
+                o[4 * k + 1] = fmaf(pj[e], v.y, o[4 * k + 1]);
+                o[4 * k + 2] = fmaf(pj[e], v.z, o[4 * k + 2]);
+                o[4 * k + 3] = fmaf(pj[e], v.w, o[4 * k + 3]);
+              }
           }
         }
       }
@@ -224,10 +241,9 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
         const int RGP = padded_group_rows(pr.RG, pr.G);
         if (TVA_CHECK(pp < RGP, a.status)) {
 #pragma unroll
-          for (int k = 0; k < D / 8; ++k) {
-            const int c = kg + 8 * k;
-            a.o_part[o_part_offset(slot, pp, c >> 2, RGP, D) + (c & 3)] = o[k] * inv;
-          }
+          for (int k = 0; k < D / 32; ++k)
+            *reinterpret_cast<float4*>(a.o_part + o_part_offset(slot, pp, 8 * k + kg, RGP, D)) =
+                make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
           if (kg == 0) a.lse_part[(size_t)slot * RGP + pp] = m_run + log2f(l_run);
         }
       }

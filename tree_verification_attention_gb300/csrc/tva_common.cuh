@@ -190,6 +190,10 @@ __device__ __forceinline__ int seq_groups(const Problem& pr, int m) {
   return (m * pr.G + pr.RG - 1) / pr.RG;
 }
 
+// Batches from this size on are worth the running sums (three block barriers); at 8 sequences
+// they cost what they save.
+constexpr int kSumsFrom = 16;
+
 // Fills pr.unit_start / group_start (4 (B + 1) ints of `buf` hold the cu_* copies and the
 // sums) when they fit and the units can be counted in 32 bits.  Every thread of the block
 // must call it, after the cu_* copies are in place; it ends with a block barrier.
@@ -263,7 +267,7 @@ __device__ __forceinline__ void stage_cu(Problem& pr, int* buf, int cap) {
   if (fits) {
     pr.cu_prefix = buf;
     pr.cu_nodes = buf + pr.B + 1;
-    stage_sums(pr, buf, cap);
+    if (pr.B >= kSumsFrom) stage_sums(pr, buf, cap);
   }
 }
 
@@ -282,7 +286,7 @@ __device__ __forceinline__ void stage_problem(const Problem& src, Problem* dst, 
     __syncthreads();
     pr.cu_prefix = buf;
     pr.cu_nodes = buf + src.B + 1;
-    stage_sums(pr, buf, cap);
+    if (pr.B >= kSumsFrom) stage_sums(pr, buf, cap);
   }
   if (threadIdx.x == 0) *dst = pr;
   __syncthreads();
