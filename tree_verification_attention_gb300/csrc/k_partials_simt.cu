@@ -20,7 +20,8 @@ namespace {
 
 constexpr int kRB = 32;       // rows per block
 constexpr int kKT = 32;       // keys per sub-tile
-constexpr int kThreads = 256; // 8 threads per row: 4 keys each for QK, D/8 columns for PV
+constexpr int kRows = 2;      // rows per thread, kRB / kRows apart
+constexpr int kThreads = 128; // 8 threads per kRows rows: 4 keys each for QK, D/8 columns for PV
 
 template <typename T> __device__ __forceinline__ float to_f(T v);
 template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
@@ -47,8 +48,8 @@ constexpr size_t simt_smem_bytes() {
 template <typename T, int D, bool kWin>
 __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs a) {
   extern __shared__ float smem[];
-  // All shared-memory reads of the two products are 16 bytes wide (with single values they
-  // bound the kernel).  Chunk c (4 floats) of row r of qs is at c ^ (r mod 8), of key r of ks
+  // The products' shared-memory reads bound the kernel: they are 16 bytes wide, and a thread
+  // uses each K and V value for two rows.  Chunk c (4 floats) of row r of qs is at c ^ (r mod 8), of key r of ks
   // at c ^ (r / 4 mod 8): the rows that a warp reads together are then in different banks.
   float* qs = smem;                          // [kRB][D]
   float* ks = qs + kRB * D;                  // [kKT][D]
@@ -64,7 +65,7 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
   stage_cu(pr, cu_buf, 512);
   const T* __restrict__ q = static_cast<const T*>(a.q);
   const int tid = threadIdx.x;
-  const int r_loc = tid >> 3;  // row of this thread inside the block
+  const int r_loc = tid >> 3;  // first row of this thread inside the block
   const int kg = tid & 7;      // key group (QK) / column phase (PV)
   const int u = blockIdx.x;
   if (u == 0 && tid == 0) validate_sequences(pr, a.status);
@@ -127,13 +128,19 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
           *reinterpret_cast<float4*>(qs + r * D + (dd ^ ((r & 7) * 4))) = qv[i];
         }
       }
-      const int my_row = rb + r_loc;
-      const bool row_ok = my_row < row_end;
-      const int my_node = row_ok ? my_row / pr.G : 0;
-      float m_run = -INFINITY, l_run = 0.f;
-      float o[D / 8];
+      int my_row[kRows], my_node[kRows];
+      bool row_ok[kRows];
+      float m_run[kRows], l_run[kRows], o[kRows][D / 8];
 #pragma unroll
-      for (int k = 0; k < D / 8; ++k) o[k] = 0.f;
+      for (int x = 0; x < kRows; ++x) {
+        my_row[x] = rb + r_loc + x * (kRB / kRows);
+        row_ok[x] = my_row[x] < row_end;
+        my_node[x] = row_ok[x] ? my_row[x] / pr.G : 0;
+        m_run[x] = -INFINITY;
+        l_run[x] = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) o[x][k] = 0.f;
+      }
 
       for (int tile = tile0; tile < tile1; ++tile) {
         const bool is_tree = tile == 0;
@@ -141,7 +148,9 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
         const int nkeys = is_tree ? s.m
                           : kWin  ? tile_keys(pr, s, tile)
                                   : min(kKeyTile, s.P - (tile - 1) * kKeyTile);
-        const int low = kWin && !is_tree ? low_s[my_node] : 0;  // my_node < m
+        int low[kRows];
+#pragma unroll
+        for (int x = 0; x < kRows; ++x) low[x] = kWin && !is_tree ? low_s[my_node[x]] : 0;  // my_node < m
         const T* kb = static_cast<const T*>(is_tree ? a.tree_k : a.k_cache);
         const T* vb = static_cast<const T*>(is_tree ? a.tree_v : a.v_cache);
         const size_t first = is_tree ? (size_t)s.n0 : (size_t)s.p0 + (size_t)key0;
@@ -171,80 +180,102 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
           }
           if (k0 + kKT < nkeys) fetch(k0 + kKT);
           __syncthreads();
-          float sc[4];
+          float sc[kRows][4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sc[k] = 0.f;
-#pragma unroll 4
+          for (int x = 0; x < kRows; ++x)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc[x][k] = 0.f;
+#pragma unroll 2
           for (int dd = 0; dd < D; dd += 4) {
-            const float4 qv = *reinterpret_cast<const float4*>(qs + r_loc * D + (dd ^ ((r_loc & 7) * 4)));
+            float4 qv[kRows];
+#pragma unroll
+            for (int x = 0; x < kRows; ++x) {
+              const int r = r_loc + x * (kRB / kRows);
+              qv[x] = *reinterpret_cast<const float4*>(qs + r * D + (dd ^ ((r & 7) * 4)));
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float4 kv = *reinterpret_cast<const float4*>(ks + (kg * 4 + k) * D + (dd ^ (kg * 4)));
-              sc[k] = fmaf(qv.x, kv.x, sc[k]);
-              sc[k] = fmaf(qv.y, kv.y, sc[k]);
-              sc[k] = fmaf(qv.z, kv.z, sc[k]);
-              sc[k] = fmaf(qv.w, kv.w, sc[k]);
+#pragma unroll
+              for (int x = 0; x < kRows; ++x) {
+                sc[x][k] = fmaf(qv[x].x, kv.x, sc[x][k]);
+                sc[x][k] = fmaf(qv[x].y, kv.y, sc[x][k]);
+                sc[x][k] = fmaf(qv[x].z, kv.z, sc[x][k]);
+                sc[x][k] = fmaf(qv[x].w, kv.w, sc[x][k]);
+              }
             }
           }
-          float mx = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int key = k0 + kg * 4 + k;
-            bool vis = row_ok && key < nkeys;
-            if (kWin && !is_tree) vis = vis && (key0 + key >= low || key0 + key < pr.sinks);
-            if (is_tree && vis) vis = (masks[my_node * 4 + (key >> 5)] >> (key & 31)) & 1u;
-            sc[k] = vis ? sc[k] * a.scale_log2 : -INFINITY;
-            mx = fmaxf(mx, sc[k]);
-          }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          const float m_new = fmaxf(m_run, mx);
-          const float alpha = (m_new == -INFINITY) ? 1.f : exp2f(m_run - m_new);
-          float psum = 0.f;
+          for (int x = 0; x < kRows; ++x) {
+            float mx = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float p = (sc[k] == -INFINITY) ? 0.f : exp2f(sc[k] - m_new);
-            ps[r_loc * (kKT + 4) + kg * 4 + k] = p;
-            psum += p;
+            for (int k = 0; k < 4; ++k) {
+              const int key = k0 + kg * 4 + k;
+              bool vis = row_ok[x] && key < nkeys;
+              if (kWin && !is_tree) vis = vis && (key0 + key >= low[x] || key0 + key < pr.sinks);
+              if (is_tree && vis) vis = (masks[my_node[x] * 4 + (key >> 5)] >> (key & 31)) & 1u;
+              sc[x][k] = vis ? sc[x][k] * a.scale_log2 : -INFINITY;
+              mx = fmaxf(mx, sc[x][k]);
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            const float m_new = fmaxf(m_run[x], mx);
+            const float alpha = (m_new == -INFINITY) ? 1.f : exp2f(m_run[x] - m_new);
+            float psum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float p = (sc[x][k] == -INFINITY) ? 0.f : exp2f(sc[x][k] - m_new);
+              ps[(r_loc + x * (kRB / kRows)) * (kKT + 4) + kg * 4 + k] = p;
+              psum += p;
+            }
+            psum += __shfl_xor_sync(0xffffffffu, psum, 4);
+            psum += __shfl_xor_sync(0xffffffffu, psum, 2);
+            psum += __shfl_xor_sync(0xffffffffu, psum, 1);
+            l_run[x] = l_run[x] * alpha + psum;
+            m_run[x] = m_new;
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) o[x][k] *= alpha;
           }
-          psum += __shfl_xor_sync(0xffffffffu, psum, 4);
-          psum += __shfl_xor_sync(0xffffffffu, psum, 2);
-          psum += __shfl_xor_sync(0xffffffffu, psum, 1);
-          l_run = l_run * alpha + psum;
-          m_run = m_new;
           __syncwarp();
-#pragma unroll
-          for (int k = 0; k < D / 8; ++k) o[k] *= alpha;
 #pragma unroll 2
           for (int j = 0; j < kKT; j += 4) {  // this thread's columns: 4 kg .. 4 kg + 3 of every 32
-            const float4 pv = *reinterpret_cast<const float4*>(ps + r_loc * (kKT + 4) + j);
-            const float pj[4] = {pv.x, pv.y, pv.z, pv.w};
+            float pj[kRows][4];
+#pragma unroll
+            for (int x = 0; x < kRows; ++x) {
+              const float4 pv = *reinterpret_cast<const float4*>(ps + (r_loc + x * (kRB / kRows)) * (kKT + 4) + j);
+              pj[x][0] = pv.x; pj[x][1] = pv.y; pj[x][2] = pv.z; pj[x][3] = pv.w;
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
               for (int k = 0; k < D / 32; ++k) {
                 const float4 v = *reinterpret_cast<const float4*>(vs + (j + e) * D + 32 * k + 4 * kg);
-                o[4 * k] = fmaf(pj[e], v.x, o[4 * k]);
-                o[4 * k + 1] = fmaf(pj[e], v.y, o[4 * k + 1]);
-                o[4 * k + 2] = fmaf(pj[e], v.z, o[4 * k + 2]);
-                o[4 * k + 3] = fmaf(pj[e], v.w, o[4 * k + 3]);
+#pragma unroll
+                for (int x = 0; x < kRows; ++x) {
+                  o[x][4 * k] = fmaf(pj[x][e], v.x, o[x][4 * k]);
+                  o[x][4 * k + 1] = fmaf(pj[x][e], v.y, o[x][4 * k + 1]);
+                  o[x][4 * k + 2] = fmaf(pj[x][e], v.z, o[x][4 * k + 2]);
+                  o[x][4 * k + 3] = fmaf(pj[x][e], v.w, o[x][4 * k + 3]);
+                }
               }
           }
         }
       }
-      if (row_ok && slot_ok) {
+#pragma unroll
+      for (int x = 0; x < kRows; ++x) {
+        if (!row_ok[x] || !slot_ok) continue;
         // under a window a row may see no key of the segment: its partial is 0, log 0
-        const float inv = kWin && l_run == 0.f ? 0.f : 1.f / l_run;
-        const int rr = my_row - row_begin, MT = mtile_rows(pr.G);
+        const float inv = kWin && l_run[x] == 0.f ? 0.f : 1.f / l_run[x];
+        const int rr = my_row[x] - row_begin, MT = mtile_rows(pr.G);
         const int pp = rr / MT * 128 + rr % MT;  // padded row (see o_part_offset)
         const int RGP = padded_group_rows(pr.RG, pr.G);
         if (TVA_CHECK(pp < RGP, a.status)) {
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
             *reinterpret_cast<float4*>(a.o_part + o_part_offset(slot, pp, 8 * k + kg, RGP, D)) =
-                make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
-          if (kg == 0) a.lse_part[(size_t)slot * RGP + pp] = m_run + log2f(l_run);
+                make_float4(o[x][4 * k] * inv, o[x][4 * k + 1] * inv, o[x][4 * k + 2] * inv, o[x][4 * k + 3] * inv);
+          if (kg == 0) a.lse_part[(size_t)slot * RGP + pp] = m_run[x] + log2f(l_run[x]);
         }
       }
     }
