@@ -28,7 +28,7 @@
 // Every wait is bounded as in k_partials_tc.cu.
 #include <cuda.h>
 
-#include <atomic>
+#include <algorithm>
 #include <cstdio>
 
 #include "kv4.cuh"
@@ -73,6 +73,10 @@ struct Kv4Args {
   PartialArgs a;
   int W;    // M-tiles per row group (1 or 2)
   int npt;  // nodes per M-tile: floor(128 / G)
+  // What is fetched of an M-tile's nodes and of the tree tile's rows: no more than the
+  // largest tree has.  A TMA copy takes time for each row of its box, so full boxes would
+  // hold up the first tiles of small trees.
+  int q_nodes, tree_rows;
   uint64_t wait_ns;  // limit of every main-loop wait
   int stall;         // test hook: the MMA thread first waits on a barrier nothing completes
 };
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
       bool ok = true;
       long long t = t_begin;
       Segment S;
-      const uint32_t q_box_bytes = 64u * G * npt * 2u;
+      const uint32_t q_box_bytes = 64u * G * args.q_nodes * 2u;
       const uint64_t evict_first = policy_evict_first();  // records are read once
       while (ok && next_segment(pr, u, t, t_end, S, kShare)) {
         const Loc& L = S.L;
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
           if (trees > 0 && !warp_wait(TREE_EMPTY + (is_v ? 8 : 0), (trees - 1) & 1, abort_flag, wait_ns)) return false;
           int z = L.s.n0;
           if (!TVA_CHECK(z >= 0 && z < pr.node_capacity && L.s.m > 0, a.status)) z = 0;
-          mbar_expect_tx_elect(TREE_FULL + (is_v ? 8 : 0), C::kTileBytes);
+          mbar_expect_tx_elect(TREE_FULL + (is_v ? 8 : 0), (uint32_t)C::kHalves * 128u * args.tree_rows);
           for (int h = 0; h < C::kHalves; ++h)
             tma_load_3d_elect(kv_s + stage * C::kTileBytes + h * kHalfBytes, is_v ? &tm_tv : &tm_tk, 64 * h, L.g, z,
                               TREE_FULL + (is_v ? 8 : 0));
@@ -790,10 +794,11 @@ cudaError_t launch_typed(const PartialArgs& a, int W, int npt, cudaStream_t s) {
   auto kernel = partials_kv4_kernel<D, kBF16, kShare>;
   const Problem& pr = a.pr;
   CUtensorMap mq, mraw, mtk, mtv;
-  if (!make_map(&mq, type, a.q, D, pr.Hq, pr.node_capacity, pr.G, npt) ||
+  const int q_nodes = std::min(npt, pr.max_nodes), tree_rows = std::min(kKeyTile, (pr.max_nodes + 7) / 8 * 8);
+  if (!make_map(&mq, type, a.q, D, pr.Hq, pr.node_capacity, pr.G, q_nodes) ||
       !make_record_map(&mraw, pr.kv_capacity > 0 ? a.k_cache : a.tree_k, kv4_record_bytes(D), pr.Hkv, pr.kv_capacity) ||
-      !make_map(&mtk, type, a.tree_k, D, pr.Hkv, pr.node_capacity, 1, kKeyTile) ||
-      !make_map(&mtv, type, a.tree_v, D, pr.Hkv, pr.node_capacity, 1, kKeyTile))
+      !make_map(&mtk, type, a.tree_k, D, pr.Hkv, pr.node_capacity, 1, tree_rows) ||
+      !make_map(&mtv, type, a.tree_v, D, pr.Hkv, pr.node_capacity, 1, tree_rows))
     return cudaErrorInvalidValue;
   constexpr int smem = Cfg<D>::kSmemBytes;
   cudaError_t e = check_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
@@ -808,7 +813,7 @@ cudaError_t launch_typed(const PartialArgs& a, int W, int npt, cudaStream_t s) {
     record_error("launch partials_kv4_kernel", regs, "built with fewer registers than its warpgroups share");
     return cudaErrorInvalidConfiguration;
   }
-  Kv4Args ka{a, W, npt, 0, 0};
+  Kv4Args ka{a, W, npt, q_nodes, tree_rows, 0, 0};
   tc_wait_settings(&ka.wait_ns, &ka.stall);
   return check_cuda(launch_pdl(kernel, dim3(pr.U), dim3(kThreadsKv4), (size_t)smem, s, mq, mraw, mtk, mtv, ka),
                     "launch partials_kv4_kernel");

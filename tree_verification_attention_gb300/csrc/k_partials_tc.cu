@@ -39,6 +39,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdio>
 
@@ -73,6 +74,10 @@ struct TcArgs {
   PartialArgs a;
   int W;    // M-tiles per row group (1 or 2)
   int npt;  // nodes per M-tile: floor(128 / G)
+  // kWin: what is fetched of an M-tile's nodes and of the tree tile's rows, no more than the
+  // largest tree has (a TMA copy takes time for each row of its box; V rows beyond are
+  // zeroed, and the logits of K rows beyond masked).  Without a window, whole boxes.
+  int q_nodes, tree_rows;
   uint64_t wait_ns;  // limit of every main-loop wait
   int stall;         // test hook: the MMA thread first waits on a barrier nothing completes
 };
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       bool ok = true;
       long long t = t_begin;
       Segment S;
-      const uint32_t q_box_bytes = 64u * G * npt * 2u;
+      const uint32_t q_box_bytes = 64u * G * (kWin ? args.q_nodes : npt) * 2u;
       const uint64_t evict_first = policy_evict_first();  // K/V are read once
       while (ok && next_segment(pr, u, t, t_end, S, kShare)) {
         const Loc& L = S.L;
@@ -231,7 +236,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           if (!TVA_CHECK(z >= 0 && (tree ? z < pr.node_capacity && L.s.m > 0
                                          : z < L.s.p0 + L.s.len && z < pr.kv_capacity), a.status))
             z = 0;
-          mbar_expect_tx_elect(KV_FULL + 8 * stage, C::kTileBytes);
+          mbar_expect_tx_elect(KV_FULL + 8 * stage,
+                               kWin && tree ? (uint32_t)C::kHalves * 128u * args.tree_rows : (uint32_t)C::kTileBytes);
           for (int h = 0; h < C::kHalves; ++h)
             tma_load_3d_hint_elect(kv_s + stage * C::kTileBytes + h * kHalfBytes, m, 64 * h, L.g, z,
                              KV_FULL + 8 * stage, evict_first);
@@ -765,18 +771,20 @@ cudaError_t launch_tc_typed(const PartialArgs& a, int W, int npt, cudaStream_t s
   CUtensorMap mq, mk, mv, mtk, mtv;
   const void* kbase = pr.kv_capacity > 0 ? a.k_cache : a.tree_k;
   const void* vbase = pr.kv_capacity > 0 ? a.v_cache : a.tree_v;
-  if (!make_map(&mq, type, a.q, D, pr.Hq, pr.node_capacity, pr.G, npt) ||
+  const int q_nodes = kWin ? std::min(npt, pr.max_nodes) : npt;
+  const int tree_rows = kWin ? std::min(kKeyTile, (pr.max_nodes + 7) / 8 * 8) : kKeyTile;
+  if (!make_map(&mq, type, a.q, D, pr.Hq, pr.node_capacity, pr.G, q_nodes) ||
       !make_map(&mk, type, kbase, D, pr.Hkv, pr.kv_capacity, 1, kKeyTile) ||
       !make_map(&mv, type, vbase, D, pr.Hkv, pr.kv_capacity, 1, kKeyTile) ||
-      !make_map(&mtk, type, a.tree_k, D, pr.Hkv, pr.node_capacity, 1, kKeyTile) ||
-      !make_map(&mtv, type, a.tree_v, D, pr.Hkv, pr.node_capacity, 1, kKeyTile))
+      !make_map(&mtk, type, a.tree_k, D, pr.Hkv, pr.node_capacity, 1, tree_rows) ||
+      !make_map(&mtv, type, a.tree_v, D, pr.Hkv, pr.node_capacity, 1, tree_rows))
     return cudaErrorInvalidValue;
   constexpr int smem = Cfg<D>::kSmemBytes;
   cudaError_t e = check_cuda(cudaFuncSetAttribute(partials_tc_kernel<D, kBF16, kShare, kWin>,
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                              "cudaFuncSetAttribute(partials_tc_kernel)");
   if (e != cudaSuccess) return e;
-  TcArgs ta{a, W, npt, 0, 0};
+  TcArgs ta{a, W, npt, q_nodes, tree_rows, 0, 0};
   tc_wait_settings(&ta.wait_ns, &ta.stall);
   e = launch_pdl(partials_tc_kernel<D, kBF16, kShare, kWin>, dim3(pr.U), dim3(kThreadsTc), (size_t)smem, s, mq, mk, mv, mtk,
                  mtv, ta);

@@ -185,6 +185,12 @@ __device__ __forceinline__ void validate_sequences(const Problem& pr, int32_t* s
   }
 }
 
+// a / b for a >= 0, b > 0: in 32 bits where a fits (a 64-bit division takes a few hundred
+// clocks, and several stand between a launch and its first copy).
+__device__ __forceinline__ long long div_ll(long long a, int b) {
+  return a <= 0x7fffffffLL ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 __device__ __forceinline__ int seq_tiles(int P) { return (P + kKeyTile - 1) / kKeyTile + 1; }
 __device__ __forceinline__ int seq_groups(const Problem& pr, int m) {
   return (m * pr.G + pr.RG - 1) / pr.RG;
@@ -304,7 +310,7 @@ __device__ __forceinline__ long long total_units(const Problem& pr) {
 }
 
 __device__ __forceinline__ long long chunk_units(const Problem& pr, long long T) {
-  return (T + pr.U - 1) / pr.U;
+  return div_ll(T + pr.U - 1, pr.U);
 }
 
 // Where unit t lives.
@@ -335,10 +341,10 @@ __device__ __forceinline__ Loc locate_unit(const Problem& pr, long long t) {
     long long units = (long long)pr.Hkv * MP * tiles;
     if (t < acc + units) {
       long long local = t - acc;
-      int gi = (int)(local / tiles);
+      int gi = (int)div_ll(local, tiles);
       L.s = s; L.b = b; L.MP = MP; L.tiles = tiles;
       L.g = gi / MP; L.mp = gi % MP;
-      L.tile = (int)(local % tiles);
+      L.tile = (int)(local - (long long)gi * tiles);
       L.q = qacc + gi;
       L.start = acc + (long long)gi * tiles;
       return L;
@@ -396,7 +402,7 @@ __device__ __forceinline__ int share_teams(const Problem& pr) { return pr.U / pr
 __device__ __forceinline__ long long share_columns_per_team(const Problem& pr, int tiles) {
   const long long C = (long long)pr.Hkv * tiles;
   const int Q = share_teams(pr);
-  return (C + Q - 1) / Q;
+  return div_ll(C + Q - 1, Q);
 }
 
 // Worker u's walk positions [t0, t1).  `shared` is pr.share != 0; kernels that know it
@@ -444,7 +450,7 @@ __device__ __forceinline__ bool next_segment(const Problem& pr, int u, long long
     L.b = 0;
     L.MP = seq_groups(pr, L.s.m);
     L.tiles = seq_tiles(L.s.P);
-    L.g = (int)(t / L.tiles);
+    L.g = (int)div_ll(t, L.tiles);
     L.mp = u % pr.share;
     L.tile = (int)(t - (long long)L.g * L.tiles);
     L.q = L.g * L.MP + L.mp;
