@@ -48,7 +48,7 @@ bool check(int P, const std::vector<int>& parent, int window, int sinks) {
   ++g_problems;
   const int m = (int)parent.size();
   const int32_t cu_p[3] = {0, 5, 5 + P}, cu_n[3] = {0, 2, 2 + m};  // the second of two sequences
-  tva::Problem pr{};
+  tva::WinProblem pr{};
   pr.cu_prefix = cu_p;
   pr.cu_nodes = cu_n;
   pr.B = 2;
@@ -109,7 +109,7 @@ bool check(int P, const std::vector<int>& parent, int window, int sinks) {
   if (covered != tva::total_units(pr)) return fail("units covered", covered, tva::total_units(pr));
   // the same walk with the staged running sums
   int buf[16];
-  tva::Problem sums = pr;
+  tva::WinProblem sums = pr;
   tva::stage_sums(sums, buf, 16);
   if (sums.unit_start == nullptr) return fail("no sums", 0, 0);
   if (tva::total_units(sums) != tva::total_units(pr)) return fail("total", tva::total_units(sums), 0);

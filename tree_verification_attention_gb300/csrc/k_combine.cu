@@ -140,11 +140,11 @@ __device__ __forceinline__ void merge_rows(const Problem& pr, const float* o_par
 
 constexpr int kCuCap = 2048;      // ints of shared memory for the staged cu_* arrays
 
-template <typename T, int D, int CG, int NB, int WPB>
-__global__ void __launch_bounds__(32 * WPB) combine_kernel(CombineArgs a) {
+template <typename T, int D, int CG, int NB, int WPB, class PR>
+__global__ void __launch_bounds__(32 * WPB) combine_kernel(CombineArgsOf<PR> a) {
   constexpr int NCG = D / 4 / CG;  // column-group sets per row block
   __shared__ int cu_buf[kCuCap];
-  Problem pr = a.pr;
+  PR pr = a.pr;
   stage_cu(pr, cu_buf, kCuCap);  // block-wide; reads caller inputs only
   const int lane = threadIdx.x & 31;
   const int MT = mtile_rows(pr.G);
@@ -215,8 +215,8 @@ int sm_count(int* dev_out) {
 // item per warp; when the items fill less than one wave of blocks, the grid is widened
 // to a full wave (never past one block per item) and the round-robin deal spreads the
 // items evenly over it.
-template <typename T, int D, int CG, int NB>
-cudaError_t launch_typed(const CombineArgs& a, cudaStream_t s) {
+template <typename T, int D, int CG, int NB, class PR>
+cudaError_t launch_typed(const CombineArgsOf<PR>& a, cudaStream_t s) {
   constexpr int WPB = CG == 1 ? 8 : 4;
   const int RGP = padded_group_rows(a.pr.RG, a.pr.G);
   const long long warps = max_row_groups(a.pr) * (RGP / 32) * (D / 4 / CG);
@@ -226,7 +226,7 @@ cudaError_t launch_typed(const CombineArgs& a, cudaStream_t s) {
   int resident = sms > 0 ? per_sm[dev].load(std::memory_order_relaxed) : 0;
   if (sms > 0 && resident == 0) {
     int v = 0;
-    resident = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, combine_kernel<T, D, CG, NB, WPB>, 32 * WPB, 0) ==
+    resident = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, combine_kernel<T, D, CG, NB, WPB, PR>, 32 * WPB, 0) ==
                            cudaSuccess && v > 0 ? v : 1;
     per_sm[dev].store(resident, std::memory_order_relaxed);
   }
@@ -234,7 +234,7 @@ cudaError_t launch_typed(const CombineArgs& a, cudaStream_t s) {
   long long blocks = (warps + WPB - 1) / WPB;
   if (blocks < wave) blocks = std::min<long long>(wave, warps);
   if (blocks <= 0) return cudaSuccess;
-  return check_cuda(launch_pdl(combine_kernel<T, D, CG, NB, WPB>, dim3((unsigned)blocks), dim3(32 * WPB), 0,
+  return check_cuda(launch_pdl(combine_kernel<T, D, CG, NB, WPB, PR>, dim3((unsigned)blocks), dim3(32 * WPB), 0,
                                s, a),
                     "launch combine_kernel");
 }
@@ -243,7 +243,8 @@ cudaError_t launch_typed(const CombineArgs& a, cudaStream_t s) {
 // of one row group (prefix tiles + the tree tile) spread over ceil(tiles / chunk) + 1
 // workers at most (stream-K), or over the teams that cover its KV head (shared mode).  Smaller sequences shrink the chunk and can raise the count; the
 // kernel loops over any number, this only sizes its first round of loads.
-int expected_partials(const Problem& pr) {
+template <class PR>
+int expected_partials(const PR& pr) {
   const long long tiles = (walk_prefix_bound(pr) + kKeyTile - 1) / kKeyTile + 1;
   if (pr.share == 0 && pr.align > 0) return (int)std::min<long long>(pr.align, tiles);
   if (pr.share > 0) {  // a head's columns spread over ceil(tiles / columns per team) + 1 teams
@@ -256,25 +257,29 @@ int expected_partials(const Problem& pr) {
   return (int)((tiles + c - 1) / c + 1);
 }
 
-template <typename T, int D>
-cudaError_t launch_d(const CombineArgs& a, cudaStream_t s) {
+template <typename T, int D, class PR>
+cudaError_t launch_d(const CombineArgsOf<PR>& a, cudaStream_t s) {
   const int np = expected_partials(a.pr);
   if (np <= 6) return launch_typed<T, D, 4, 6>(a, s);
   if (np <= 12) return launch_typed<T, D, 2, 12>(a, s);
   return launch_typed<T, D, 2, 20>(a, s);
 }
 
-template <typename T>
-cudaError_t launch_dtype(const CombineArgs& a, cudaStream_t s) {
+template <typename T, class PR>
+cudaError_t launch_dtype(const CombineArgsOf<PR>& a, cudaStream_t s) {
   return a.pr.d == 64 ? launch_d<T, 64>(a, s) : launch_d<T, 128>(a, s);
 }
 
-}  // namespace
-
-cudaError_t launch_combine(const CombineArgs& a, int dtype, cudaStream_t s) {
+template <class PR>
+cudaError_t launch_any(const CombineArgsOf<PR>& a, int dtype, cudaStream_t s) {
   if (dtype == 1) return launch_dtype<float>(a, s);
   if (dtype == 2) return launch_dtype<__half>(a, s);
   return launch_dtype<__nv_bfloat16>(a, s);
 }
+
+}  // namespace
+
+cudaError_t launch_combine(const CombineArgs& a, int dtype, cudaStream_t s) { return launch_any(a, dtype, s); }
+cudaError_t launch_combine(const WinCombineArgs& a, int dtype, cudaStream_t s) { return launch_any(a, dtype, s); }
 
 }  // namespace tva

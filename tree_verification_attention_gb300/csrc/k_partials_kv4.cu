@@ -70,7 +70,7 @@ struct Cfg {
 };
 
 struct Kv4Args {
-  PartialArgs a;
+  WinPartialArgs a;
   int W;    // M-tiles per row group (1 or 2)
   int npt;  // nodes per M-tile: floor(128 / G)
   // What is fetched of an M-tile's nodes and of the tree tile's rows: no more than the
@@ -204,10 +204,10 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const PartialArgs& a = args.a;
-  Problem* pr_s = reinterpret_cast<Problem*>(smem + C::kBarOff + C::kCuOff - 128);
-  static_assert(sizeof(Problem) <= 128, "staged problem");
-  const Problem& pr = *pr_s;
+  const WinPartialArgs& a = args.a;
+  WinProblem* pr_s = reinterpret_cast<WinProblem*>(smem + C::kBarOff + C::kCuOff - 128);
+  static_assert(sizeof(WinProblem) <= 128, "staged problem");
+  const WinProblem& pr = *pr_s;
   const int W = args.W, npt = args.npt, G = a.pr.G;  // kernel parameters: readable before staging
   const uint64_t wait_ns = args.wait_ns;  // main-loop waits; drains use kDrainNs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -789,10 +789,10 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
 }
 
 template <int D, bool kBF16, bool kShare>
-cudaError_t launch_typed(const PartialArgs& a, int W, int npt, cudaStream_t s) {
+cudaError_t launch_typed(const WinPartialArgs& a, int W, int npt, cudaStream_t s) {
   constexpr CUtensorMapDataType type = kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   auto kernel = partials_kv4_kernel<D, kBF16, kShare>;
-  const Problem& pr = a.pr;
+  const WinProblem& pr = a.pr;
   CUtensorMap mq, mraw, mtk, mtv;
   const int q_nodes = std::min(npt, pr.max_nodes), tree_rows = std::min(kKeyTile, (pr.max_nodes + 7) / 8 * 8);
   if (!make_map(&mq, type, a.q, D, pr.Hq, pr.node_capacity, pr.G, q_nodes) ||
@@ -820,14 +820,14 @@ cudaError_t launch_typed(const PartialArgs& a, int W, int npt, cudaStream_t s) {
 }
 
 template <bool kShare>
-cudaError_t launch_mode(const PartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
+cudaError_t launch_mode(const WinPartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
   if (bf16) return a.pr.d == 64 ? launch_typed<64, true, kShare>(a, W, npt, s) : launch_typed<128, true, kShare>(a, W, npt, s);
   return a.pr.d == 64 ? launch_typed<64, false, kShare>(a, W, npt, s) : launch_typed<128, false, kShare>(a, W, npt, s);
 }
 
 }  // namespace
 
-cudaError_t launch_partials_kv4(const PartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
+cudaError_t launch_partials_kv4(const WinPartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
   return a.pr.share != 0 ? launch_mode<true>(a, bf16, W, npt, s) : launch_mode<false>(a, bf16, W, npt, s);
 }
 

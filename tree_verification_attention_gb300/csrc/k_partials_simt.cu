@@ -13,6 +13,8 @@
 //
 // This path carries the float32 dtype (head_dim 64 or 128).  bfloat16 inputs go to
 // the tensor-core kernel.
+#include <type_traits>
+
 #include "tva_internal.h"
 
 namespace tva {
@@ -46,7 +48,7 @@ constexpr size_t simt_smem_bytes() {
 }
 
 template <typename T, int D, bool kWin>
-__global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgsOf<std::conditional_t<kWin, WinProblem, Problem>> a) {
   extern __shared__ float smem[];
   // The products' shared-memory reads bound the kernel: they are 16 bytes wide, and a thread
   // uses each K and V value for two rows.  Chunk c (4 floats) of row r of qs is at c ^ (r mod 8), of key r of ks
@@ -61,7 +63,7 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
   __shared__ int low_s[kWin ? kMaxNodes : 1];  // kWin: lowest prefix key each node sees through its window
 
   __shared__ int cu_buf[512];
-  Problem pr = a.pr;
+  auto pr = a.pr;
   stage_cu(pr, cu_buf, 512);
   const T* __restrict__ q = static_cast<const T*>(a.q);
   const int tid = threadIdx.x;
@@ -144,10 +146,14 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
 
       for (int tile = tile0; tile < tile1; ++tile) {
         const bool is_tree = tile == 0;
-        const int key0 = kWin && !is_tree ? tile_key0(s, tile) : (tile - 1) * kKeyTile;
-        const int nkeys = is_tree ? s.m
-                          : kWin  ? tile_keys(pr, s, tile)
-                                  : min(kKeyTile, s.P - (tile - 1) * kKeyTile);
+        int key0 = (tile - 1) * kKeyTile, nkeys = is_tree ? s.m : min(kKeyTile, s.P - key0), sinks = 0;
+        if constexpr (kWin) {
+          sinks = pr.sinks;
+          if (!is_tree) {
+            key0 = tile_key0(s, tile);
+            nkeys = tile_keys(pr, s, tile);
+          }
+        }
         int low[kRows];
 #pragma unroll
         for (int x = 0; x < kRows; ++x) low[x] = kWin && !is_tree ? low_s[my_node[x]] : 0;  // my_node < m
@@ -212,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
             for (int k = 0; k < 4; ++k) {
               const int key = k0 + kg * 4 + k;
               bool vis = row_ok[x] && key < nkeys;
-              if (kWin && !is_tree) vis = vis && (key0 + key >= low[x] || key0 + key < pr.sinks);
+              if (kWin && !is_tree) vis = vis && (key0 + key >= low[x] || key0 + key < sinks);
               if (is_tree && vis) vis = (masks[my_node[x] * 4 + (key >> 5)] >> (key & 31)) & 1u;
               sc[x][k] = vis ? sc[x][k] * a.scale_log2 : -INFINITY;
               mx = fmaxf(mx, sc[x][k]);
@@ -283,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgs 
 }
 
 template <typename T, int D, bool kWin>
-cudaError_t launch_simt_typed(const PartialArgs& a, cudaStream_t s) {
+cudaError_t launch_simt_typed(const PartialArgsOf<std::conditional_t<kWin, WinProblem, Problem>>& a, cudaStream_t s) {
   constexpr size_t smem = simt_smem_bytes<D>();
   cudaError_t e = check_cuda(cudaFuncSetAttribute(partials_simt_kernel<T, D, kWin>,
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
@@ -302,9 +308,15 @@ cudaError_t launch_partials_simt(const PartialArgs& a, int dtype, cudaStream_t s
     record_error("launch_partials_simt", 0, "float32 only");
     return cudaErrorInvalidValue;
   }
-  if (a.pr.window > 0)
-    return a.pr.d == 64 ? launch_simt_typed<float, 64, true>(a, s) : launch_simt_typed<float, 128, true>(a, s);
   return a.pr.d == 64 ? launch_simt_typed<float, 64, false>(a, s) : launch_simt_typed<float, 128, false>(a, s);
+}
+
+cudaError_t launch_partials_simt(const WinPartialArgs& a, int dtype, cudaStream_t s) {
+  if (dtype != 1) {
+    record_error("launch_partials_simt", 0, "float32 only");
+    return cudaErrorInvalidValue;
+  }
+  return a.pr.d == 64 ? launch_simt_typed<float, 64, true>(a, s) : launch_simt_typed<float, 128, true>(a, s);
 }
 
 }  // namespace tva

@@ -42,6 +42,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdio>
+#include <type_traits>
 
 #include "tc_pipeline.cuh"
 #include "tc_ptx.cuh"
@@ -70,8 +71,13 @@ struct Cfg {
   static constexpr int kSmemBytes = kBarOff + kMiscBytes + 1024;  // + alignment slack
 };
 
+// The windowed kernels' problem, and the plain ones'.
+template <bool kWin>
+using ProblemOf = std::conditional_t<kWin, WinProblem, Problem>;
+
+template <bool kWin>
 struct TcArgs {
-  PartialArgs a;
+  PartialArgsOf<ProblemOf<kWin>> a;
   int W;    // M-tiles per row group (1 or 2)
   int npt;  // nodes per M-tile: floor(128 / G)
   // kWin: what is fetched of an M-tile's nodes and of the tree tile's rows, no more than the
@@ -99,14 +105,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                        const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ CUtensorMap tm_tk,
-                       const __grid_constant__ CUtensorMap tm_tv, const TcArgs args) {
+                       const __grid_constant__ CUtensorMap tm_tv, const TcArgs<kWin> args) {
   using C = Cfg<D>;
+  using PR = ProblemOf<kWin>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  const PartialArgs& a = args.a;
-  Problem* pr_s = reinterpret_cast<Problem*>(smem + C::kBarOff + C::kCuOff - 128);
-  const Problem& pr = *pr_s;
+  const PartialArgsOf<PR>& a = args.a;
+  PR* pr_s = reinterpret_cast<PR*>(smem + C::kBarOff + C::kCuOff - 128);
+  static_assert(sizeof(PR) <= 128, "staged problem");
+  const PR& pr = *pr_s;
   const int W = args.W, npt = args.npt, G = a.pr.G;  // kernel parameters: readable before staging
   const uint64_t wait_ns = args.wait_ns;  // main-loop waits; drains use kDrainNs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -453,10 +461,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (!ok) break;
         tc_fence_after();
         // keys of this tile: [0, lim) exist; the tree tile also needs the ancestor bit
-        const int key0 = kWin && !is_tree ? tile_key0(L.s, tile) : 0;
-        const int lim = is_tree ? L.s.m
-                        : kWin  ? tile_keys(pr, L.s, tile)
-                                : min(kKeyTile, L.s.P - (tile - 1) * kKeyTile);
+        int lim = is_tree ? L.s.m : min(kKeyTile, L.s.P - (tile - 1) * kKeyTile);
+        int key0 = 0;        // kWin: the tile's first key
+        bool cut = false;    // kWin: some row may not see some of its keys
+        if constexpr (kWin) {
+          if (!is_tree) {
+            key0 = tile_key0(L.s, tile);
+            lim = tile_keys(pr, L.s, tile);
+            cut = window_cuts(pr, L.s, key0, lim);
+          }
+        }
         if constexpr (kWin) {
           // Rows of V past the keys that exist, or that no node sees, may hold anything (an
           // evicted or unwritten cache row: infinities, NaN), and a weight of zero would
@@ -479,7 +493,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             fence_async_shared();  // the MMA reads V through the asynchronous proxy
           }
         }
-        if (is_tree || lim < kKeyTile || (kWin && window_cuts(pr, L.s, key0, lim))) {
+        if (is_tree || lim < kKeyTile || cut) {
           // Rare tiles (the last, partial prefix tile; the tree tile): rewrite the logits
           // the row does not see to -inf in TMEM, 32 columns at a time, so the two
           // passes below carry no masking code.
@@ -765,9 +779,9 @@ void tc_wait_settings(uint64_t* wait_ns, int* stall) {
 namespace {
 
 template <int D, bool kBF16, bool kShare, bool kWin>
-cudaError_t launch_tc_typed(const PartialArgs& a, int W, int npt, cudaStream_t s) {
+cudaError_t launch_tc_typed(const PartialArgsOf<ProblemOf<kWin>>& a, int W, int npt, cudaStream_t s) {
   constexpr CUtensorMapDataType type = kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const Problem& pr = a.pr;
+  const ProblemOf<kWin>& pr = a.pr;
   CUtensorMap mq, mk, mv, mtk, mtv;
   const void* kbase = pr.kv_capacity > 0 ? a.k_cache : a.tree_k;
   const void* vbase = pr.kv_capacity > 0 ? a.v_cache : a.tree_v;
@@ -784,7 +798,7 @@ cudaError_t launch_tc_typed(const PartialArgs& a, int W, int npt, cudaStream_t s
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                              "cudaFuncSetAttribute(partials_tc_kernel)");
   if (e != cudaSuccess) return e;
-  TcArgs ta{a, W, npt, q_nodes, tree_rows, 0, 0};
+  TcArgs<kWin> ta{a, W, npt, q_nodes, tree_rows, 0, 0};
   tc_wait_settings(&ta.wait_ns, &ta.stall);
   e = launch_pdl(partials_tc_kernel<D, kBF16, kShare, kWin>, dim3(pr.U), dim3(kThreadsTc), (size_t)smem, s, mq, mk, mv, mtk,
                  mtv, ta);
@@ -807,7 +821,7 @@ void set_tc_wait_limit(unsigned long long ns, int stall) {
 }
 
 template <bool kShare, bool kWin>
-cudaError_t launch_tc_mode(const PartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
+cudaError_t launch_tc_mode(const PartialArgsOf<ProblemOf<kWin>>& a, bool bf16, int W, int npt, cudaStream_t s) {
   if (bf16)
     return a.pr.d == 64 ? launch_tc_typed<64, true, kShare, kWin>(a, W, npt, s)
                         : launch_tc_typed<128, true, kShare, kWin>(a, W, npt, s);
@@ -816,9 +830,11 @@ cudaError_t launch_tc_mode(const PartialArgs& a, bool bf16, int W, int npt, cuda
 }
 
 cudaError_t launch_partials_tc(const PartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
-  if (a.pr.window > 0)
-    return a.pr.share != 0 ? launch_tc_mode<true, true>(a, bf16, W, npt, s) : launch_tc_mode<false, true>(a, bf16, W, npt, s);
   return a.pr.share != 0 ? launch_tc_mode<true, false>(a, bf16, W, npt, s) : launch_tc_mode<false, false>(a, bf16, W, npt, s);
+}
+
+cudaError_t launch_partials_tc(const WinPartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
+  return a.pr.share != 0 ? launch_tc_mode<true, true>(a, bf16, W, npt, s) : launch_tc_mode<false, true>(a, bf16, W, npt, s);
 }
 
 }  // namespace tva

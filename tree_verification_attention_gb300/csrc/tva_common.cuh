@@ -63,6 +63,14 @@ struct Problem {
   // range crosses into another row group (stream-K ranges do, and such a worker pays a
   // second segment - epilogue, Q copy, tree tile - in the middle of its stream).
   int align;
+  static constexpr bool kWindowed = false;
+};
+
+// The problem of the windowed and the 4-bit-cache forms.  The schedule below is written for
+// both; the plain forms' kernels are compiled without what only these need (with it they
+// lost 2 to 14 % - most of it instruction fetches at the start of a launch).
+struct WinProblem : Problem {
+  static constexpr bool kWindowed = true;
   // 0: every node sees the whole prefix.  W >= 1: a node at position t (the prefix length
   // plus its number of proper ancestors) sees the key at position s when t - s < W or
   // s < sinks; the walk then covers only the prefix keys that some node sees (SeqInfo).
@@ -106,7 +114,8 @@ __device__ __forceinline__ bool checked_ok(bool cond, int32_t* st) {
 #define TVA_CHECK(cond, st) (true)
 #endif
 
-__device__ __forceinline__ SeqInfo seq_info(const Problem& pr, int b) {
+template <class PR>
+__device__ __forceinline__ SeqInfo seq_info(const PR& pr, int b) {
   SeqInfo s;
   if (pr.cu_prefix == nullptr) {
     s.p0 = 0; s.P = pr.single_prefix; s.n0 = 0; s.m = pr.single_nodes;
@@ -122,13 +131,15 @@ __device__ __forceinline__ SeqInfo seq_info(const Problem& pr, int b) {
   if (!s.ok) { s.P = 0; s.m = 0; }
   s.len = s.P;
   s.ns = s.w0 = 0;
-  if (pr.window > 0) {
-    const int lo = s.P > pr.window - 1 ? s.P - (pr.window - 1) : 0;
-    const int sk = pr.sinks < s.P ? pr.sinks : s.P;
-    if (lo > sk) {
-      s.ns = (sk + kKeyTile - 1) / kKeyTile;
-      s.w0 = lo;
-      s.P = s.ns * kKeyTile + (s.len - lo);
+  if constexpr (PR::kWindowed) {
+    if (pr.window > 0) {
+      const int lo = s.P > pr.window - 1 ? s.P - (pr.window - 1) : 0;
+      const int sk = pr.sinks < s.P ? pr.sinks : s.P;
+      if (lo > sk) {
+        s.ns = (sk + kKeyTile - 1) / kKeyTile;
+        s.w0 = lo;
+        s.P = s.ns * kKeyTile + (s.len - lo);
+      }
     }
   }
   return s;
@@ -140,20 +151,20 @@ __device__ __forceinline__ int tile_key0(const SeqInfo& s, int tile) {
   const int k = tile - 1;
   return k < s.ns ? k * kKeyTile : s.w0 + (k - s.ns) * kKeyTile;
 }
-__device__ __forceinline__ int tile_keys(const Problem& pr, const SeqInfo& s, int tile) {
+__device__ __forceinline__ int tile_keys(const WinProblem& pr, const SeqInfo& s, int tile) {
   const int end = tile - 1 < s.ns ? (pr.sinks < s.len ? pr.sinks : s.len) : s.len;
   const int n = end - tile_key0(s, tile);
   return n < kKeyTile ? n : kKeyTile;
 }
 // The lowest prefix key that a node `depth` levels below the roots sees through the window
 // (it sees every key from there on, and the sinks).
-__device__ __forceinline__ int window_low(const Problem& pr, const SeqInfo& s, int depth) {
+__device__ __forceinline__ int window_low(const WinProblem& pr, const SeqInfo& s, int depth) {
   const int low = s.len + depth - (pr.window - 1);
   return low > 0 ? low : 0;
 }
 // Whether some row may not see some of the tile's keys: they start below the deepest
 // possible node's window (depth <= m - 1) and are not all sinks.
-__device__ __forceinline__ bool window_cuts(const Problem& pr, const SeqInfo& s, int key0, int keys) {
+__device__ __forceinline__ bool window_cuts(const WinProblem& pr, const SeqInfo& s, int key0, int keys) {
   return key0 < window_low(pr, s, s.m - 1) && key0 + keys > pr.sinks;
 }
 // Bits first .. 31 (all when first <= 0) and bits 0 .. count - 1 of a 32-key mask word.
@@ -167,7 +178,8 @@ __device__ __forceinline__ uint32_t window_bits(int c0, int keys, int low, int s
   return bits_below(keys) & (bits_from(low - c0) | bits_below(sinks - c0));
 }
 // The longest walk of a sequence within the stated bound (sizes launches only).
-__host__ __device__ __forceinline__ long long walk_prefix_bound(const Problem& pr) {
+__host__ __device__ __forceinline__ long long walk_prefix_bound(const Problem& pr) { return pr.max_prefix; }
+__host__ __device__ __forceinline__ long long walk_prefix_bound(const WinProblem& pr) {
   if (pr.window <= 0) return pr.max_prefix;
   const long long a = (long long)pr.max_prefix + kKeyTile - 1;
   const long long b = ((long long)pr.sinks + kKeyTile - 1) / kKeyTile * kKeyTile + pr.window - 1;
@@ -176,7 +188,8 @@ __host__ __device__ __forceinline__ long long walk_prefix_bound(const Problem& p
 
 // Reports (once, from one thread) a cu_* entry outside the stated bounds.  The
 // offending sequence is treated as empty by every kernel.
-__device__ __forceinline__ void validate_sequences(const Problem& pr, int32_t* status) {
+template <class PR>
+__device__ __forceinline__ void validate_sequences(const PR& pr, int32_t* status) {
   for (int b = 0; b < pr.B; ++b) {
     if (!seq_info(pr, b).ok) {
       set_status(status, kStatusInvalidArg);
@@ -203,7 +216,7 @@ constexpr int kSumsFrom = 16;
 // Fills pr.unit_start / group_start (4 (B + 1) ints of `buf` hold the cu_* copies and the
 // sums) when they fit and the units can be counted in 32 bits.  Every thread of the block
 // must call it, after the cu_* copies are in place; it ends with a block barrier.
-__device__ __forceinline__ void stage_sums(Problem& pr, int* buf, int cap) {
+__device__ __forceinline__ void stage_sums(WinProblem& pr, int* buf, int cap) {
   constexpr int kOwn = 4;  // entries per thread
   const int n = pr.B + 1;
   if (4 * n > cap || n > kOwn * (int)blockDim.x) return;  // uniform over the block
@@ -261,7 +274,8 @@ __device__ __forceinline__ int find_sequence(const int32_t* start, int n, long l
 // fit in `cap` ints, and points `pr` at the copies, so that the sequence walks below
 // cost shared-memory loads instead of one round of global loads per sequence.  Every
 // thread of the block must call it; it ends with a block barrier.
-__device__ __forceinline__ void stage_cu(Problem& pr, int* buf, int cap) {
+template <class PR>
+__device__ __forceinline__ void stage_cu(PR& pr, int* buf, int cap) {
   const bool fits = pr.cu_prefix != nullptr && 2 * (pr.B + 1) <= cap;
   if (fits) {
     for (int i = threadIdx.x; i <= pr.B; i += blockDim.x) {
@@ -273,13 +287,16 @@ __device__ __forceinline__ void stage_cu(Problem& pr, int* buf, int cap) {
   if (fits) {
     pr.cu_prefix = buf;
     pr.cu_nodes = buf + pr.B + 1;
-    if (pr.B >= kSumsFrom) stage_sums(pr, buf, cap);
+    if constexpr (PR::kWindowed) {
+      if (pr.B >= kSumsFrom) stage_sums(pr, buf, cap);
+    }
   }
 }
 
 // Same, but the resulting problem description is also placed in shared memory (`dst`),
 // so that kernels short of registers can read its fields from there.
-__device__ __forceinline__ void stage_problem(const Problem& src, Problem* dst, int* buf, int cap) {
+template <class PR>
+__device__ __forceinline__ void stage_problem(const PR& src, PR* dst, int* buf, int cap) {
   const bool fits = src.cu_prefix != nullptr && 2 * (src.B + 1) <= cap;
   if (fits) {
     for (int i = threadIdx.x; i <= src.B; i += blockDim.x) {
@@ -287,20 +304,31 @@ __device__ __forceinline__ void stage_problem(const Problem& src, Problem* dst, 
       buf[src.B + 1 + i] = __ldg(src.cu_nodes + i);
     }
   }
-  Problem pr = src;
-  if (fits) {
-    __syncthreads();
-    pr.cu_prefix = buf;
-    pr.cu_nodes = buf + src.B + 1;
-    if (pr.B >= kSumsFrom) stage_sums(pr, buf, cap);
+  if constexpr (PR::kWindowed) {
+    PR pr = src;
+    if (fits) {
+      __syncthreads();
+      pr.cu_prefix = buf;
+      pr.cu_nodes = buf + src.B + 1;
+      if (pr.B >= kSumsFrom) stage_sums(pr, buf, cap);
+    }
+    if (threadIdx.x == 0) *dst = pr;
+  } else if (threadIdx.x == 0) {
+    *dst = src;
+    if (fits) {
+      dst->cu_prefix = buf;
+      dst->cu_nodes = buf + src.B + 1;
+    }
   }
-  if (threadIdx.x == 0) *dst = pr;
   __syncthreads();
 }
 
 // Total units T and the chunk size c = ceil(T / U).
-__device__ __forceinline__ long long total_units(const Problem& pr) {
-  if (pr.unit_start != nullptr) return pr.unit_start[pr.B];
+template <class PR>
+__device__ __forceinline__ long long total_units(const PR& pr) {
+  if constexpr (PR::kWindowed) {
+    if (pr.unit_start != nullptr) return pr.unit_start[pr.B];
+  }
   long long T = 0;
   for (int b = 0; b < pr.B; ++b) {
     SeqInfo s = seq_info(pr, b);
@@ -309,8 +337,10 @@ __device__ __forceinline__ long long total_units(const Problem& pr) {
   return T;
 }
 
-__device__ __forceinline__ long long chunk_units(const Problem& pr, long long T) {
-  return div_ll(T + pr.U - 1, pr.U);
+template <class PR>
+__device__ __forceinline__ long long chunk_units(const PR& pr, long long T) {
+  if constexpr (PR::kWindowed) return div_ll(T + pr.U - 1, pr.U);
+  return (T + pr.U - 1) / pr.U;
 }
 
 // Where unit t lives.
@@ -325,14 +355,17 @@ struct Loc {
   long long start;    // global index of the row group's first unit
 };
 
-__device__ __forceinline__ Loc locate_unit(const Problem& pr, long long t) {
+template <class PR>
+__device__ __forceinline__ Loc locate_unit(const PR& pr, long long t) {
   Loc L;
   long long acc = 0;
   int qacc = 0, b = 0;
-  if (pr.unit_start != nullptr) {
-    b = find_sequence(pr.unit_start, pr.B, t);
-    acc = pr.unit_start[b];
-    qacc = pr.group_start[b];
+  if constexpr (PR::kWindowed) {
+    if (pr.unit_start != nullptr) {
+      b = find_sequence(pr.unit_start, pr.B, t);
+      acc = pr.unit_start[b];
+      qacc = pr.group_start[b];
+    }
   }
   for (; b < pr.B; ++b) {
     SeqInfo s = seq_info(pr, b);
@@ -341,7 +374,7 @@ __device__ __forceinline__ Loc locate_unit(const Problem& pr, long long t) {
     long long units = (long long)pr.Hkv * MP * tiles;
     if (t < acc + units) {
       long long local = t - acc;
-      int gi = (int)div_ll(local, tiles);
+      int gi = PR::kWindowed ? (int)div_ll(local, tiles) : (int)(local / tiles);
       L.s = s; L.b = b; L.MP = MP; L.tiles = tiles;
       L.g = gi / MP; L.mp = gi % MP;
       L.tile = (int)(local - (long long)gi * tiles);
@@ -365,7 +398,8 @@ struct RowLoc {
   long long T;        // total units
 };
 
-__device__ __forceinline__ bool locate_row(const Problem& pr, int n, int h, RowLoc& R) {
+template <class PR>
+__device__ __forceinline__ bool locate_row(const PR& pr, int n, int h, RowLoc& R) {
   long long acc = 0;
   int qacc = 0;
   bool found = false;
@@ -399,15 +433,18 @@ struct Segment {
 
 // Shared mode: teams, and the columns a team takes.
 __device__ __forceinline__ int share_teams(const Problem& pr) { return pr.U / pr.share; }
-__device__ __forceinline__ long long share_columns_per_team(const Problem& pr, int tiles) {
+template <class PR>
+__device__ __forceinline__ long long share_columns_per_team(const PR& pr, int tiles) {
   const long long C = (long long)pr.Hkv * tiles;
   const int Q = share_teams(pr);
-  return div_ll(C + Q - 1, Q);
+  if constexpr (PR::kWindowed) return div_ll(C + Q - 1, Q);
+  return (C + Q - 1) / Q;
 }
 
 // Worker u's walk positions [t0, t1).  `shared` is pr.share != 0; kernels that know it
 // at compile time pass a constant, so the other mode's code is not in them.
-__device__ __forceinline__ void worker_range(const Problem& pr, int u, long long& t0, long long& t1, bool shared) {
+template <class PR>
+__device__ __forceinline__ void worker_range(const PR& pr, int u, long long& t0, long long& t1, bool shared) {
   if (!shared) {
     if (pr.align > 0) {  // worker j of row group q: its share of the group's tiles
       const SeqInfo s = seq_info(pr, 0);
@@ -437,7 +474,8 @@ __device__ __forceinline__ void worker_range(const Problem& pr, int u, long long
 }
 
 // The segment of worker u's walk that starts at t; advances t past it.
-__device__ __forceinline__ bool next_segment(const Problem& pr, int u, long long& t, long long t_end, Segment& seg,
+template <class PR>
+__device__ __forceinline__ bool next_segment(const PR& pr, int u, long long& t, long long t_end, Segment& seg,
                                              bool shared) {
   if (t >= t_end) return false;
   long long end;
@@ -450,7 +488,7 @@ __device__ __forceinline__ bool next_segment(const Problem& pr, int u, long long
     L.b = 0;
     L.MP = seq_groups(pr, L.s.m);
     L.tiles = seq_tiles(L.s.P);
-    L.g = (int)div_ll(t, L.tiles);
+    L.g = PR::kWindowed ? (int)div_ll(t, L.tiles) : (int)(t / L.tiles);
     L.mp = u % pr.share;
     L.tile = (int)(t - (long long)L.g * L.tiles);
     L.q = L.g * L.MP + L.mp;
@@ -497,19 +535,22 @@ struct GroupLoc {
   bool found;
 };
 
-__device__ __forceinline__ GroupLoc locate_group(const Problem& pr, long long qg) {
+template <class PR>
+__device__ __forceinline__ GroupLoc locate_group(const PR& pr, long long qg) {
   GroupLoc R;
   R.found = false;
   R.b = R.g = R.mp = R.tiles = 0;
   R.start = 0;
   long long acc = 0, qacc = 0;
   int first = 0;
-  if (pr.unit_start != nullptr) {
-    R.T = pr.unit_start[pr.B];
-    if (qg >= pr.group_start[pr.B]) return R;
-    first = find_sequence(pr.group_start, pr.B, qg);
-    acc = pr.unit_start[first];
-    qacc = pr.group_start[first];
+  if constexpr (PR::kWindowed) {
+    if (pr.unit_start != nullptr) {
+      R.T = pr.unit_start[pr.B];
+      if (qg >= pr.group_start[pr.B]) return R;
+      first = find_sequence(pr.group_start, pr.B, qg);
+      acc = pr.unit_start[first];
+      qacc = pr.group_start[first];
+    }
   }
   for (int b = first; b < pr.B; ++b) {
     const SeqInfo s = seq_info(pr, b);
@@ -521,7 +562,9 @@ __device__ __forceinline__ GroupLoc locate_group(const Problem& pr, long long qg
       R.s = s; R.b = b; R.g = (int)(gi / MP); R.mp = (int)(gi % MP); R.tiles = tiles;
       R.start = acc + gi * tiles;
       R.found = true;
-      if (pr.unit_start != nullptr) return R;
+      if constexpr (PR::kWindowed) {
+        if (pr.unit_start != nullptr) return R;
+      }
     }
     acc += nq * tiles;
     qacc += nq;

@@ -119,8 +119,6 @@ tva_status make_layout(int B, int Hq, int Hkv, int d, int dtype, int max_prefix,
   L->pair = allow_pair && g_use_cta_pair.load(std::memory_order_relaxed) != 0 && dtype != TVA_FP32 && W == 2 && d == 128;
   pr.U = dtype == TVA_FP32 ? sms * tva::simt_workers_per_sm() : (L->pair ? sms / 2 : sms);
   pr.max_prefix = max_prefix; pr.max_nodes = max_nodes;
-  pr.window = pr.sinks = 0;
-  pr.unit_start = pr.group_start = nullptr;
   pr.kv_capacity = kv_cap; pr.node_capacity = node_cap;
   const int mp_max = (max_nodes + W * npt - 1) / (W * npt);  // row groups per KV head
   const long long groups = (long long)B * Hkv * mp_max;
@@ -150,11 +148,13 @@ float scale_log2(float softmax_scale, int d) {
   return s * 1.44269504088896340736f;
 }
 
-tva::PartialArgs partial_args(const Layout& L, float softmax_scale, const void* q, const void* k_cache,
+// Arguments of the two stages for the plain problem (PR = Problem) or a windowed one.
+template <class PR>
+tva::PartialArgsOf<PR> partial_args(const Layout& L, const PR& pr, float softmax_scale, const void* q, const void* k_cache,
                               const void* v_cache, const void* tree_k, const void* tree_v, const int32_t* parent,
                               void* workspace, int32_t* dev_status) {
-  tva::PartialArgs a;
-  a.pr = L.pr;
+  tva::PartialArgsOf<PR> a;
+  a.pr = pr;
   a.q = q; a.k_cache = k_cache; a.v_cache = v_cache; a.tree_k = tree_k; a.tree_v = tree_v;
   a.parent = parent;
   a.scale_log2 = scale_log2(softmax_scale, L.pr.d);
@@ -170,7 +170,7 @@ tva_status run_partials(const Layout& L, int dtype, float softmax_scale, const v
                         const void* tree_v, const int32_t* parent, void* workspace,
                         int32_t* dev_status, cudaStream_t s) {
   const tva::PartialArgs a =
-      partial_args(L, softmax_scale, q, k_cache, v_cache, tree_k, tree_v, parent, workspace, dev_status);
+      partial_args(L, L.pr, softmax_scale, q, k_cache, v_cache, tree_k, tree_v, parent, workspace, dev_status);
   const cudaError_t e = dtype == TVA_FP32 ? tva::launch_partials_simt(a, dtype, s)
                         : L.pair           ? tva::launch_partials_pair(a, dtype == TVA_BF16, L.npt, s)
                                            : tva::launch_partials_tc(a, dtype == TVA_BF16, L.W, L.npt, s);
@@ -192,15 +192,21 @@ tva_status run_attention(const Layout& L, int dtype, float softmax_scale, const 
   return run_combine(L, dtype, workspace, out, lse, dev_status, s);
 }
 
-tva_status run_combine(const Layout& L, int dtype, const void* workspace, void* out, float* lse,
-                       int32_t* dev_status, cudaStream_t s) {
-  tva::CombineArgs a;
-  a.pr = L.pr;
+template <class PR>
+tva_status run_combine_of(const Layout& L, const PR& pr, int dtype, const void* workspace, void* out, float* lse,
+                          int32_t* dev_status, cudaStream_t s) {
+  tva::CombineArgsOf<PR> a;
+  a.pr = pr;
   a.o_part = static_cast<const float*>(workspace);
   a.lse_part = reinterpret_cast<const float*>(static_cast<const char*>(workspace) + L.o_bytes);
   a.slots = L.slots;
   a.out = out; a.lse = lse; a.status = dev_status;
   return tva::launch_combine(a, dtype, s) == cudaSuccess ? TVA_OK : TVA_ERR_CUDA;
+}
+
+tva_status run_combine(const Layout& L, int dtype, const void* workspace, void* out, float* lse,
+                       int32_t* dev_status, cudaStream_t s) {
+  return run_combine_of(L, L.pr, dtype, workspace, out, lse, dev_status, s);
 }
 
 tva_status check_io_ptrs(const void* q, const void* k_cache, const void* v_cache,
@@ -220,12 +226,12 @@ tva_status check_workspace(const Layout& L, const void* ws, size_t bytes) {
   return TVA_OK;
 }
 
-// The checks and the layout that the windowed and the 4-bit-cache forms share; p's window
-// is set in the layout's problem (0: the whole prefix).
+// The checks, the layout and the problem that the windowed and the 4-bit-cache forms share
+// (window 0: the whole prefix).
 tva_status check_varlen_window(const tva_params* p, int window, int sinks, const void* q, const void* k_cache,
                                const void* v_cache, const void* tree_k, const void* tree_v, const int32_t* parent,
                                const void* out, const float* lse, const void* workspace, size_t workspace_bytes,
-                               const int32_t* dev_status, Layout* L) {
+                               const int32_t* dev_status, Layout* L, tva::WinProblem* pr) {
   if (out == nullptr || lse == nullptr || !aligned16(out)) return TVA_ERR_INVALID_ARG;
   if (p == nullptr || p->cu_prefix == nullptr || p->cu_nodes == nullptr || dev_status == nullptr)
     return TVA_ERR_INVALID_ARG;
@@ -238,8 +244,10 @@ tva_status check_varlen_window(const tva_params* p, int window, int sinks, const
   st = make_layout(p->batch, p->num_q_heads, p->num_kv_heads, p->head_dim, (int)p->dtype, p->max_prefix_len,
                    p->max_nodes, p->kv_capacity, p->node_capacity, p->cu_prefix, p->cu_nodes, 0, 0, L, false);
   if (st != TVA_OK) return st;
-  L->pr.window = window;
-  L->pr.sinks = sinks;
+  static_cast<Problem&>(*pr) = L->pr;
+  pr->window = window;
+  pr->sinks = sinks;
+  pr->unit_start = pr->group_start = nullptr;
   return check_workspace(*L, workspace, workspace_bytes);
 }
 
@@ -500,11 +508,18 @@ tva_status tree_verify_attn_window_varlen(const tva_params* p, int window, int s
                                           void* stream) {
   if (window < 1) return TVA_ERR_INVALID_ARG;
   Layout L;
+  tva::WinProblem pr;
   const tva_status st = check_varlen_window(p, window, sinks, q, k_cache, v_cache, tree_k, tree_v, parent, out, lse,
-                                            workspace, workspace_bytes, dev_status, &L);
+                                            workspace, workspace_bytes, dev_status, &L, &pr);
   if (st != TVA_OK) return st;
-  return run_attention(L, (int)p->dtype, p->softmax_scale, q, k_cache, v_cache, tree_k, tree_v, parent, workspace,
-                       out, lse, dev_status, static_cast<cudaStream_t>(stream));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int dtype = (int)p->dtype;
+  const tva::WinPartialArgs a = partial_args(L, pr, p->softmax_scale, q, k_cache, v_cache, tree_k, tree_v, parent,
+                                             workspace, dev_status);
+  const cudaError_t e = dtype == TVA_FP32 ? tva::launch_partials_simt(a, dtype, s)
+                                          : tva::launch_partials_tc(a, dtype == TVA_BF16, L.W, L.npt, s);
+  if (e != cudaSuccess) return TVA_ERR_CUDA;
+  return run_combine_of(L, pr, dtype, workspace, out, lse, dev_status, s);
 }
 
 tva_status tree_verify_attn_kv4_varlen(const tva_params* p, int window, int sinks, const void* q,
@@ -513,14 +528,15 @@ tva_status tree_verify_attn_kv4_varlen(const tva_params* p, int window, int sink
                                        size_t workspace_bytes, int32_t* dev_status, void* stream) {
   if (p != nullptr && p->dtype == TVA_FP32) return TVA_ERR_UNSUPPORTED;
   Layout L;
+  tva::WinProblem pr;
   const tva_status st = check_varlen_window(p, window, sinks, q, kv4_cache, kv4_cache, tree_k, tree_v, parent, out,
-                                            lse, workspace, workspace_bytes, dev_status, &L);
+                                            lse, workspace, workspace_bytes, dev_status, &L, &pr);
   if (st != TVA_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const tva::PartialArgs a = partial_args(L, p->softmax_scale, q, kv4_cache, kv4_cache, tree_k, tree_v, parent,
-                                          workspace, dev_status);
+  const tva::WinPartialArgs a = partial_args(L, pr, p->softmax_scale, q, kv4_cache, kv4_cache, tree_k, tree_v, parent,
+                                             workspace, dev_status);
   if (tva::launch_partials_kv4(a, p->dtype == TVA_BF16, L.W, L.npt, s) != cudaSuccess) return TVA_ERR_CUDA;
-  return run_combine(L, (int)p->dtype, workspace, out, lse, dev_status, s);
+  return run_combine_of(L, pr, (int)p->dtype, workspace, out, lse, dev_status, s);
 }
 
 size_t tva_kv4_record_bytes(int head_dim) {

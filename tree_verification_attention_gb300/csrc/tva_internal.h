@@ -11,8 +11,9 @@
 
 namespace tva {
 
-struct PartialArgs {
-  Problem pr;
+template <class PR>
+struct PartialArgsOf {
+  PR pr;
   const void* q;
   const void* k_cache;
   const void* v_cache;
@@ -26,8 +27,12 @@ struct PartialArgs {
   int32_t* status;
 };
 
-struct CombineArgs {
-  Problem pr;
+using PartialArgs = PartialArgsOf<Problem>;
+using WinPartialArgs = PartialArgsOf<WinProblem>;
+
+template <class PR>
+struct CombineArgsOf {
+  PR pr;
   const float* o_part;
   const float* lse_part;
   long long slots;
@@ -35,6 +40,9 @@ struct CombineArgs {
   float* lse;
   int32_t* status;
 };
+
+using CombineArgs = CombineArgsOf<Problem>;
+using WinCombineArgs = CombineArgsOf<WinProblem>;
 
 struct AcceptArgs {
   int B;
@@ -133,10 +141,12 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 // dtype: 0 = bf16, 1 = fp32, 2 = fp16 (tva_dtype values)
 int simt_workers_per_sm();
 cudaError_t launch_partials_simt(const PartialArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_partials_simt(const WinPartialArgs& a, int dtype, cudaStream_t s);  // under a window
 // bf16 (bf16 = true) or fp16, head_dim 64 or 128; W M-tiles of npt nodes per row group
 cudaError_t launch_partials_tc(const PartialArgs& a, bool bf16, int W, int npt, cudaStream_t s);
+cudaError_t launch_partials_tc(const WinPartialArgs& a, bool bf16, int W, int npt, cudaStream_t s);  // under a window
 // The same over a 4-bit prefix cache (a.k_cache: the records; a.v_cache unused).
-cudaError_t launch_partials_kv4(const PartialArgs& a, bool bf16, int W, int npt, cudaStream_t s);
+cudaError_t launch_partials_kv4(const WinPartialArgs& a, bool bf16, int W, int npt, cudaStream_t s);
 // Row groups of two M-tiles at head_dim 128 on CTA pairs (a.pr.U = pairs); bf16 or fp16.
 cudaError_t launch_partials_pair(const PartialArgs& a, bool bf16, int npt, cudaStream_t s);
 // 3-D 16-bit tensor map over [rows][heads][d] with a box of {64, box_heads, box_rows}
@@ -151,6 +161,7 @@ void tc_wait_settings(uint64_t* wait_ns, int* stall);
 // default 2 s) and the test stall (tva_diag_set_wait_limit).
 void set_tc_wait_limit(unsigned long long ns, int stall);
 cudaError_t launch_combine(const CombineArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_combine(const WinCombineArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s);
 cudaError_t launch_commit(const CommitArgs& a, cudaStream_t s);
 cudaError_t launch_append_kv4(const Kv4RowArgs& a, int dtype, cudaStream_t s);
