@@ -304,16 +304,7 @@ __device__ __forceinline__ void stage_problem(const PR& src, PR* dst, int* buf, 
       buf[src.B + 1 + i] = __ldg(src.cu_nodes + i);
     }
   }
-  if constexpr (PR::kWindowed) {
-    PR pr = src;
-    if (fits) {
-      __syncthreads();
-      pr.cu_prefix = buf;
-      pr.cu_nodes = buf + src.B + 1;
-      if (pr.B >= kSumsFrom) stage_sums(pr, buf, cap);
-    }
-    if (threadIdx.x == 0) *dst = pr;
-  } else if (threadIdx.x == 0) {
+  if (threadIdx.x == 0) {
     *dst = src;
     if (fits) {
       dst->cu_prefix = buf;
@@ -321,6 +312,17 @@ __device__ __forceinline__ void stage_problem(const PR& src, PR* dst, int* buf, 
     }
   }
   __syncthreads();
+  if constexpr (PR::kWindowed) {
+    if (fits && src.B >= kSumsFrom) {
+      PR pr = *dst;
+      stage_sums(pr, buf, cap);
+      if (threadIdx.x == 0) {
+        dst->unit_start = pr.unit_start;
+        dst->group_start = pr.group_start;
+      }
+      __syncthreads();
+    }
+  }
 }
 
 // Total units T and the chunk size c = ceil(T / U).
