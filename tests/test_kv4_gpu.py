@@ -395,3 +395,24 @@ def test_the_binding_refuses_what_does_not_fit():
         api.append_kv4(k.transpose(0, 1), k.transpose(0, 1), _i32([0, 1]), t["kv4_cache"])
     with pytest.raises(ValueError):
         api.read_kv4(t["kv4_cache"], 128)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("seed", range(6))
+def test_batches_of_short_sequences_agree_call_after_call(dtype, seed):
+    """Workers whose ranges cross several short row groups, in batches large enough for the
+    staged running sums: right, and the same bits every time."""
+    rng = np.random.default_rng(60 + seed)
+    B = int(rng.integers(16, 48))
+    P = [int(x) for x in rng.integers(0, (100, 300, 2000)[seed % 3], B)]
+    m = [int(x) for x in rng.integers(0, 9 if seed % 2 else 50, B)]
+    m[0] = 1
+    heads, d = [((12, 4), 128), ((8, 2), 64), ((32, 8), 128)][seed % 3]
+    pr = _window.Problem(dtype, P, m, heads, d, "random", seed=seed, kv4=True)
+    t = pr.device()
+    for window, sinks in ((0, 0), (60, 4)):
+        out, lse = pr.run(window, sinks, t)
+        pr.check(out, lse, window, sinks, (B, P, m))
+        for _ in range(10):
+            again = pr.run(window, sinks, t)
+            assert torch.equal(out, again[0]) and torch.equal(lse, again[1])

@@ -180,3 +180,40 @@ def test_the_binding_refuses_what_does_not_fit():
         pr.call(t, 8, 0, out=torch.empty(4, 8, 32, dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(ValueError):
         pr.call(dict(t, k_cache=t["k_cache"].half()), 8, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("seed", range(6))
+def test_batches_of_short_sequences_agree_call_after_call(dtype, seed):
+    """Workers whose ranges cross several short row groups, in batches large enough for the
+    staged running sums: right, and the same bits every time."""
+    rng = np.random.default_rng(80 + seed)
+    B = int(rng.integers(16, 48))
+    P = [int(x) for x in rng.integers(0, (100, 300, 2000)[seed % 3], B)]
+    m = [int(x) for x in rng.integers(0, 9 if seed % 2 else 50, B)]
+    m[0] = 1
+    heads, d = [((12, 4), 128), ((8, 2), 64), ((32, 8), 128)][seed % 3]
+    window, sinks = (60, 4) if seed < 3 else (700, 0)
+    pr = _window.Problem(dtype, P, m, heads, d, "random", seed=seed)
+    t = pr.device()
+    out, lse = pr.run(window, sinks, t)
+    pr.check(out, lse, window, sinks, (B, P, m))
+    for _ in range(10):
+        again = pr.run(window, sinks, t)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_batches_beyond_the_staged_arrays():
+    """Batches whose arrays no longer fit in shared memory, or whose sums do not."""
+    for B in (200, 300, 700):
+        rng = np.random.default_rng(B)
+        P = [int(x) for x in rng.integers(0, 60, B)]
+        m = [int(x) for x in rng.integers(0, 3, B)]
+        m[0] = 1
+        for dtype in ("bf16", "fp32"):
+            pr = _window.Problem(dtype, P, m, (4, 2), 64, "random", seed=B)
+            out, lse = pr.run(25, 3)
+            pr.check(out, lse, 25, 3)
+        pr = _window.Problem("bf16", P, m, (4, 2), 64, "random", seed=B, kv4=True)
+        out, lse = pr.run(0, 0)
+        pr.check(out, lse, 0, 0)

@@ -7,20 +7,17 @@
 // type - exactly: a value has at most 7 significant bits - on their way to the tensor
 // cores: DRAM and L2 carry 144 bytes a row and head (d = 128) instead of 512.
 //
-// How (one CTA per SM, 640 threads in five warpgroups with registers of their own):
-//   warp 16 (producer): TMA of Q, of the tree tile's K / V (16-bit, into the ring) and of
-//           the raw 128-record tiles (a box of records, 18 KB at d = 128) into a ring.
-//   warps 8-11 and 12-15 (widening K, widening V): thread r widens record r of a tile: 16
-//           bytes of codes become 64 bytes of a K or V tile in the 128-byte-swizzled ring
-//           that the MMAs read.  A shift and one and-or put two codes n into the mantissas
-//           of 128 + n (fp16: 16 + n), one fused multiply-add takes the offset off and
-//           applies the scale.  Rows past a tile's last key are written as zeros, so nothing
-//           that a record of another sequence holds can reach a product.  K and V have a
-//           warpgroup each because a tile's widening is a chain of about 1300 clocks however
-//           few rows the tree has: one warpgroup for both took 3000 a tile, more than
-//           everything else when the tree has one M-tile.
-//   warp 17 (MMA), warps 0-7 (softmax): as in k_partials_tc.cu, two streams of 4 warps.
-//           A warp whose 32 rows are all padding leaves its logits alone.
+// How (one CTA per SM; Roles gives the warps):
+//   producer warp: TMA of Q, and of the raw 128-record tiles (a box of records, 18 KB at
+//           d = 128) into a ring of their own.
+//   widening warps: thread r widens record r of a tile: 16 bytes of codes become 64 bytes of
+//           a K or V tile in the 128-byte-swizzled ring that the MMAs read.  A shift and one
+//           and-or put two codes n into the mantissas of 128 + n (fp16: 16 + n), one fused
+//           multiply-add takes the offset off and applies the scale.  Rows past a tile's last
+//           key are written as zeros, so nothing that a record of another sequence holds can
+//           reach a product.  The tree tile's K / V are 16-bit already and fetched by TMA.
+//   MMA warp, softmax warps: as in k_partials_tc.cu, two streams of 4 softmax warps.  A
+//           softmax warp whose 32 rows are all padding leaves its logits alone.
 // TMEM columns: S/P buffers at 0 and 128, O accumulators at 256 and 384 (512 total).
 // A window (pr.window > 0) is handled as there too, at run time: it only adds masks to the
 // tiles that its lower edge crosses.
@@ -42,16 +39,29 @@ namespace {
 using namespace ptx;
 
 
-constexpr int kWidenWarp = 8;     // 8-11: K, 12-15: V
-constexpr int kProducerWarp = 16;
-constexpr int kMmaWarp = kProducerWarp + 1;
-constexpr int kThreadsKv4 = 640;
 constexpr int kHalfBytes = 128 * 128;  // 128 rows of 64 16-bit values (one swizzle span)
-// Registers per thread of the five warpgroups (two of softmax, K, V, the rest).  They share
-// what the block is launched with, 640 x 96 (checked before the first launch): a split above
-// that would wait forever.
-constexpr int kLaunchRegs = 96, kSoftmaxRegs = 152, kWidenRegs = 56, kOtherRegs = 64;
-static_assert(2 * kSoftmaxRegs + 2 * kWidenRegs + kOtherRegs <= 5 * kLaunchRegs, "register split");
+// The warps of a kernel for row groups of W M-tiles, and the registers per thread of its
+// warpgroups (two of softmax, the widening ones, the rest).  They share what the block is
+// launched with (checked before the first launch): a split above that would wait forever.
+//   W = 1: a widening warpgroup each for K and V.  A tile's K or V is a chain of about 1300
+//          clocks however few rows the tree has; one warpgroup for both took 3000 a tile,
+//          more than everything else (8 sequences, 4k..32k: 105 us instead of 89).
+//   W = 2: one for both.  The softmax of two M-tiles then bounds a tile and is slowed by
+//          every further warp (64k prefix, 64 nodes: 68 us instead of 72).
+template <int W>
+struct Roles {
+  static constexpr int kWidenGroups = W == 1 ? 2 : 1;
+  static constexpr int kWidenWarp = 8;
+  static constexpr int kProducerWarp = kWidenWarp + 4 * kWidenGroups;
+  static constexpr int kMmaWarp = kProducerWarp + 1;
+  static constexpr int kThreads = 32 * (kProducerWarp + 4);
+  static constexpr int kLaunchRegs = W == 1 ? 96 : 128;
+  static constexpr int kSoftmaxRegs = W == 1 ? 152 : 168;
+  static constexpr int kWidenRegs = W == 1 ? 56 : 88;
+  static constexpr int kOtherRegs = W == 1 ? 64 : 88;
+  static_assert(2 * kSoftmaxRegs + kWidenGroups * kWidenRegs + kOtherRegs <= (3 + kWidenGroups) * kLaunchRegs,
+                "register split");
+};
 
 template <int D>
 struct Cfg {
@@ -71,7 +81,6 @@ struct Cfg {
 
 struct Kv4Args {
   WinPartialArgs a;
-  int W;    // M-tiles per row group (1 or 2)
   int npt;  // nodes per M-tile: floor(128 / G)
   // What is fetched of an M-tile's nodes and of the tree tile's rows: no more than the
   // largest tree has.  A TMA copy takes time for each row of its box, so full boxes would
@@ -196,19 +205,20 @@ __device__ __forceinline__ void mbar_arrive_elect(uint32_t bar) {
       : "memory");
 }
 
-template <int D, bool kBF16, bool kShare>
-__global__ void __launch_bounds__(kThreadsKv4, 1)
+template <int D, bool kBF16, bool kShare, int W>
+__global__ void __launch_bounds__(Roles<W>::kThreads, 1)
     partials_kv4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_raw,
                         const __grid_constant__ CUtensorMap tm_tk, const __grid_constant__ CUtensorMap tm_tv,
                         const Kv4Args args) {
   using C = Cfg<D>;
+  using R = Roles<W>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const WinPartialArgs& a = args.a;
   WinProblem* pr_s = reinterpret_cast<WinProblem*>(smem + C::kBarOff + C::kCuOff - 128);
   static_assert(sizeof(WinProblem) <= 128, "staged problem");
   const WinProblem& pr = *pr_s;
-  const int W = args.W, npt = args.npt, G = a.pr.G;  // kernel parameters: readable before staging
+  const int npt = args.npt, G = a.pr.G;  // kernel parameters: readable before staging
   const uint64_t wait_ns = args.wait_ns;  // main-loop waits; drains use kDrainNs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int u = blockIdx.x;
@@ -240,7 +250,7 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
   int* par_s = reinterpret_cast<int*>(smem + C::kBarOff + 2560);    // [2][128] parent ids
 
   // ---- Set-up that reads nothing an earlier kernel may write (programmatic dependent).
-  if (warp == kProducerWarp && lane == 0) {
+  if (warp == R::kProducerWarp && lane == 0) {
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_raw);
     prefetch_tmap(&tm_tk);
@@ -251,7 +261,7 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
     }
     for (int s = 0; s < C::kRaws; ++s) {
       mbar_init(RAW_FULL + 8 * s, 1);
-      mbar_init(RAW_EMPTY + 8 * s, 8);
+      mbar_init(RAW_EMPTY + 8 * s, 4 * R::kWidenGroups);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(Q_FULL + 8 * w, 1);
@@ -281,26 +291,27 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
   // The other warps wait for the TMEM allocation on named barrier 1, which the producer
   // warp only arrives at: it goes straight on to its first copies.
   uint32_t tmem = 0;
-  if (warp == kProducerWarp) {
+  if (warp == R::kProducerWarp) {
     __syncwarp();
-    bar_arrive(1, kThreadsKv4);
+    bar_arrive(1, R::kThreads);
   } else {
-    if (warp == kMmaWarp) {
+    if (warp == R::kMmaWarp) {
       tmem_alloc(smem_u32(tmem_slot), 512);
       tmem_relinquish();
     }
     tc_fence_before();
-    bar_sync(1, kThreadsKv4);
+    bar_sync(1, R::kThreads);
     tc_fence_after();
     tmem = *tmem_slot;
   }
 
-  if (warp >= kProducerWarp) {
-    reg_dec<kOtherRegs>();
-    if (warp == kProducerWarp) {
+  if (warp >= R::kProducerWarp) {
+    reg_dec<R::kOtherRegs>();
+    if (warp == R::kProducerWarp) {
       // ---------------------------------------------------------------- producer
       // All 32 lanes run this role; one elected lane issues each copy and expect-tx.
-      int ring = 0, raw = 0, sg = 0, trees = 0;
+      int raw = 0, sg = 0;
+      int q_loads = 0;  // segments whose Q has been issued
       bool ok = true;
       long long t = t_begin;
       Segment S;
@@ -322,22 +333,7 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
               tma_load_3d_elect(q_s + ((qb + mt) * C::kHalves + h) * kHalfBytes, &tm_q, 64 * h, L.g * G, qrow,
                                 Q_FULL + 8 * qb);
           }
-          return true;
-        };
-        // the tree tile's K (or V) straight into its ring stage; the widening warps
-        // complete the stage once it has landed
-        auto load_tree = [&](bool is_v) -> bool {
-          const int idx = ring + (is_v ? ring_v(W, 0, n) : ring_k(W, 0));
-          const int stage = idx % C::kStages, use = idx / C::kStages;
-          if (use > 0 && !warp_wait(KV_EMPTY + 8 * stage, (use - 1) & 1, abort_flag, wait_ns)) return false;
-          // short segments could put two tree tiles into the ring: TREE_FULL stays one ahead
-          if (trees > 0 && !warp_wait(TREE_EMPTY + (is_v ? 8 : 0), (trees - 1) & 1, abort_flag, wait_ns)) return false;
-          int z = L.s.n0;
-          if (!TVA_CHECK(z >= 0 && z < pr.node_capacity && L.s.m > 0, a.status)) z = 0;
-          mbar_expect_tx_elect(TREE_FULL + (is_v ? 8 : 0), (uint32_t)C::kHalves * 128u * args.tree_rows);
-          for (int h = 0; h < C::kHalves; ++h)
-            tma_load_3d_elect(kv_s + stage * C::kTileBytes + h * kHalfBytes, is_v ? &tm_tv : &tm_tk, 64 * h, L.g, z,
-                              TREE_FULL + (is_v ? 8 : 0));
+          ++q_loads;
           return true;
         };
         auto load_raw = [&](int i) -> bool {  // the segment's i-th prefix tile
@@ -351,32 +347,23 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
           return true;
         };
         // The first kRaws record tiles wait only for earlier segments, so they may be
-        // fetched before this segment's Q and tree tile; the later ones wait for this
-        // segment's own progress, which needs both.
-        const int head = min(n_raw, C::kRaws);
+        // fetched before this segment's Q; the later ones wait for this segment's own
+        // progress, which needs it.
         int i = 0;
         if (sg > 0)
-          for (; i < head && ok; ++i) ok = load_raw(i);
-        ok = ok && load_q() && (!tree || load_tree(false));
-        for (; i < head && ok; ++i) ok = load_raw(i);
-        ok = ok && (!tree || load_tree(true));
+          for (; i < min(n_raw, C::kRaws) && ok; ++i) ok = load_raw(i);
+        ok = ok && load_q();
         for (; i < n_raw && ok; ++i) ok = load_raw(i);
-        if (tree) ++trees;
-        ring += 2 * n;
         ++sg;
-        if (!ok) break;
       }
-      // drain: every copy this thread started has landed before TMEM / smem go away.  (A
-      // run that gave up in mid-segment may wait here for a phase without a copy: bounded.)
+      // drain: every copy this thread started has landed before TMEM / smem go away
       for (int i = max(0, raw - C::kRaws); i < raw; ++i)
         drain_wait(RAW_FULL + 8 * (i % C::kRaws), (i / C::kRaws) & 1);
-      for (int w = 0; w < 2; ++w)
-        if (trees > 0) drain_wait(TREE_FULL + 8 * w, (trees - 1) & 1);
       for (int b = 0; b < 2; ++b) {  // the last load into each Q buffer
-        const int uses = (W == 1) ? (sg + 1 - b) / 2 : (b == 0 ? sg : 0);
+        const int uses = (W == 1) ? (q_loads + 1 - b) / 2 : (b == 0 ? q_loads : 0);
         if (uses > 0) drain_wait(Q_FULL + 8 * b, (uses - 1) & 1);
       }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == R::kMmaWarp) {
       // ---------------------------------------------------------------- MMA issuer
       // All 32 lanes run this role; the *_elect forms issue each MMA / commit from one lane.
       constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, kBF16);
@@ -494,44 +481,65 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
       tc_commit_elect(DRAIN);
       drain_wait(DRAIN, 0);
     }
-  } else if (warp >= kWidenWarp) {
+  } else if (warp >= R::kWidenWarp) {
     // ------------------------------------------------------------------ widening
-    reg_dec<kWidenRegs>();
-    const bool is_v = warp >= kWidenWarp + 4;
+    reg_dec<R::kWidenRegs>();
     const int r = threadIdx.x & 127;  // the tile's row (key) of this thread
     const uint32_t row_s = kv_s + r * 128 + ((r & 7) << 4);  // 16-byte chunk c of a span is at c ^ (row mod 8)
-    const uint32_t codes = raw_s + r * kv4_record_bytes(D) + (is_v ? D / 2 : 0);
-    const uint32_t scales = raw_s + r * kv4_record_bytes(D) + D + (is_v ? D / 16 : 0);
-    const uint32_t tree_bar = is_v ? 8 : 0;
+    const uint32_t rec_s = raw_s + r * kv4_record_bytes(D);
+    const int mine = (warp - R::kWidenWarp) >> 2;  // W = 1: 0 widens K, 1 V
     uint32_t raw = 0, raw_ph = 0;
-    int ring = 0, trees = 0;
+    int ring = 0, trees = 0, k_loads = 0, v_loads = 0;
     bool ok = true;
     long long t = t_begin;
     Segment S;
     while (ok && next_segment(pr, u, t, t_end, S, kShare)) {
       const int n = S.n;
 #pragma unroll 1
-      for (int k = 0; k < n; ++k) {
+      for (int i = 0; i < (R::kWidenGroups == 2 ? n : 2 * n); ++i) {
+        const int k = R::kWidenGroups == 2 ? i : i >> 1;
+        const bool is_v = (R::kWidenGroups == 2 ? mine : i & 1) != 0;
         const int idx = ring + (is_v ? ring_v(W, k, n) : ring_k(W, k));
         const uint32_t stage = (uint32_t)idx % C::kStages, use = (uint32_t)idx / C::kStages;
         const int tile = S.tile0 + k;
+        // The stage's last tile has been used.  (A wait for the phase before a fresh barrier's
+        // first returns at once.  With two groups the tiles in between are the other's: its
+        // place in the ring is at most three from this group's last one, whose wait implies
+        // that every phase but the awaited one is complete - tiles are released in order.)
+        if (!(ok = warp_wait(KV_EMPTY + 8 * stage, (use & 1u) ^ 1u, abort_flag, wait_ns))) break;
         int lim;  // rows from here on are written as zeros
         if (tile == 0) {
-          // fetched by the producer; rows past the tree are another sequence's, or nothing's
+          // The tree's own K / V are 16-bit already: the group's first warp fetches them into
+          // the stage.  (It cannot be the producer warp, which does not follow the ring:
+          // a phase of KV_EMPTY that it had not waited for in turn looks like the one two
+          // earlier.)  Rows past the tree are another sequence's, or nothing's.
+          const uint32_t tree_bar = is_v ? 8 : 0;
+          if ((warp & 3) == 0) {
+            // TREE_FULL stays one phase ahead: every warp has seen the last tree's
+            if (trees > 0 && !(ok = warp_wait(TREE_EMPTY + tree_bar, (trees - 1) & 1, abort_flag, wait_ns))) break;
+            int z = S.L.s.n0;
+            if (!TVA_CHECK(z >= 0 && z < pr.node_capacity && S.L.s.m > 0, a.status)) z = 0;
+            mbar_expect_tx_elect(TREE_FULL + tree_bar, (uint32_t)C::kHalves * 128u * args.tree_rows);
+            for (int h = 0; h < C::kHalves; ++h)
+              tma_load_3d_elect(kv_s + stage * C::kTileBytes + h * kHalfBytes, is_v ? &tm_tv : &tm_tk, 64 * h, S.L.g,
+                                z, TREE_FULL + tree_bar);
+            (is_v ? v_loads : k_loads)++;
+          }
           if (!(ok = warp_wait(TREE_FULL + tree_bar, trees & 1, abort_flag, wait_ns))) break;
           mbar_arrive_elect(TREE_EMPTY + tree_bar);
           lim = S.L.s.m;
         } else {
-          // a wait for the phase before a fresh barrier's first returns at once
-          if (!(ok = warp_wait(KV_EMPTY + 8 * stage, (use & 1u) ^ 1u, abort_flag, wait_ns))) break;
           if (!(ok = warp_wait(RAW_FULL + 8 * raw, raw_ph, abort_flag, wait_ns))) break;
           lim = tile_keys(pr, S.L.s, tile);
+          const uint32_t rec = rec_s + raw * C::kRawBytes;
           if (r < lim)
-            widen_row<D, kBF16>(codes + raw * C::kRawBytes, scales + raw * C::kRawBytes, row_s + stage * C::kTileBytes);
-          __syncwarp();
-          mbar_arrive_elect(RAW_EMPTY + 8 * raw);
-          raw = raw + 1 == C::kRaws ? 0 : raw + 1;
-          raw_ph ^= raw == 0 ? 1u : 0u;
+            widen_row<D, kBF16>(rec + (is_v ? D / 2 : 0), rec + D + (is_v ? D / 16 : 0), row_s + stage * C::kTileBytes);
+          if (R::kWidenGroups == 2 || is_v) {  // done with the records
+            __syncwarp();
+            mbar_arrive_elect(RAW_EMPTY + 8 * raw);
+            raw = raw + 1 == C::kRaws ? 0 : raw + 1;
+            raw_ph ^= raw == 0 ? 1u : 0u;
+          }
         }
         if (r >= lim) {
           const uint32_t dst = kv_s + stage * C::kTileBytes + r * 128;
@@ -546,9 +554,12 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
       ring += 2 * n;
       if (S.tile0 == 0) ++trees;
     }
+    // drain: the copies that this warp started
+    if (k_loads > 0) drain_wait(TREE_FULL, (k_loads - 1) & 1);
+    if (v_loads > 0) drain_wait(TREE_FULL + 8, (v_loads - 1) & 1);
   } else {
     // ------------------------------------------------------------------ softmax
-    reg_inc<kSoftmaxRegs>();
+    reg_inc<R::kSoftmaxRegs>();
     const int w = warp >> 2;
     const int r = threadIdx.x & 127;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -782,16 +793,16 @@ __global__ void __launch_bounds__(kThreadsKv4, 1)
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) set_status(a.status, kStatusTimeout);
-  if (warp == kMmaWarp) {
+  if (warp == R::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-template <int D, bool kBF16, bool kShare>
-cudaError_t launch_typed(const WinPartialArgs& a, int W, int npt, cudaStream_t s) {
+template <int D, bool kBF16, bool kShare, int W>
+cudaError_t launch_typed(const WinPartialArgs& a, int npt, cudaStream_t s) {
   constexpr CUtensorMapDataType type = kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  auto kernel = partials_kv4_kernel<D, kBF16, kShare>;
+  auto kernel = partials_kv4_kernel<D, kBF16, kShare, W>;
   const WinProblem& pr = a.pr;
   CUtensorMap mq, mraw, mtk, mtv;
   const int q_nodes = std::min(npt, pr.max_nodes), tree_rows = std::min(kKeyTile, (pr.max_nodes + 7) / 8 * 8);
@@ -809,26 +820,29 @@ cudaError_t launch_typed(const WinPartialArgs& a, int W, int npt, cudaStream_t s
     cudaFuncAttributes fa{};
     return cudaFuncGetAttributes(&fa, kernel) == cudaSuccess ? fa.numRegs : 0;
   }();
-  if (regs < kLaunchRegs) {
+  if (regs < Roles<W>::kLaunchRegs) {
     record_error("launch partials_kv4_kernel", regs, "built with fewer registers than its warpgroups share");
     return cudaErrorInvalidConfiguration;
   }
-  Kv4Args ka{a, W, npt, q_nodes, tree_rows, 0, 0};
+  Kv4Args ka{a, npt, q_nodes, tree_rows, 0, 0};
   tc_wait_settings(&ka.wait_ns, &ka.stall);
-  return check_cuda(launch_pdl(kernel, dim3(pr.U), dim3(kThreadsKv4), (size_t)smem, s, mq, mraw, mtk, mtv, ka),
+  return check_cuda(launch_pdl(kernel, dim3(pr.U), dim3(Roles<W>::kThreads), (size_t)smem, s, mq, mraw, mtk, mtv, ka),
                     "launch partials_kv4_kernel");
 }
 
-template <bool kShare>
-cudaError_t launch_mode(const WinPartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
-  if (bf16) return a.pr.d == 64 ? launch_typed<64, true, kShare>(a, W, npt, s) : launch_typed<128, true, kShare>(a, W, npt, s);
-  return a.pr.d == 64 ? launch_typed<64, false, kShare>(a, W, npt, s) : launch_typed<128, false, kShare>(a, W, npt, s);
+template <bool kShare, int W>
+cudaError_t launch_mode(const WinPartialArgs& a, bool bf16, int npt, cudaStream_t s) {
+  if (bf16)
+    return a.pr.d == 64 ? launch_typed<64, true, kShare, W>(a, npt, s) : launch_typed<128, true, kShare, W>(a, npt, s);
+  return a.pr.d == 64 ? launch_typed<64, false, kShare, W>(a, npt, s) : launch_typed<128, false, kShare, W>(a, npt, s);
 }
 
 }  // namespace
 
 cudaError_t launch_partials_kv4(const WinPartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
-  return a.pr.share != 0 ? launch_mode<true>(a, bf16, W, npt, s) : launch_mode<false>(a, bf16, W, npt, s);
+  if (W == 1)
+    return a.pr.share != 0 ? launch_mode<true, 1>(a, bf16, npt, s) : launch_mode<false, 1>(a, bf16, npt, s);
+  return a.pr.share != 0 ? launch_mode<true, 2>(a, bf16, npt, s) : launch_mode<false, 2>(a, bf16, npt, s);
 }
 
 }  // namespace tva
