@@ -89,19 +89,23 @@ __device__ __forceinline__ int quantise16(const T* src, uint32_t code[2]) {
     const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     uint32_t m = w[0] & 0x7fff7fffu;  // the order of magnitudes is that of their bits
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    for (int i = 1; i < 8; ++i) m = ptx::max_s16x2(m, w[i] & 0x7fff7fffu);
     m = max(m & 0xffffu, m >> 16);
     const int byte = kv4_scale_byte(pair_f<T>(m).x);
     if (m >= kInf || byte < 8 || byte >= kKv4MaxScale) return quantise16_any(src, code);
     const float inv = __fdividef(1.0f, kv4_scale_value(byte));
+    const uint64_t inv2 = ptx::f2_pack(inv, inv), near2 = ptx::f2_pack(384.0f, 384.0f);
+    const uint64_t whole2 = ptx::f2_pack(12582536.0f, 12582536.0f);  // 3 * 2^22 - 384 + 8
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t c = 0u - 0x4b400000u * 0x11111111u;  // what the eight sums' exponent bits add up to
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < 8; e += 2) {
         const float2 p = pair_f<T>(w[4 * h + e / 2]);
-        const float z = fmaf(e & 1 ? p.y : p.x, inv, 384.0f);
-        c += __float_as_uint(z + 12582536.0f) << kv4_shift(e);  // 3 * 2^22 - 384 + 8
+        float z0, z1;
+        ptx::f2_unpack(ptx::f2_add(ptx::f2_fma(ptx::f2_pack(p.x, p.y), inv2, near2), whole2), z0, z1);
+        c += __float_as_uint(z0) << kv4_shift(e);
+        c += __float_as_uint(z1) << kv4_shift(e + 1);
       }
       code[h] = c;
     }
@@ -196,24 +200,25 @@ __global__ void __launch_bounds__(kThreads) commit_kv4_kernel(CommitArgs a, int 
                        static_cast<uint8_t*>(a.k_cache), (long long)n0 + s_path[j], dst + j, Hkv, d, t);
 }
 
-// Eight values of code word `w` at scale byte `byte`.
-__device__ __forceinline__ void values8(uint32_t w, int byte, float x[8]) {
-  const float s = kv4_scale_value(byte);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = (float)((int)((w >> kv4_shift(e)) & 15u) - 8) * s;
+// The eight values of code word `w` at scale byte `byte`, exactly, in each type: by pairs, as
+// the attention widens them (value by value the conversions bound the kernel).
+__device__ __forceinline__ void store8(__nv_bfloat16* dst, uint32_t w, uint32_t byte) {
+  uint32_t s, c;
+  widen_scale<true>(byte, 0, s, c);
+  *reinterpret_cast<uint4*>(dst) = widen8<true>(w, s, c);
 }
-
-__device__ __forceinline__ void store8(float* dst, const float x[8]) {
-  reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void store8(__half* dst, uint32_t w, uint32_t byte) {
+  uint32_t s, c;
+  widen_scale<false>(byte, 0, s, c);
+  *reinterpret_cast<uint4*>(dst) = widen8<false>(w, s, c);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* dst, const float x[8]) {  // exact
-  *reinterpret_cast<uint4*>(dst) = make_uint4(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]),
-                                              ptx::pack_bf16x2(x[4], x[5]), ptx::pack_bf16x2(x[6], x[7]));
-}
-__device__ __forceinline__ void store8(__half* dst, const float x[8]) {  // exact
-  *reinterpret_cast<uint4*>(dst) = make_uint4(ptx::pack_f16x2(x[0], x[1]), ptx::pack_f16x2(x[2], x[3]),
-                                              ptx::pack_f16x2(x[4], x[5]), ptx::pack_f16x2(x[6], x[7]));
+__device__ __forceinline__ void store8(float* dst, uint32_t w, uint32_t byte) {
+  uint32_t s, c;
+  widen_scale<false>(byte, 0, s, c);
+  const uint4 h = widen8<false>(w, s, c);
+  const float2 x0 = pair_f<__half>(h.x), x1 = pair_f<__half>(h.y), x2 = pair_f<__half>(h.z), x3 = pair_f<__half>(h.w);
+  reinterpret_cast<float4*>(dst)[0] = make_float4(x0.x, x0.y, x1.x, x1.y);
+  reinterpret_cast<float4*>(dst)[1] = make_float4(x2.x, x2.y, x3.x, x3.y);
 }
 
 // A thread reads one code word (8 values), numbered as the destination's elements.
@@ -232,16 +237,16 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Kv4RowArgs a, int rows_p
     const int half = t >= per_half ? 1 : 0, in_row = t - half * per_half;
     const int head = in_row >> shift, i = in_row & ((1 << shift) - 1);
     const long long slot = a.slot != nullptr ? (long long)__ldg(a.slot + row) : row;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    uint32_t word = 0u, byte = 0u;  // at scale 0 every code is 0
     if (slot >= a.kv_capacity) {
       if (t == 0) set_status(a.status, kStatusInvalidArg);
     } else if (slot >= 0) {
       const uint8_t* rec = a.cache + (slot * a.Hkv + head) * (long long)kv4_record_bytes(a.d);
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(rec + half * (a.d / 2)) + i);
-      values8(w, __ldg(rec + a.d + half * (a.d / 16) + i / 2), x);
+      word = __ldg(reinterpret_cast<const uint32_t*>(rec + half * (a.d / 2)) + i);
+      byte = __ldg(rec + a.d + half * (a.d / 16) + i / 2);
     }
     T* dst = static_cast<T*>(const_cast<void*>(half ? a.v : a.k)) + (row * per_half + in_row) * 8;
-    store8(dst, x);
+    store8(dst, word, byte);
   }
 }
 

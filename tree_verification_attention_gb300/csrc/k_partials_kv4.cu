@@ -100,60 +100,6 @@ __device__ __forceinline__ int ring_v(int W, int k, int n) {
   return W == 2 ? 2 * k + 1 : (k <= n - 2 ? 2 + 2 * k : 2 * n - 1);
 }
 
-__device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// Byte i of `scales` - a block's scale - as a pair, and the pair that takes the codes'
-// offset off.  Every step is exact: the scale has 4 significant bits; 136 = 8 x 17 times it
-// at most 8 (17 x 15 = 255), 24 = 8 x 3 times it 6.
-template <bool kBF16>
-__device__ __forceinline__ void widen_scale(uint32_t scales, int i, uint32_t& s, uint32_t& c) {
-  const uint32_t b = __byte_perm(scales, 0u, 0x4040u + 0x0101u * i);  // the byte in both halves
-  if constexpr (kBF16) {
-    s = bf2_mul(b << 4, 0x77807780u);  // exponent bias 15 -> 127: times 2^112
-    c = bf2_mul(s, 0xc308c308u);       // -136
-  } else {
-    s = b << 7;
-    c = h2_mul(s, 0xce00ce00u);        // -24
-  }
-}
-
-// One code word (8 values) to four pairs, in the order of the elements.
-template <bool kBF16>
-__device__ __forceinline__ uint4 widen8(uint32_t w, uint32_t s, uint32_t c) {
-  uint4 o;
-  if constexpr (kBF16) {  // 128 + n: a code in the low mantissa bits of 2^7
-    o.x = bf2_fma((w & 0x000f000fu) | 0x43004300u, s, c);
-    o.y = bf2_fma(((w >> 4) & 0x000f000fu) | 0x43004300u, s, c);
-    o.z = bf2_fma(((w >> 8) & 0x000f000fu) | 0x43004300u, s, c);
-    o.w = bf2_fma(((w >> 12) & 0x000f000fu) | 0x43004300u, s, c);
-  } else {                // 16 + n: a code in the high mantissa bits of 2^4
-    o.x = h2_fma(((w << 6) & 0x03c003c0u) | 0x4c004c00u, s, c);
-    o.y = h2_fma(((w << 2) & 0x03c003c0u) | 0x4c004c00u, s, c);
-    o.z = h2_fma(((w >> 2) & 0x03c003c0u) | 0x4c004c00u, s, c);
-    o.w = h2_fma(((w >> 6) & 0x03c003c0u) | 0x4c004c00u, s, c);
-  }
-  return o;
-}
-
 // One row's K or V values (codes at `codes`, scales at `scales`, both shared
 // addresses) into a swizzled tile, from 16-byte chunk `chunk0` of the row on; the row starts
 // at `row`, with the swizzle's row term already in it.  All loads come first.
