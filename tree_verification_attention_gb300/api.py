@@ -8,6 +8,8 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 
 import torch
@@ -412,8 +414,25 @@ def _check_all(*named):
     return here
 
 
-def _raw_stream(stream, device):
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _on_stream(call):
+    """With ``stream`` given, runs the call with that stream current: what the call allocates
+    then belongs to it, so a status word is zeroed before the kernels write it, and a
+    workspace's memory is not handed out again while they still use it."""
+    at = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def run(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None:
+            return call(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return call(*args, **kwargs)
+
+    return run
 
 
 def _status_word(dev_status, device):
@@ -425,7 +444,7 @@ def _status_word(dev_status, device):
 
 
 def _window_attention(name, window, sinks, q, cache, tree_k, tree_v, parent, cu_prefix, cu_nodes, max_prefix_len,
-                      max_nodes, out, lse, workspace, dev_status, softmax_scale, stream, params):
+                      max_nodes, out, lse, workspace, dev_status, softmax_scale, params):
     """The checks and the call that the windowed and the 4-bit-cache forms share; ``cache``
     holds (name, tensor, dtype, row shape) of each cache tensor."""
     dt, i32 = q.dtype, torch.int32
@@ -439,6 +458,8 @@ def _window_attention(name, window, sinks, q, cache, tree_k, tree_v, parent, cu_
     Nk, Hkv, dk = tree_k.shape
     if Nk != N or dk != d or parent.shape[0] != N:
         raise ValueError("q, tree_k and parent must have one row per tree node")
+    if cu_prefix.dim() != 1 or cu_nodes.shape != cu_prefix.shape:
+        raise ValueError("cu_prefix and cu_nodes must hold B + 1 entries each")
     rows = cache[0][1].shape[0]
     for label, t, _, row in cache:
         if t.dim() != 3 or t.shape[0] != rows or t.shape[1] != Hkv or t.shape[2] != row:
@@ -467,12 +488,13 @@ def _window_attention(name, window, sinks, q, cache, tree_k, tree_v, parent, cu_
     code = getattr(load_library(), name)(
         ctypes.byref(p), int(window), int(sinks), q.data_ptr(), *(c[1].data_ptr() for c in cache), tree_k.data_ptr(),
         tree_v.data_ptr(), parent.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        dev_status.data_ptr(), _raw_stream(stream, here))
+        dev_status.data_ptr(), _raw_stream(here))
     if code:
         _check(code, name)
     return out, lse
 
 
+@_on_stream
 def tree_verify_attn_window_varlen(q, k_cache, v_cache, tree_k, tree_v, parent, cu_prefix, cu_nodes,
                                    max_prefix_len, max_nodes, window, sinks=0, out=None, lse=None, workspace=None,
                                    dev_status=None, softmax_scale=0.0, stream=None, params=None):
@@ -483,9 +505,10 @@ def tree_verify_attn_window_varlen(q, k_cache, v_cache, tree_k, tree_v, parent, 
     return _window_attention("tree_verify_attn_window_varlen", window, sinks, q,
                              (("k_cache", k_cache, q.dtype, d), ("v_cache", v_cache, q.dtype, d)), tree_k, tree_v,
                              parent, cu_prefix, cu_nodes, max_prefix_len, max_nodes, out, lse, workspace, dev_status,
-                             softmax_scale, stream, params)
+                             softmax_scale, params)
 
 
+@_on_stream
 def tree_verify_attn_kv4_varlen(q, kv4_cache, tree_k, tree_v, parent, cu_prefix, cu_nodes, max_prefix_len,
                                 max_nodes, window=0, sinks=0, out=None, lse=None, workspace=None, dev_status=None,
                                 softmax_scale=0.0, stream=None, params=None):
@@ -495,7 +518,7 @@ def tree_verify_attn_kv4_varlen(q, kv4_cache, tree_k, tree_v, parent, cu_prefix,
     return _window_attention("tree_verify_attn_kv4_varlen", window, sinks, q,
                              (("kv4_cache", kv4_cache, torch.uint8, kv4_record_bytes(q.shape[-1])),), tree_k, tree_v,
                              parent, cu_prefix, cu_nodes, max_prefix_len, max_nodes, out, lse, workspace, dev_status,
-                             softmax_scale, stream, params)
+                             softmax_scale, params)
 
 
 _record_bytes = {}
@@ -530,6 +553,7 @@ def _check_rows(k, v):
         raise ValueError("k and v must be [rows, Hkv, d], alike")
 
 
+@_on_stream
 def append_kv4(k, v, slot, kv4_cache, dev_status=None, stream=None):
     """Quantises k, v [n, Hkv, d] into rows slot[i] (int32; negative: skipped) of the 4-bit
     cache, in place.  Returns dev_status (int32 [1], 0 = ok)."""
@@ -543,12 +567,13 @@ def append_kv4(k, v, slot, kv4_cache, dev_status=None, stream=None):
     dev_status = _status_word(dev_status, k.device)
     code = load_library().append_kv4(n, Hkv, d, DTYPES[k.dtype], kv4_cache.shape[0], k.data_ptr(), v.data_ptr(),
                                      slot.data_ptr(), kv4_cache.data_ptr(), dev_status.data_ptr(),
-                                     _raw_stream(stream, here))
+                                     _raw_stream(here))
     if code:
         _check(code, "append_kv4")
     return dev_status
 
 
+@_on_stream
 def read_kv4(kv4_cache, head_dim, slot=None, dtype=torch.bfloat16, k=None, v=None, dev_status=None, stream=None):
     """(k, v) [n, Hkv, head_dim] of ``dtype``: the values that rows slot[i] (int32; negative:
     zeros) of the 4-bit cache stand for, or all rows in order when ``slot`` is None."""
@@ -574,12 +599,13 @@ def read_kv4(kv4_cache, head_dim, slot=None, dtype=torch.bfloat16, k=None, v=Non
     dev_status = _status_word(dev_status, kv4_cache.device)
     code = load_library().read_kv4(n, Hkv, shape[2], DTYPES[dtype], rows, kv4_cache.data_ptr(),
                                    None if slot is None else slot.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                   dev_status.data_ptr(), _raw_stream(stream, here))
+                                   dev_status.data_ptr(), _raw_stream(here))
     if code:
         _check(code, "read_kv4")
     return k, v
 
 
+@_on_stream
 def commit_accepted_kv4(cu_nodes, accept_len, accept_path, tree_k, tree_v, dst_row, kv4_cache, max_nodes=None,
                         dev_status=None, stream=None):
     """commit_accepted_kv into a 4-bit cache [rows, Hkv, record], in place.  Returns
@@ -600,7 +626,7 @@ def commit_accepted_kv4(cu_nodes, accept_len, accept_path, tree_k, tree_v, dst_r
     code = load_library().commit_accepted_kv4(
         B, Hkv, d, DTYPES[dt], N, max(1, int(max_nodes)), kv4_cache.shape[0], cu_nodes.data_ptr(),
         accept_len.data_ptr(), accept_path.data_ptr(), tree_k.data_ptr(), tree_v.data_ptr(), dst_row.data_ptr(),
-        kv4_cache.data_ptr(), dev_status.data_ptr(), _raw_stream(stream, here))
+        kv4_cache.data_ptr(), dev_status.data_ptr(), _raw_stream(here))
     if code:
         _check(code, "commit_accepted_kv4")
     return dev_status
