@@ -254,7 +254,8 @@ tva_status commit_accepted_kv(int batch, int num_kv_heads, int head_dim, tva_dty
  * lse covers the keys that the row sees.  The work and the bytes read grow with
  * min(P_b, window + sinks), not with P_b.  A K / V row of the cache that no node of its
  * sequence sees may hold anything, NaN included; a V row that some node of the sequence
- * sees must be finite (one weight of a product is zero for the nodes that do not see it). */
+ * sees must be finite (one weight of a product is zero for the nodes that do not see it).
+ * tva_diag_use_cta_pair does not apply here: size the workspace with it off. */
 tva_status tree_verify_attn_window_varlen(const tva_params* p, int window, int sinks, const void* q,
                                           const void* k_cache, const void* v_cache, const void* tree_k,
                                           const void* tree_v, const int32_t* parent, void* out, float* lse,

@@ -38,7 +38,6 @@ namespace {
 
 using namespace ptx;
 
-
 constexpr int kHalfBytes = 128 * 128;  // 128 rows of 64 16-bit values (one swizzle span)
 // The warps of a kernel for row groups of W M-tiles, and the registers per thread of its
 // warpgroups (two of softmax, the widening ones, the rest).  They share what the block is
@@ -100,31 +99,26 @@ __device__ __forceinline__ int ring_v(int W, int k, int n) {
   return W == 2 ? 2 * k + 1 : (k <= n - 2 ? 2 + 2 * k : 2 * n - 1);
 }
 
-// One row's K or V values (codes at `codes`, scales at `scales`, both shared
-// addresses) into a swizzled tile, from 16-byte chunk `chunk0` of the row on; the row starts
-// at `row`, with the swizzle's row term already in it.  All loads come first.
+// One row's K or V values (codes at `codes`, scales at `scales`, both shared addresses) into
+// a swizzled tile whose row starts at `row`, the swizzle's row term already in it.  All loads
+// come first.
 template <int D, bool kBF16>
 __device__ __forceinline__ void widen_row(uint32_t codes, uint32_t scales, uint32_t row) {
-  constexpr int kVals = D;
-  uint4 code[kVals / 32];
-  uint32_t sc = 0u, sc1 = 0u, s[kVals / 16], c[kVals / 16];
+  uint4 code[D / 32];
+  uint32_t sc1 = 0u, s[D / 16], c[D / 16];
 #pragma unroll
-  for (int q = 0; q < kVals / 32; ++q) code[q] = ld_shared_v4(codes + 16 * q);
-  if constexpr (kVals == 32) {
-    sc = ld_shared_u16(scales);
-  } else {
-    sc = ld_shared(scales);
-    if constexpr (kVals == 128) sc1 = ld_shared(scales + 4);
-  }
+  for (int q = 0; q < D / 32; ++q) code[q] = ld_shared_v4(codes + 16 * q);
+  const uint32_t sc = ld_shared(scales);
+  if constexpr (D == 128) sc1 = ld_shared(scales + 4);
 #pragma unroll
-  for (int b = 0; b < kVals / 16; ++b) widen_scale<kBF16>(b < 4 ? sc : sc1, b & 3, s[b], c[b]);
+  for (int b = 0; b < D / 16; ++b) widen_scale<kBF16>(b < 4 ? sc : sc1, b & 3, s[b], c[b]);
 #pragma unroll
-  for (int i = 0; i < (kVals < 64 ? kVals / 8 : 8); ++i) {  // chunk i of a span (of both when a thread has both)
+  for (int i = 0; i < 8; ++i) {  // chunk i of a span (of both at d = 128)
     const uint32_t at = row ^ (uint32_t)(i << 4);
     const uint4 v = code[i >> 2];
     const uint32_t w = (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
     st_shared_v4_at<0>(at, widen8<kBF16>(w, s[i >> 1], c[i >> 1]));
-    if constexpr (kVals == 128) {
+    if constexpr (D == 128) {
       const uint4 v1 = code[2 + (i >> 2)];
       const uint32_t w1 = (i & 3) == 0 ? v1.x : (i & 3) == 1 ? v1.y : (i & 3) == 2 ? v1.z : v1.w;
       st_shared_v4_at<kHalfBytes>(at, widen8<kBF16>(w1, s[4 + (i >> 1)], c[4 + (i >> 1)]));
