@@ -62,14 +62,14 @@ struct Roles {
                 "register split");
 };
 
-template <int D>
+template <int D, int W>
 struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kHalves * kHalfBytes;
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kStages = (D == 128 ? 3 : 6) + (W == 1 ? 1 : 0);
   static constexpr int kRawBytes = kKeyTile * kv4_record_bytes(D);
   static constexpr int kRaws = D == 128 ? 3 : 6;
-  static constexpr int kQBytes = 2 * kHalves * kHalfBytes;
+  static constexpr int kQBytes = W * kTileBytes;
   static constexpr int kRawOff = kQBytes + kStages * kTileBytes;
   static constexpr int kBarOff = kRawOff + kRaws * kRawBytes;
   static constexpr int kCuOff = 4096;               // staged cu_* arrays inside misc
@@ -88,9 +88,6 @@ struct Kv4Args {
   uint64_t wait_ns;  // limit of every main-loop wait
   int stall;         // test hook: the MMA thread first waits on a barrier nothing completes
 };
-
-__device__ __forceinline__ int q_buffer(int W, int sg) { return W == 1 ? (sg & 1) : 0; }
-__device__ __forceinline__ int q_use(int W, int sg) { return W == 1 ? (sg >> 1) : sg; }
 
 // Ring positions of a segment's K and V tiles, after those of the earlier segments.  With
 // W = 2: K0 V0 K1 V1 ..; with W = 1: K0, K1, then V_j followed by K_{j+2}.
@@ -150,7 +147,7 @@ __global__ void __launch_bounds__(Roles<W>::kThreads, 1)
     partials_kv4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_raw,
                         const __grid_constant__ CUtensorMap tm_tk, const __grid_constant__ CUtensorMap tm_tv,
                         const Kv4Args args) {
-  using C = Cfg<D>;
+  using C = Cfg<D, W>;
   using R = Roles<W>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -172,9 +169,9 @@ __global__ void __launch_bounds__(Roles<W>::kThreads, 1)
   const uint32_t KV_EMPTY = KV_FULL + 8 * C::kStages;     // [kStages]
   const uint32_t RAW_FULL = KV_EMPTY + 8 * C::kStages;    // [kRaws]
   const uint32_t RAW_EMPTY = RAW_FULL + 8 * C::kRaws;     // [kRaws], 4 widening warps
-  const uint32_t Q_FULL = RAW_EMPTY + 8 * C::kRaws;       // [2]
-  const uint32_t Q_EMPTY = Q_FULL + 16;                   // [2]
-  const uint32_t S_FULL = Q_EMPTY + 16;                   // [2]
+  const uint32_t Q_FULL = RAW_EMPTY + 8 * C::kRaws;
+  const uint32_t Q_EMPTY = Q_FULL + 8;
+  const uint32_t S_FULL = Q_EMPTY + 8;                    // [2]
   const uint32_t P_FULL = S_FULL + 16;                    // [2]
   const uint32_t O_FULL = P_FULL + 16;                    // [2]
   const uint32_t TREE_FULL = O_FULL + 16;                 // [2]: the tree tile's K, V have landed
@@ -203,9 +200,9 @@ __global__ void __launch_bounds__(Roles<W>::kThreads, 1)
       mbar_init(RAW_FULL + 8 * s, 1);
       mbar_init(RAW_EMPTY + 8 * s, 4 * R::kWidenGroups);
     }
+    mbar_init(Q_FULL, 1);
+    mbar_init(Q_EMPTY, 1);
     for (int w = 0; w < 2; ++w) {
-      mbar_init(Q_FULL + 8 * w, 1);
-      mbar_init(Q_EMPTY + 8 * w, 1);
       mbar_init(S_FULL + 8 * w, 1);
       mbar_init(P_FULL + 8 * w, 128);
       mbar_init(O_FULL + 8 * w, 1);
@@ -263,15 +260,13 @@ __global__ void __launch_bounds__(Roles<W>::kThreads, 1)
         const bool tree = S.tile0 == 0;
         const int n_raw = n - (tree ? 1 : 0);
         auto load_q = [&]() -> bool {
-          const int qb = q_buffer(W, sg), quse = q_use(W, sg);
-          if (quse > 0 && !warp_wait(Q_EMPTY + 8 * qb, (quse - 1) & 1, abort_flag, wait_ns)) return false;
-          mbar_expect_tx_elect(Q_FULL + 8 * qb, (uint32_t)W * C::kHalves * q_box_bytes);
+          if (sg > 0 && !warp_wait(Q_EMPTY, (sg - 1) & 1, abort_flag, wait_ns)) return false;
+          mbar_expect_tx_elect(Q_FULL, (uint32_t)W * C::kHalves * q_box_bytes);
           for (int mt = 0; mt < W; ++mt) {
             int qrow = L.s.n0 + (L.mp * W + mt) * npt;  // past the sequence's nodes: padding rows
             if (!TVA_CHECK(qrow >= L.s.n0 && L.g >= 0 && L.g < pr.Hkv, a.status)) qrow = 0;
             for (int h = 0; h < C::kHalves; ++h)
-              tma_load_3d_elect(q_s + ((qb + mt) * C::kHalves + h) * kHalfBytes, &tm_q, 64 * h, L.g * G, qrow,
-                                Q_FULL + 8 * qb);
+              tma_load_3d_elect(q_s + (mt * C::kHalves + h) * kHalfBytes, &tm_q, 64 * h, L.g * G, qrow, Q_FULL);
           }
           ++q_loads;
           return true;
@@ -299,10 +294,7 @@ __global__ void __launch_bounds__(Roles<W>::kThreads, 1)
       // drain: every copy this thread started has landed before TMEM / smem go away
       for (int i = max(0, raw - C::kRaws); i < raw; ++i)
         drain_wait(RAW_FULL + 8 * (i % C::kRaws), (i / C::kRaws) & 1);
-      for (int b = 0; b < 2; ++b) {  // the last load into each Q buffer
-        const int uses = (W == 1) ? (q_loads + 1 - b) / 2 : (b == 0 ? q_loads : 0);
-        if (uses > 0) drain_wait(Q_FULL + 8 * b, (uses - 1) & 1);
-      }
+      if (q_loads > 0) drain_wait(Q_FULL, (q_loads - 1) & 1);
     } else if (warp == R::kMmaWarp) {
       // ---------------------------------------------------------------- MMA issuer
       // All 32 lanes run this role; the *_elect forms issue each MMA / commit from one lane.
@@ -324,10 +316,9 @@ __global__ void __launch_bounds__(Roles<W>::kThreads, 1)
       const uint32_t k_lo = (uint32_t)sdesc_sw128(kv_s, 16, 1024);
       const uint32_t v_lo = (uint32_t)sdesc_sw128(kv_s, kHalfBytes, 1024);
       const uint32_t q_lo = (uint32_t)sdesc_sw128(q_s, 16, 1024);
-      int qb = 0;  // Q buffer of the current segment
       auto issue_s = [&](int w, int mt, int idx) {
         const uint32_t kl = k_lo + (uint32_t)((idx % C::kStages) * C::kTileBytes >> 4);
-        const uint32_t ql = q_lo + (uint32_t)((qb + mt) * C::kHalves * kHalfBytes >> 4);
+        const uint32_t ql = q_lo + (uint32_t)(mt * C::kTileBytes >> 4);
         const uint32_t dt = tmem + w * 128;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -359,8 +350,7 @@ __global__ void __launch_bounds__(Roles<W>::kThreads, 1)
       if (args.stall && !warp_wait(DRAIN, 0, abort_flag, wait_ns)) ok = false;  // test hook
       while (ok && next_segment(pr, u, t, t_end, S, kShare)) {
         const int n = S.n;
-        qb = q_buffer(W, sg);
-        if (!warp_wait(Q_FULL + 8 * qb, q_use(W, sg) & 1, abort_flag, wait_ns)) { ok = false; break; }
+        if (!warp_wait(Q_FULL, sg & 1, abort_flag, wait_ns)) { ok = false; break; }
         tc_fence_after();
         auto rK = [&](int k) { return ring + ring_k(W, k); };
         auto rV = [&](int k) { return ring + ring_v(W, k, n); };
@@ -369,7 +359,7 @@ __global__ void __launch_bounds__(Roles<W>::kThreads, 1)
         if (W == 2) {
           issue_s(1, 1, rK(0));
           free_kv(rK(0));
-          if (n == 1) tc_commit_elect(Q_EMPTY + 8 * qb);
+          if (n == 1) tc_commit_elect(Q_EMPTY);
           for (int k = 0; k < n && ok; ++k) {
             if (!(ok = wait_kv(rV(k)))) break;
             for (int w = 0; w < 2 && ok; ++w) {
@@ -384,7 +374,7 @@ __global__ void __launch_bounds__(Roles<W>::kThreads, 1)
                 issue_s(w, w, rK(k + 1));
                 if (w == 1) {
                   free_kv(rK(k + 1));
-                  if (k + 1 == n - 1) tc_commit_elect(Q_EMPTY + 8 * qb);
+                  if (k + 1 == n - 1) tc_commit_elect(Q_EMPTY);
                 }
               }
             }
@@ -396,7 +386,7 @@ __global__ void __launch_bounds__(Roles<W>::kThreads, 1)
             issue_s(1, 0, rK(1));
             free_kv(rK(1));
           }
-          if (n <= 2) tc_commit_elect(Q_EMPTY + 8 * qb);
+          if (n <= 2) tc_commit_elect(Q_EMPTY);
           for (int j = 0; j < n && ok; ++j) {
             const int w = j & 1;
             if (!(ok = wait_kv(rV(j)))) break;
@@ -410,7 +400,7 @@ __global__ void __launch_bounds__(Roles<W>::kThreads, 1)
               if (!(ok = wait_kv(rK(j + 2)))) break;
               issue_s(w, 0, rK(j + 2));
               free_kv(rK(j + 2));
-              if (j + 2 == n - 1) tc_commit_elect(Q_EMPTY + 8 * qb);
+              if (j + 2 == n - 1) tc_commit_elect(Q_EMPTY);
             }
           }
         }
@@ -751,7 +741,7 @@ cudaError_t launch_typed(const WinPartialArgs& a, int npt, cudaStream_t s) {
       !make_map(&mtk, type, a.tree_k, D, pr.Hkv, pr.node_capacity, 1, tree_rows) ||
       !make_map(&mtv, type, a.tree_v, D, pr.Hkv, pr.node_capacity, 1, tree_rows))
     return cudaErrorInvalidValue;
-  constexpr int smem = Cfg<D>::kSmemBytes;
+  constexpr int smem = Cfg<D, W>::kSmemBytes;
   cudaError_t e = check_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                              "cudaFuncSetAttribute(partials_kv4_kernel)");
   if (e != cudaSuccess) return e;
