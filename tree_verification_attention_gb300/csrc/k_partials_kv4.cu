@@ -770,6 +770,8 @@ cudaError_t launch_mode(const WinPartialArgs& a, bool bf16, int npt, cudaStream_
 }  // namespace
 
 cudaError_t launch_partials_kv4(const WinPartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
+  const int rows = a.pr.G * std::min(npt, a.pr.max_nodes);  // of the largest row group
+  if (W == 1 && a.pr.share == 0 && rows <= 16) return launch_partials_kv4_rows(a, rows, bf16, s);
   if (W == 1)
     return a.pr.share != 0 ? launch_mode<true, 1>(a, bf16, npt, s) : launch_mode<false, 1>(a, bf16, npt, s);
   return a.pr.share != 0 ? launch_mode<true, 2>(a, bf16, npt, s) : launch_mode<false, 2>(a, bf16, npt, s);

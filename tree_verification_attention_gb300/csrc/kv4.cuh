@@ -87,12 +87,11 @@ __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Byte i of `scales` - a block's scale - as a pair, and the pair that takes the codes'
+// Two scale bytes (bits 0 .. 7 and 16 .. 23) as a pair, and the pair that takes the codes'
 // offset off.  Every step is exact: the scale has 4 significant bits; 136 = 8 x 17 times it
 // at most 8 (17 x 15 = 255), 24 = 8 x 3 times it 6.
 template <bool kBF16>
-__device__ __forceinline__ void widen_scale(uint32_t scales, int i, uint32_t& s, uint32_t& c) {
-  const uint32_t b = __byte_perm(scales, 0u, 0x4040u + 0x0101u * i);  // the byte in both halves
+__device__ __forceinline__ void widen_scales(uint32_t b, uint32_t& s, uint32_t& c) {
   if constexpr (kBF16) {
     s = bf2_mul(b << 4, 0x77807780u);  // exponent bias 15 -> 127: times 2^112
     c = bf2_mul(s, 0xc308c308u);       // -136
@@ -100,6 +99,11 @@ __device__ __forceinline__ void widen_scale(uint32_t scales, int i, uint32_t& s,
     s = b << 7;
     c = h2_mul(s, 0xce00ce00u);        // -24
   }
+}
+// The same for byte i of `scales` - a block's scale - in both halves.
+template <bool kBF16>
+__device__ __forceinline__ void widen_scale(uint32_t scales, int i, uint32_t& s, uint32_t& c) {
+  widen_scales<kBF16>(__byte_perm(scales, 0u, 0x4040u + 0x0101u * i), s, c);
 }
 
 // One code word (8 values) to four pairs, in the order of the elements.

@@ -147,6 +147,8 @@ cudaError_t launch_partials_tc(const PartialArgs& a, bool bf16, int W, int npt, 
 cudaError_t launch_partials_tc(const WinPartialArgs& a, bool bf16, int W, int npt, cudaStream_t s);  // under a window
 // The same over a 4-bit prefix cache (a.k_cache: the records; a.v_cache unused).
 cudaError_t launch_partials_kv4(const WinPartialArgs& a, bool bf16, int W, int npt, cudaStream_t s);
+// The same for one row group of at most `rows` <= 16 rows a KV head.
+cudaError_t launch_partials_kv4_rows(const WinPartialArgs& a, int rows, bool bf16, cudaStream_t s);
 // Row groups of two M-tiles at head_dim 128 on CTA pairs (a.pr.U = pairs); bf16 or fp16.
 cudaError_t launch_partials_pair(const PartialArgs& a, bool bf16, int npt, cudaStream_t s);
 // 3-D 16-bit tensor map over [rows][heads][d] with a box of {64, box_heads, box_rows}
