@@ -1,5 +1,5 @@
 // k_partials_kv4_rows.cu - attention partials over a 4-bit prefix cache for row groups of at
-// most 32 rows (a few tree nodes times the query heads of a KV head: the single tokens and
+// most 16 rows (a few tree nodes times the query heads of a KV head: the single tokens and
 // short drafts of a serving batch).
 //
 // What is computed is what k_partials_kv4.cu computes.  There the records are widened into
@@ -12,8 +12,9 @@
 //
 // How (one CTA per SM, kWarps computing warps and a producer):
 //   producer warp: TMA of the raw 128-record tiles into a ring.
-//   computing warps: 16 keys at a time, dealt in turn.  A warp holds all rows' Q fragments,
-//           its own running maxima, sums and O; the warps' partials meet at a segment's end.
+//   computing warps: teams of 4 (2) take the tiles in turn, a warp 16 keys at a time.  It holds
+//           all rows' Q fragments, its own running maxima, sums and O; the warps' partials
+//           meet at a segment's end.
 //   S^T = K Q^T, so that the rows are the product's short side (8 or 16 of them, not 16 or
 //           32).  The contraction index may run in any order, as long as Q's does too: lane
 //           4 g + c takes the whole code words (d / 32) c .. of keys g and g + 8, in one wide
@@ -23,6 +24,13 @@
 //           permutation of their codes puts two keys' values into the pairs that the
 //           fragments want.  The weights are transposed between the products (movmatrix).
 // The tree tile's K / V are 16-bit; their fragments are loaded from global memory.
+//
+// Measured (bf16, 8 KV heads, d = 128, back to back; k_partials_kv4.cu in brackets): 4 rows
+// over a prefix of 16384 13.7 us (22.7), of 131072 44.0 us (76.5; 3.4 TB/s of records), 32
+// sequences of 32768 330 us (527; 3.7 TB/s).  12 or 16 rows: 63 us (71 .. 75) and 435 us (496 ..
+// 527).  32 rows as four blocks spill: 122 us (75), so they stay with that kernel.  A tile's
+// widening and softmax - instructions, at about half of the issue slots - bound it now: with the
+// products taken out, the records alone stream at 131072 in 31 us.
 //
 // P is rounded to q's type for the second product, as in the other kernels; the row sums
 // take the unrounded weights, in fp32.
@@ -46,12 +54,21 @@ using namespace ptx;
 // NT: 8-row blocks of Q (1 or 2).
 template <int D, int NT>
 struct Rows {
-  static constexpr int kWarps = NT == 1 ? 15 : 11;  // with the producer: 128 or 168 registers a thread
+  // Warps, and how many of them share a tile.  A team sees every kTeams-th tile only: with all
+  // 15 warps at every tile, what a tile costs each of them beside its products was a third of
+  // the kernel (128k rows, one token: 52.8 us instead of 44.0).  With the producer that is 128
+  // registers a thread, or 168 for two blocks (teams of four: 65 us instead of 63).
+  static constexpr int kWarps = NT == 1 ? 12 : 8;
+  static constexpr int kTeam = NT == 1 ? 4 : 2;
+  static constexpr int kTeams = kWarps / kTeam;
   static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kRows = 8 * NT;
   static constexpr int kRec = kv4_record_bytes(D);
   static constexpr int kRawBytes = kKeyTile * kRec;
-  static constexpr int kStages = D == 64 || NT == 1 ? 8 : 6;
+  // A multiple of kTeams: a team then meets its stages in turn, and the parity of a stage's
+  // barrier tells its uses apart.  (Nine stages read a batch of 32 sequences slower, 370 us
+  // instead of 330.)
+  static constexpr int kStages = NT == 1 ? 6 : 8;
   static constexpr int kORow = D + 4;  // floats of a row of a warp's O in shared memory
   static constexpr int kOOff = kStages * kRawBytes;
   static constexpr int kMLOff = kOOff + 4 * kWarps * kRows * kORow;  // [2][kWarps][kRows]
@@ -61,6 +78,7 @@ struct Rows {
   static constexpr int kPrOff = kBarOff + 256;
   static constexpr int kCuOff = kPrOff + 128;
   static constexpr int kSmemBytes = kCuOff + 4 * kCuCap + 128;  // + alignment slack
+  static_assert(kStages % kTeams == 0 && kWarps % kTeam == 0, "teams");
   static_assert(kRawBytes % 128 == 0 && kMLOff % 16 == 0 && kBarOff % 16 == 0, "layout");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
@@ -126,7 +144,7 @@ __global__ void __launch_bounds__(Rows<D, NT>::kThreads, 1)
   const int u = blockIdx.x;
   const uint32_t sbase = smem_u32(smem);
   const uint32_t FULL = sbase + C::kBarOff;        // [kStages]
-  const uint32_t EMPTY = FULL + 8 * C::kStages;    // [kStages], every computing warp
+  const uint32_t EMPTY = FULL + 8 * C::kStages;    // [kStages], the team's warps
   const uint32_t STALL = EMPTY + 8 * C::kStages;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + 16 * C::kStages + 8);
 
@@ -134,7 +152,7 @@ __global__ void __launch_bounds__(Rows<D, NT>::kThreads, 1)
     prefetch_tmap(&tm_raw);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(FULL + 8 * s, 1);
-      mbar_init(EMPTY + 8 * s, kWarps);
+      mbar_init(EMPTY + 8 * s, C::kTeam);
     }
     mbar_init(STALL, 1);
     *abort_flag = 0;
@@ -179,7 +197,9 @@ __global__ void __launch_bounds__(Rows<D, NT>::kThreads, 1)
     float* const xm = reinterpret_cast<float*>(smem + C::kMLOff);
     float* const xl = xm + kWarps * C::kRows;
     int* const par = reinterpret_cast<int*>(smem + C::kParOff) + 32 * warp;
-    uint32_t stage = 0, phase = 0;
+    constexpr int kTeams = C::kTeams;
+    const int team = warp / C::kTeam;
+    uint32_t base = 0;  // tiles of the earlier segments
     bool ok = true;
     long long t = t_begin;
     Segment S;
@@ -338,8 +358,9 @@ __global__ void __launch_bounds__(Rows<D, NT>::kThreads, 1)
               true,
               [&](int nt, int x) { return anc[nt][x] >> (16 * warp); });
       }
-      int turn = (warp + kWarps - n_tree) % kWarps;  // this warp's next chunk, from the tile on
-      for (int k = tree ? 1 : 0; k < S.n; ++k) {
+      const int first = tree ? 1 : 0;
+      for (int k = first + (team + kTeams - (int)(base % kTeams)) % kTeams; k < S.n; k += kTeams) {
+        const uint32_t raw = base + (k - first), stage = raw % C::kStages, phase = raw / C::kStages & 1u;
         if (ok) ok = warp_wait(FULL + 8 * stage, phase, abort_flag, args.wait_ns);
         int key0 = 0, lim = kKeyTile;  // the tile's first key (used under a window) and its keys
         bool cut = false;
@@ -350,9 +371,8 @@ __global__ void __launch_bounds__(Rows<D, NT>::kThreads, 1)
         } else if (k == S.n - 1) {
           lim = min(kKeyTile, L.s.len - (S.tile0 + k - 1) * kKeyTile);
         }
-        for (; turn < 8 && ok; turn += kWarps) {
-          const int at = 16 * turn;  // the chunk's first row of the tile
-          if (at >= lim) continue;
+#pragma unroll 1
+        for (int at = 16 * (warp % C::kTeam); at < lim && ok; at += 16 * C::kTeam) {
           const uint32_t rec = sbase + stage * C::kRawBytes + at * C::kRec;
           // all loads first
           uint32_t kc[2][KW], vc[4][VW], ks[2], vs[4];
@@ -400,14 +420,10 @@ __global__ void __launch_bounds__(Rows<D, NT>::kThreads, 1)
                   return win ? window_bits(key0 + at, lim - at, low[nt][x], pr.sinks) : bits_below(lim - at);
                 });
         }
-        turn -= turn >= 8 ? 8 : 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(EMPTY + 8 * stage);
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
+      base += S.n - first;
 
       // ---------------------------------------------------------------- the warps' partials
 #pragma unroll
