@@ -47,3 +47,52 @@ def test_weights_that_differ_by_many_binades():
     t = pr.device()
     out, lse = pr.run(0, 0, t)
     pr.check(out, lse, 0, 0)
+
+
+def test_more_sequences_than_the_staged_arrays_hold():
+    B = 600
+    pr = _window.Problem("bf16", [(7 * b) % 300 for b in range(B)], [1] * B, (4, 1), 64, "chain", seed=21, kv4=True)
+    t = pr.device()
+    for window, sinks in ((0, 0), (100, 4)):
+        out, lse = pr.run(window, sinks, t)
+        pr.check(out, lse, window, sinks, (window, sinks))
+
+
+def test_calls_on_two_streams_and_a_replayed_graph():
+    """Two problems at once, each with its own workspace, then both captured and replayed."""
+    prs = [_window.Problem("bf16", P, m, (32, 8), 128, "random", seed=31, kv4=True)
+           for P, m in (([3000, 17, 900], [2, 1, 2]), ([5000], [4]))]
+    ts = [pr.device() for pr in prs]
+    streams = [torch.cuda.Stream() for _ in prs]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        outs = [pr.call(t, 0, 0, dev_status=st, stream=s) for pr, t, s in zip(prs, ts, streams)]
+    torch.cuda.synchronize()
+    for pr, (out, lse) in zip(prs, outs):
+        pr.check(out, lse, 0, 0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = [pr.call(t, 0, 0, dev_status=st) for pr, t in zip(prs, ts)]
+    for _ in range(3):
+        for out, lse in held:
+            out.zero_()
+            lse.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for (out, lse), (o, l) in zip(held, outs):
+            assert torch.equal(out, o) and torch.equal(lse, l)
+    assert int(st.item()) == 0
+
+
+def test_a_bad_tree_and_bad_lengths_are_reported():
+    pr = _window.Problem("bf16", [300, 40], [3, 4], (8, 2), 128, "chain", seed=33, kv4=True)
+    for name, at, value, code in (("parent", 4, 2, 3), ("parent", 1, -2, 3), ("cu_prefix", 2, 1 << 20, 1),
+                                  ("cu_nodes", 1, 6, 1)):
+        t = pr.device()
+        t[name][at] = value
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        pr.call(t, 0, 0, dev_status=st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == code, (name, at)
