@@ -21,6 +21,8 @@ CASES = [
     ([513, 0, 127, 128, 129, 1], [9, 3, 1, 17, 2, 5], (8, 2), 64, "random", 128, 1),
     ([640, 641, 5], [40, 40, 40], (32, 2), 128, "random", 260, 129),
     ([90 * i for i in range(20)], [i % 7 for i in range(1, 21)], (12, 4), 128, "random", 100, 4),
+    ([211 * i for i in range(20)], [i % 3 for i in range(1, 21)], (8, 2), 128, "random", 300, 140),  # up to 8 rows
+    ([97 * i for i in range(18)], [i % 4 for i in range(1, 19)], (20, 4), 64, "random", 0x7fffffff, 4),  # up to 15
 ]
 
 
