@@ -443,6 +443,29 @@ def _status_word(dev_status, device):
     return dev_status
 
 
+def _scale(softmax_scale, d):
+    """The logit scale that a call uses (the library's rule)."""
+    return softmax_scale if softmax_scale > 0 else d ** -0.5
+
+
+def _check_plan(p, q, Hkv, rows, cu_prefix, cu_nodes, max_prefix_len, max_nodes, softmax_scale, reported):
+    """Refuses a kept plan that is not one of this call: other tensors (a slice of a longer
+    cu_prefix starts at the same address, so the batch counts too), another scale than the
+    one asked for, or - unless ``reported``, the caller's status word, will tell - lengths
+    beyond the plan's bounds."""
+    N, Hq, d = q.shape
+    if (p.num_q_heads != Hq or p.num_kv_heads != Hkv or p.head_dim != d or p.dtype != DTYPES[q.dtype]
+            or p.batch != cu_prefix.shape[0] - 1 or p.node_capacity > N or p.kv_capacity > rows
+            or p.cu_prefix != cu_prefix.data_ptr() or p.cu_nodes != cu_nodes.data_ptr()):
+        raise ValueError("params do not describe these tensors")
+    if softmax_scale != 0:
+        mine, plans = _scale(softmax_scale, d), _scale(p.softmax_scale, d)
+        if not abs(mine - plans) <= 2.0 ** -22 * plans:  # the plan's is a float32
+            raise ValueError(f"params hold another softmax_scale ({plans}) than the call's ({mine})")
+    if not reported and (p.max_prefix_len < max_prefix_len or p.max_nodes < max_nodes):
+        raise ValueError("params were made for shorter prefixes or smaller trees than the call's")
+
+
 def _window_attention(name, window, sinks, q, cache, tree_k, tree_v, parent, cu_prefix, cu_nodes, max_prefix_len,
                       max_nodes, out, lse, workspace, dev_status, softmax_scale, params):
     """The checks and the call that the windowed and the 4-bit-cache forms share; ``cache``
@@ -467,10 +490,9 @@ def _window_attention(name, window, sinks, q, cache, tree_k, tree_v, parent, cu_
     p = params
     if p is None:
         p = make_params(q, cache[0][1], cu_prefix, cu_nodes, Hkv, max_prefix_len, max_nodes, softmax_scale)
-    elif (p.num_q_heads != Hq or p.num_kv_heads != Hkv or p.head_dim != d or p.dtype != DTYPES[dt]
-          or p.node_capacity > N or p.kv_capacity > rows or p.cu_prefix != cu_prefix.data_ptr()
-          or p.cu_nodes != cu_nodes.data_ptr()):
-        raise ValueError("params do not describe these tensors")
+    else:
+        _check_plan(p, q, Hkv, rows, cu_prefix, cu_nodes, max_prefix_len, max_nodes, softmax_scale,
+                    dev_status is not None)
     if out is None:
         out = torch.empty_like(q)
     elif out.get_device() != here or out.dtype is not dt or out.shape != q.shape or not out.is_contiguous():
