@@ -32,6 +32,7 @@ def test_a_plan_of_the_same_call_is_taken():
     t = _tensors("cpu")
     _check(t, _plan(t, 3), 3)
     _check(t, _plan(t, 3, max_prefix_len=9, max_nodes=7), 3)      # bounds may be generous
+    _check(t, _plan(t, 3), 3, None, None)                         # none named: the plan's
     for s in (0.3, 1.0 / 3.0, 7.0):
         _check(t, _plan(t, 3, softmax_scale=s), 3, softmax_scale=s)
         _check(t, _plan(t, 3, softmax_scale=s), 3)                # no scale given: the plan's

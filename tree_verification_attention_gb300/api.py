@@ -462,7 +462,8 @@ def _check_plan(p, q, Hkv, rows, cu_prefix, cu_nodes, max_prefix_len, max_nodes,
         mine, plans = _scale(softmax_scale, d), _scale(p.softmax_scale, d)
         if not abs(mine - plans) <= 2.0 ** -22 * plans:  # the plan's is a float32
             raise ValueError(f"params hold another softmax_scale ({plans}) than the call's ({mine})")
-    if not reported and (p.max_prefix_len < max_prefix_len or p.max_nodes < max_nodes):
+    if not reported and ((max_prefix_len is not None and p.max_prefix_len < max_prefix_len)
+                         or (max_nodes is not None and p.max_nodes < max_nodes)):
         raise ValueError("params were made for shorter prefixes or smaller trees than the call's")
 
 
