@@ -401,6 +401,15 @@ def tree_verify_attn_varlen_noalloc(q, k_cache, v_cache, tree_k, tree_v, parent,
 # The calls below cost the host about as much as a small call costs the GPU, so their checks
 # are few and cheap: one pass over the tensors, pointers as plain integers.
 
+def _c_int(name, value):
+    """``value`` for a C int argument: one that does not fit, which ctypes would cut to its low
+    bits, and one that is not whole are refused."""
+    n = int(value)
+    if n != value or not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} = {value} is not a 32-bit whole number")
+    return n
+
+
 def _check_all(*named):
     """Each (name, tensor, dtype): contiguous, of that type, on the current device (whose
     stream the kernels run on).  Returns that device's index."""
@@ -474,6 +483,11 @@ def _window_attention(name, window, sinks, q, cache, tree_k, tree_v, parent, cu_
     dt, i32 = q.dtype, torch.int32
     if dt not in DTYPES:
         raise ValueError(f"unsupported dtype {dt}")
+    window, sinks = _c_int("window", window), _c_int("sinks", sinks)
+    if params is None or max_prefix_len is not None:
+        max_prefix_len = _c_int("max_prefix_len", max_prefix_len)
+    if params is None or max_nodes is not None:
+        max_nodes = _c_int("max_nodes", max_nodes)
     here = _check_all(("q", q, dt), ("tree_k", tree_k, dt), ("tree_v", tree_v, dt), ("parent", parent, i32),
                       ("cu_prefix", cu_prefix, i32), ("cu_nodes", cu_nodes, i32), *(c[:3] for c in cache))
     if q.dim() != 3 or tree_k.dim() != 3 or tree_k.shape != tree_v.shape:
@@ -509,7 +523,7 @@ def _window_attention(name, window, sinks, q, cache, tree_k, tree_v, parent, cu_
         raise ValueError("workspace must be contiguous uint8, on the tensors' device")
     dev_status = _status_word(dev_status, q.device)
     code = getattr(load_library(), name)(
-        ctypes.byref(p), int(window), int(sinks), q.data_ptr(), *(c[1].data_ptr() for c in cache), tree_k.data_ptr(),
+        ctypes.byref(p), window, sinks, q.data_ptr(), *(c[1].data_ptr() for c in cache), tree_k.data_ptr(),
         tree_v.data_ptr(), parent.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
         dev_status.data_ptr(), _raw_stream(here))
     if code:
@@ -551,7 +565,7 @@ def kv4_record_bytes(head_dim: int) -> int:
     """Bytes that one row of one KV head takes in a 4-bit cache (K and V together)."""
     n = _record_bytes.get(head_dim)
     if n is None:
-        n = int(load_library().tva_kv4_record_bytes(int(head_dim)))
+        n = int(load_library().tva_kv4_record_bytes(_c_int("head_dim", head_dim)))
         if n == 0:
             raise TvaError(2, "tva_kv4_record_bytes")
         _record_bytes[head_dim] = n
@@ -634,6 +648,8 @@ def commit_accepted_kv4(cu_nodes, accept_len, accept_path, tree_k, tree_v, dst_r
     """commit_accepted_kv into a 4-bit cache [rows, Hkv, record], in place.  Returns
     dev_status (int32 [1], 0 = ok)."""
     _check_rows(tree_k, tree_v)
+    if max_nodes is not None:
+        max_nodes = _c_int("max_nodes", max_nodes)
     dt, i32 = tree_k.dtype, torch.int32
     here = _check_all(("cu_nodes", cu_nodes, i32), ("accept_len", accept_len, i32), ("accept_path", accept_path, i32),
                       ("dst_row", dst_row, i32), ("tree_k", tree_k, dt), ("tree_v", tree_v, dt),
@@ -647,7 +663,7 @@ def commit_accepted_kv4(cu_nodes, accept_len, accept_path, tree_k, tree_v, dst_r
         max_nodes = int((cu_nodes[1:] - cu_nodes[:-1]).max().item()) if B > 0 else 1
     dev_status = _status_word(dev_status, tree_k.device)
     code = load_library().commit_accepted_kv4(
-        B, Hkv, d, DTYPES[dt], N, max(1, int(max_nodes)), kv4_cache.shape[0], cu_nodes.data_ptr(),
+        B, Hkv, d, DTYPES[dt], N, max(1, max_nodes), kv4_cache.shape[0], cu_nodes.data_ptr(),
         accept_len.data_ptr(), accept_path.data_ptr(), tree_k.data_ptr(), tree_v.data_ptr(), dst_row.data_ptr(),
         kv4_cache.data_ptr(), dev_status.data_ptr(), _raw_stream(here))
     if code:
