@@ -276,9 +276,11 @@ tva_status tree_verify_attn_window_varlen(const tva_params* p, int window, int s
  * Rounding: a block's scale is its largest magnitude / 7 rounded to the nearest scale
  * (ties to the even byte; 2560 at most); a value's code is 8 + value / scale rounded to
  * the nearest whole number (ties to even), limited to 8 - 7 .. 8 + 7; all exactly, as
- * real numbers.  A value is therefore off by at most half its scale, except that
- * magnitudes beyond 7.5 * 2560 (and infinities) saturate at 7 * 2560, that a block whose
- * largest magnitude is below 7 * 2^-18 becomes 0, and that NaN becomes 0. */
+ * real numbers.  A value is therefore off by at most half its block's scale where that is
+ * 2^-14 or more.  Smaller scales are the multiples n 2^-17: a largest magnitude between two
+ * of them may lie up to 3.5 / n scales above 7 times the lower, so there a value is off by
+ * at most 7 * 2^-18, and a block whose largest magnitude is no more than that becomes 0.
+ * Magnitudes beyond 7.5 * 2560 (and infinities) saturate at 7 * 2560, and NaN becomes 0. */
 
 /* Bytes of one record, or 0 if head_dim is not 64 or 128. */
 size_t tva_kv4_record_bytes(int head_dim);
