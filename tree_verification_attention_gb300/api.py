@@ -537,7 +537,19 @@ def tree_verify_attn_window_varlen(q, k_cache, v_cache, tree_k, tree_v, parent, 
                                    dev_status=None, softmax_scale=0.0, stream=None, params=None):
     """tree_verify_attn_varlen under a sliding window: a node at position t (prefix length
     plus proper ancestors) sees the key at position s when ``t - s < window`` or
-    ``s < sinks``.  ``window`` >= 1.  Returns (out [N, Hq, d], lse [N, Hq] float32)."""
+    ``s < sinks``.  ``window`` >= 1.  Returns (out [N, Hq, d], lse [N, Hq] float32).
+
+    Errors that only the device sees - a bad tree, lengths beyond the bounds, a wait that ran
+    out - go to ``dev_status`` (int32 [1], zeroed by the caller) and leave the outputs
+    concerned unspecified.  Without it they cannot be seen: pass it, and check it after
+    synchronising.
+
+    ``params`` is a plan made by make_params for these tensors and kept; its bounds and its
+    scale are then used.  One that does not describe the tensors (their batch included) is
+    refused, and so is a ``softmax_scale`` other than its own.  Lengths of the call beyond
+    its bounds are refused without ``dev_status``, with it the device reports them.
+
+    While diag_use_cta_pair is on, pass a workspace sized with it off."""
     d = q.shape[-1]
     return _window_attention("tree_verify_attn_window_varlen", window, sinks, q,
                              (("k_cache", k_cache, q.dtype, d), ("v_cache", v_cache, q.dtype, d)), tree_k, tree_v,
@@ -551,7 +563,8 @@ def tree_verify_attn_kv4_varlen(q, kv4_cache, tree_k, tree_v, parent, cu_prefix,
                                 softmax_scale=0.0, stream=None, params=None):
     """Tree-verification attention whose prefix rows are records of a 4-bit cache; q, tree_k,
     tree_v bf16 or fp16.  ``window`` 0: the whole prefix, else as in
-    tree_verify_attn_window_varlen.  Returns (out [N, Hq, d], lse [N, Hq] float32)."""
+    tree_verify_attn_window_varlen, as are ``dev_status`` (without it a bad tree or length
+    cannot be seen) and ``params``.  Returns (out [N, Hq, d], lse [N, Hq] float32)."""
     return _window_attention("tree_verify_attn_kv4_varlen", window, sinks, q,
                              (("kv4_cache", kv4_cache, torch.uint8, kv4_record_bytes(q.shape[-1])),), tree_k, tree_v,
                              parent, cu_prefix, cu_nodes, max_prefix_len, max_nodes, out, lse, workspace, dev_status,
@@ -613,7 +626,9 @@ def append_kv4(k, v, slot, kv4_cache, dev_status=None, stream=None):
 @_on_stream
 def read_kv4(kv4_cache, head_dim, slot=None, dtype=torch.bfloat16, k=None, v=None, dev_status=None, stream=None):
     """(k, v) [n, Hkv, head_dim] of ``dtype``: the values that rows slot[i] (int32; negative:
-    zeros) of the 4-bit cache stand for, or all rows in order when ``slot`` is None."""
+    zeros) of the 4-bit cache stand for, or all rows in order when ``slot`` is None.  A slot
+    beyond the cache reads as zeros too and is reported in ``dev_status`` (int32 [1], zeroed
+    by the caller); without it that cannot be seen."""
     if dtype not in DTYPES:
         raise ValueError(f"unsupported dtype {dtype}")
     here = _check_all(("kv4_cache", kv4_cache, torch.uint8))
