@@ -28,29 +28,16 @@ constexpr int kKT = 32;       // keys per sub-tile
 constexpr int kRows = 2;      // rows per thread, kRB / kRows apart
 constexpr int kThreads = 128; // 8 threads per kRows rows: 4 keys each for QK, D/8 columns for PV
 
-template <typename T> __device__ __forceinline__ float to_f(T v);
-template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
-template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) {
-  return __bfloat162float(v);
-}
-
-// Four consecutive elements of a row (16-byte aligned for float: rows are D floats and
-// the base pointers are 16-byte aligned).
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p) {
-  if constexpr (sizeof(T) == 4) {
-    return __ldg(reinterpret_cast<const float4*>(p));
-  } else {
-    return make_float4(to_f(p[0]), to_f(p[1]), to_f(p[2]), to_f(p[3]));
-  }
-}
+// Four consecutive elements of a row (16-byte aligned: rows are D floats and the base
+// pointers are 16-byte aligned).
+__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 
 template <int D>
 constexpr size_t simt_smem_bytes() {
   return sizeof(float) * (kRB * D + kKT * D + kKT * D + kRB * (kKT + 4)) + sizeof(uint32_t) * kMaxNodes * 4;
 }
 
-template <typename T, int D, bool kWin>
+template <int D, bool kWin>
 __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgsOf<std::conditional_t<kWin, WinProblem, Problem>> a) {
   extern __shared__ float smem[];
   // The products' shared-memory reads bound the kernel: they are 16 bytes wide, and a thread
@@ -68,7 +55,7 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgsO
   __shared__ int cu_buf[512];
   auto pr = a.pr;
   stage_cu(pr, cu_buf, 512);
-  const T* __restrict__ q = static_cast<const T*>(a.q);
+  const float* __restrict__ q = static_cast<const float*>(a.q);
   const int tid = threadIdx.x;
   const int r_loc = tid >> 3;  // first row of this thread inside the block
   const int kg = tid & 7;      // key group (QK) / column phase (PV)
@@ -160,8 +147,8 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgsO
         int low[kRows];
 #pragma unroll
         for (int x = 0; x < kRows; ++x) low[x] = kWin && !is_tree ? low_s[my_node[x]] : 0;  // my_node < m
-        const T* kb = static_cast<const T*>(is_tree ? a.tree_k : a.k_cache);
-        const T* vb = static_cast<const T*>(is_tree ? a.tree_v : a.v_cache);
+        const float* kb = static_cast<const float*>(is_tree ? a.tree_k : a.k_cache);
+        const float* vb = static_cast<const float*>(is_tree ? a.tree_v : a.v_cache);
         const size_t first = is_tree ? (size_t)s.n0 : (size_t)s.p0 + (size_t)key0;
         kb += first * kv_stride + (size_t)L.g * D;
         vb += first * kv_stride + (size_t)L.g * D;
@@ -291,14 +278,14 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgsO
   }
 }
 
-template <typename T, int D, bool kWin>
+template <int D, bool kWin>
 cudaError_t launch_simt_typed(const PartialArgsOf<std::conditional_t<kWin, WinProblem, Problem>>& a, cudaStream_t s) {
   constexpr size_t smem = simt_smem_bytes<D>();
-  cudaError_t e = check_cuda(cudaFuncSetAttribute(partials_simt_kernel<T, D, kWin>,
+  cudaError_t e = check_cuda(cudaFuncSetAttribute(partials_simt_kernel<D, kWin>,
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
                              "cudaFuncSetAttribute(partials_simt_kernel)");
   if (e != cudaSuccess) return e;
-  partials_simt_kernel<T, D, kWin><<<a.pr.U, kThreads, smem, s>>>(a);
+  partials_simt_kernel<D, kWin><<<a.pr.U, kThreads, smem, s>>>(a);
   return check_cuda(cudaGetLastError(), "launch partials_simt_kernel");
 }
 
@@ -311,7 +298,7 @@ cudaError_t launch_partials_simt(const PartialArgs& a, int dtype, cudaStream_t s
     record_error("launch_partials_simt", 0, "float32 only");
     return cudaErrorInvalidValue;
   }
-  return a.pr.d == 64 ? launch_simt_typed<float, 64, false>(a, s) : launch_simt_typed<float, 128, false>(a, s);
+  return a.pr.d == 64 ? launch_simt_typed<64, false>(a, s) : launch_simt_typed<128, false>(a, s);
 }
 
 cudaError_t launch_partials_simt(const WinPartialArgs& a, int dtype, cudaStream_t s) {
@@ -319,7 +306,7 @@ cudaError_t launch_partials_simt(const WinPartialArgs& a, int dtype, cudaStream_
     record_error("launch_partials_simt", 0, "float32 only");
     return cudaErrorInvalidValue;
   }
-  return a.pr.d == 64 ? launch_simt_typed<float, 64, true>(a, s) : launch_simt_typed<float, 128, true>(a, s);
+  return a.pr.d == 64 ? launch_simt_typed<64, true>(a, s) : launch_simt_typed<128, true>(a, s);
 }
 
 }  // namespace tva

@@ -391,40 +391,6 @@ __device__ __forceinline__ Loc locate_unit(const PR& pr, long long t) {
   return L;
 }
 
-// Row group of query row (node n, head h), for the combine.
-struct RowLoc {
-  SeqInfo s;
-  int b, q, r;        // sequence, global row group, row inside the group
-  int tiles;
-  long long start;    // first unit of the row group
-  long long T;        // total units
-};
-
-template <class PR>
-__device__ __forceinline__ bool locate_row(const PR& pr, int n, int h, RowLoc& R) {
-  long long acc = 0;
-  int qacc = 0;
-  bool found = false;
-  for (int b = 0; b < pr.B; ++b) {
-    SeqInfo s = seq_info(pr, b);
-    int MP = seq_groups(pr, s.m);
-    int tiles = seq_tiles(s.P);
-    if (!found && n >= s.n0 && n < s.n0 + s.m) {
-      int g = h / pr.G, j = h % pr.G;
-      int rs = (n - s.n0) * pr.G + j;
-      int mp = rs / pr.RG;
-      R.s = s; R.b = b; R.r = rs % pr.RG; R.tiles = tiles;
-      R.q = qacc + g * MP + mp;
-      R.start = acc + (long long)(g * MP + mp) * tiles;
-      found = true;
-    }
-    acc += (long long)pr.Hkv * MP * tiles;
-    qacc += pr.Hkv * MP;
-  }
-  R.T = acc;
-  return found;
-}
-
 // ---- A worker's work.  Walk positions are units in stream-K mode and (KV head, key
 // tile) columns of the one sequence in shared mode; a segment is a maximal run of a
 // worker's positions inside one row group.
