@@ -404,8 +404,8 @@ def tree_verify_attn_varlen_noalloc(q, k_cache, v_cache, tree_k, tree_v, parent,
 def _c_int(name, value):
     """``value`` for a C int argument: one that does not fit, which ctypes would cut to its low
     bits, and one that is not whole are refused."""
-    n = int(value)
-    if n != value or not -2 ** 31 <= n < 2 ** 31:
+    n = value if type(value) is int else int(value)
+    if n != value or not -0x80000000 <= n <= 0x7fffffff:
         raise ValueError(f"{name} = {value} is not a 32-bit whole number")
     return n
 
