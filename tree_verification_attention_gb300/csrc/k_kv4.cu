@@ -12,9 +12,9 @@
 // neighbouring 32 (fp32: 64) bytes.  A thread block takes a few whole rows, so that the
 // numbers of its items stay small and dividing them by a row's items is one multiplication.
 // What they must read and write, they do once; what bounds them is instructions.  32768 rows
-// of 8 heads, d = 128, bf16 (172 MB each way): append 35.9 us (4.8 TB/s, 70 % of the issue
-// slots), read 35.4 us (65 %); the copy peak would be 25 us.  The commit of 64 sequences takes
-// 6.9 us, latency: the lengths, the path, then its rows.
+// of 8 heads, d = 128, bf16 (172 MB each way): append 34.2 us (5.0 TB/s, 70 % of the issue
+// slots), read 36.4 us (65 %); the copy peak would be 25 us.  The commit of 64 sequences takes
+// 3.4 us back to back (6.9 cold), latency: the lengths, the path, then its rows.
 #include <type_traits>
 
 #include "kv4.cuh"

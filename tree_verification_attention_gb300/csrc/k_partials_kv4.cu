@@ -26,7 +26,8 @@
 // 67 us (the products' floor 35.8); 8 sequences of 4k .. 32k rows, 32 nodes 91 us (31.2); 128
 // nodes, Hq 64, over 131072 rows 419 us (286).  No unit is saturated (tensor 46 %, issue slots
 // 46 % in the first): what bounds it is the chain of a tile - softmax, products, widening,
-// with a hand-over between each two - and issue slots shared by the widening and softmax.
+// with a hand-over between each two - and issue slots shared by the widening and softmax.  The
+// register split spills 80 to 132 bytes a thread (W = 1), 32 to 72 (W = 2).
 // Row groups of up to 16 rows go to k_partials_kv4_rows.cu, which has no such chain.
 //
 // Every wait is bounded as in k_partials_tc.cu.
@@ -51,7 +52,7 @@ constexpr int kHalfBytes = 128 * 128;  // 128 rows of 64 16-bit values (one swiz
 // launched with (checked before the first launch): a split above that would wait forever.
 //   W = 1: a widening warpgroup each for K and V.  A tile's K or V is a chain of about 1300
 //          clocks however few rows the tree has; one warpgroup for both took 3000 a tile,
-//          more than everything else (8 sequences, 4k..32k: 105 us instead of 89).
+//          more than everything else (8 sequences, 4k..32k: 105 us; 89 when it was split).
 //   W = 2: one for both.  The softmax of two M-tiles then bounds a tile and is slowed by
 //          every further warp (64k prefix, 64 nodes: 68 us instead of 72).
 template <int W>

@@ -25,12 +25,17 @@
 //           fragments want.  The weights are transposed between the products (movmatrix).
 // The tree tile's K / V are 16-bit; their fragments are loaded from global memory.
 //
-// Measured (bf16, 8 KV heads, d = 128, back to back; k_partials_kv4.cu in brackets): 4 rows
-// over a prefix of 16384 13.7 us (22.7), of 131072 44.0 us (76.5; 3.4 TB/s of records), 32
-// sequences of 32768 330 us (527; 3.7 TB/s).  12 or 16 rows: 63 us (71 .. 75) and 435 us (496 ..
-// 527).  32 rows as four blocks spill: 122 us (75), so they stay with that kernel.  A tile's
-// widening and softmax - instructions, at about half of the issue slots - bound it now: with the
-// products taken out, the records alone stream at 131072 in 31 us.
+// Measured (bf16, 8 KV heads, d = 128, back to back with the combine; k_partials_kv4.cu in
+// brackets): 4 rows over a prefix of 16384 13.8 us (22.7), of 131072 44.6 us (76.5), 32
+// sequences of 32768 321 .. 336 us (527).  12 or 16 rows: 63 us (71 .. 75) and 435 us (496 ..
+// 527).  32 rows as four blocks spill: 122 us (75), so they stay with that kernel.  (Two blocks
+// at d = 128 spill 148 bytes a thread.)
+// What bounds it (counters): 131072 rows of one sequence, no unit alone - 58 % of the issue
+// slots, DRAM at 3.4 TB/s (each record once), three warps a scheduler; of the 5.6 clocks
+// between a warp's instructions 1.1 are fixed latencies, 0.9 another warp's turn, 0.8 a busy
+// pipe, 0.7 loads.  The batch of 32, DRAM: 6.5 TB/s (82 % of its peak) of 2.15 GB, for 1.21 GB
+// of records.  That is 256 bytes a record of 144: two lines of 128 each, none of them shared
+// with the neighbouring KV heads' records, which a batch reads at another time.
 //
 // P is rounded to q's type for the second product, as in the other kernels; the row sums
 // take the unrounded weights, in fp32.

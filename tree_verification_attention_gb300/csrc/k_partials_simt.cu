@@ -11,8 +11,12 @@
 // ancestor-or-self bits of each row's node (LongSpec's tree mask; "Faster decoding",
 // "Chains and trees consume work differently").
 //
-// Shared-memory reads bound it: 5 sequences of up to 3001 rows, 13 nodes, d = 64 under a
-// window take 34.5 us with the combine (62 with scalar reads, 45 with one row a thread).
+// Shared-memory reads bound a busy CTA: 5 sequences of up to 3001 rows, 13 nodes, d = 64
+// under a window take 34.6 us with the combine (62 with scalar reads, 45 with one row a
+// thread).  That call has 136 units for 456 CTAs, so each busy one passes its unit's 128 keys
+// twice (32 rows and 7) while the others idle: finer units would shorten it.  At d = 128 two
+// rows a thread spill (28 bytes; 64 under a window) and win all the same: 16384 rows, 8 nodes,
+// Hq 32, Hkv 8, no window 117 us instead of 174 (d = 64: 62 instead of 91).
 //
 // This path carries the float32 dtype (head_dim 64 or 128).  bfloat16 inputs go to
 // the tensor-core kernel.

@@ -32,8 +32,8 @@
 // With a window (kWin; tva_common.cuh, SeqInfo) the walk covers only the key tiles that
 // some node sees; a tile that a window's lower edge crosses is masked per row.  Measured (Hq 32,
 // Hkv 8, d = 128, with the combine, back to back): a chain of 8 under a window of 512 with 4
-// sinks 15.2 us whatever the prefix (two launches and one short segment: latency); 32
-// sequences of 1k .. 32k rows under a window of 4096, fp16, 122 us (551 MB at 4.9 TB/s in the
+// sinks 15.5 us whatever the prefix (two launches and one short segment: latency); 32
+// sequences of 1k .. 32k rows under a window of 4096, fp16, 117 us (551 MB at 4.9 TB/s in the
 // partials; the rest is their epilogues and the combine).
 // TMEM columns: S/P buffers at 0 and 128, O accumulators at 256 and 384 (512 total).
 //
