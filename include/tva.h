@@ -262,6 +262,26 @@ tva_status tree_verify_attn_window_varlen(const tva_params* p, int window, int s
                                           void* workspace, size_t workspace_bytes, int32_t* dev_status,
                                           void* stream);
 
+/* Cross-attention onto a cache of another length, over a ragged batch (LongSpec's draft layers
+ * attend to the target model's K/V cache after their windowed self-attention, "Memory-Efficient
+ * Architecture"; the pages give no interface).  Every query of sequence b sees all of the
+ * sequence's P_b cached keys, without a mask, and nothing else: queries bring no keys.
+ *   p        as for tree_verify_attn_varlen, with queries in the place of tree nodes: cu_nodes
+ *            counts queries, max_nodes bounds them (<= 65536), node_capacity is the rows
+ *            of q, out and lse
+ *   q, out   [N, Hq, d], lse [N, Hq] float32, k_cache, v_cache [kv_capacity, Hkv, d] (may be
+ *            null when kv_capacity is 0)
+ *   workspace, workspace_bytes  >= tva_cross_workspace_size(p), 256-byte aligned
+ * A query of a sequence without keys (P_b = 0) gets out 0 and lse -infinity.  Rows of out and
+ * lse behind the last sequence's are left as they were, and K / V rows of no sequence may hold
+ * anything.  Errors and dev_status as for tree_verify_attn_varlen. */
+tva_status cross_attn_varlen(const tva_params* p, const void* q, const void* k_cache, const void* v_cache, void* out,
+                             float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Bytes of workspace cross_attn_varlen needs for `p` on the current device; 0 when `p` is
+ * invalid. */
+size_t tva_cross_workspace_size(const tva_params* p);
+
 /* 4-bit cache.  One cache row of one KV head is a record of tva_kv4_record_bytes(d) bytes
  * (144 at d = 128, 80 at d = 64, against 512 and 256 in 16 bits); a cache is
  * [kv_capacity, Hkv, record], 16-byte aligned.  A record is
@@ -381,6 +401,42 @@ tva_status gdn_tree_verify(int batch, int num_heads, int head_dim, tva_dtype dty
                            int max_nodes, const int32_t* cu_nodes, const int32_t* parent, const void* q,
                            const void* k, const void* v, const float* beta, const float* alpha, const float* S0,
                            void* out, int32_t* dev_status, void* stream);
+
+/* A Gated DeltaNet layer's tokens ("DFlash-TfM", Method 3: the update whose commit its tree
+ * verification defers): every sequence's tokens through
+ *   S_t = alpha_t (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,   o_t = S_t^T q_t,
+ * from its committed state, which is updated in place: single tokens of ordinary decoding, whole
+ * prompts, or both in one batch.  The state is the S0 of gdn_tree_verify.
+ *   batch, num_heads (H), head_dim (d: 64 or 128)
+ *   dtype          type of q, k, v and out: TVA_FP32 or TVA_BF16; beta, alpha and the state are fp32
+ *   token_capacity rows of q, k, v, out [token_capacity, H, d] and beta, alpha [token_capacity, H]
+ *   max_tokens     bound on every sequence's tokens (>= 0)
+ *   cu_tokens      [B+1] device int32, cu_tokens[0] = 0, non-decreasing: sequence b's tokens are rows
+ *                  cu_tokens[b] .. cu_tokens[b+1]-1, oldest first; a sequence without tokens keeps
+ *                  its state bit for bit
+ *   state          [B, H, d, d] fp32, read and written (zeros: a fresh sequence)
+ *   out            [token_capacity, H, d]: rows of no sequence are left as they were
+ * q, k, v, state and out are 16-byte aligned; the state and out overlap no other array.  Arrays of
+ * token_capacity rows may be null when it is 0.  Arithmetic is fp32; bf16 outputs are rounded
+ * once.  A sequence outside the bounds is skipped (state and output untouched) with
+ * TVA_ERR_INVALID_ARG in *dev_status. */
+tva_status gdn_update_varlen(int batch, int num_heads, int head_dim, tva_dtype dtype, int token_capacity,
+                             int max_tokens, const int32_t* cu_tokens, const void* q, const void* k, const void* v,
+                             const float* beta, const float* alpha, float* state, void* out, int32_t* dev_status,
+                             void* stream);
+
+/* Commits each sequence's accepted path into its Gated DeltaNet state ("DFlash-TfM", Method 3: the
+ * state's commit waits for the accepted branch), in place: the nodes accept_path[cu_nodes[b] + j],
+ * j < accept_len[b], root first, through the update above.  What gdn_tree_verify was given
+ * (cu_nodes, k, v, beta, alpha, S0) and the acceptance walk wrote (accept_len, accept_path) are the
+ * arguments; state [B, H, d, d] fp32 is that S0.  A sequence with accept_len 0 keeps its state
+ * bit for bit.  Types, bounds and alignment as for gdn_tree_verify; the state overlaps no other array.  A
+ * sequence whose node range, path length or path ids are out of bounds keeps its state and
+ * TVA_ERR_INVALID_ARG goes to *dev_status. */
+tva_status commit_accepted_gdn(int batch, int num_heads, int head_dim, tva_dtype dtype, int node_capacity,
+                               int max_nodes, const int32_t* cu_nodes, const int32_t* accept_len,
+                               const int32_t* accept_path, const void* k, const void* v, const float* beta,
+                               const float* alpha, float* state, int32_t* dev_status, void* stream);
 
 /* Description of the last host-side CUDA or driver failure seen by this thread
  * (the call that failed and its error string), "" if none.  Thread-local storage,

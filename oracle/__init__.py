@@ -20,6 +20,8 @@ definition.
 * :mod:`oracle.window_attention` - tree attention under a sliding window with sinks.
 * :mod:`oracle.kv4_cache` - the 4-bit K/V record: rounding, layout, values.
 * :mod:`oracle.gdn_tree` - tree verification for Gated DeltaNet layers.
+* :mod:`oracle.gdn_update` - such a layer's tokens, and the commit of an accepted path into its state.
+* :mod:`oracle.cross_attention` - cross-attention onto a cache of another length.
 
 Every function is pinned by ``tests/test_oracle_*.py`` against facts fixed by the pages
 or by mathematics (closed forms, brute force, library routines on independently
@@ -34,6 +36,8 @@ from .rejection_sampling import verify_chain_sampling, quantised_draw
 from .window_attention import tree_verify_window_attention, tree_verify_window_rows, window_visible
 from .kv4_cache import SCALES, kv4_pack, kv4_quantise, kv4_record_bytes, kv4_unpack, kv4_values
 from .gdn_tree import gdn_tree_outputs, gdn_path_state
+from .gdn_update import gdn_update, commit_accepted_gdn
+from .cross_attention import cross_attention
 
 __all__ = [
     "ancestor_mask",
@@ -59,4 +63,7 @@ __all__ = [
     "kv4_values",
     "gdn_tree_outputs",
     "gdn_path_state",
+    "gdn_update",
+    "commit_accepted_gdn",
+    "cross_attention",
 ]

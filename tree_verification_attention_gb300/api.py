@@ -21,7 +21,8 @@ __all__ = [
     "tree_verify_attn_varlen", "tree_verify_attn_partials", "tree_verify_attn_combine",
     "tree_verify_attn", "read_device_status", "release", "diag_set_wait_limit", "diag_use_cta_pair", "accept_longest_path",
     "tree_verify_attn_window_varlen", "tree_verify_attn_kv4_varlen", "kv4_record_bytes", "alloc_kv4_cache", "append_kv4",
-    "read_kv4", "commit_accepted_kv4", "status_string", "STATUS",
+    "read_kv4", "commit_accepted_kv4", "cross_attn_varlen", "alloc_cross_workspace", "gdn_update_varlen",
+    "commit_accepted_gdn", "status_string", "STATUS",
 ]
 
 STATUS = {0: "TVA_OK", 1: "TVA_ERR_INVALID_ARG", 2: "TVA_ERR_UNSUPPORTED", 3: "TVA_ERR_BAD_TREE",
@@ -87,6 +88,10 @@ def load_library(path: str | None = None):
         "append_kv4": (_I, [_I, _I, _I, _I, ctypes.c_longlong] + [_P] * 6),
         "read_kv4": (_I, [_I, _I, _I, _I, ctypes.c_longlong] + [_P] * 6),
         "commit_accepted_kv4": (_I, [_I, _I, _I, _I, _I, _I, ctypes.c_longlong] + [_P] * 9),
+        "cross_attn_varlen": (_I, [PP] + [_P] * 6 + [_SZ, _P, _P]),
+        "tva_cross_workspace_size": (_SZ, [PP]),
+        "gdn_update_varlen": (_I, [_I] * 6 + [_P] * 10),
+        "commit_accepted_gdn": (_I, [_I] * 6 + [_P] * 10),
         "tva_status_string": (ctypes.c_char_p, [_I]),
         "tva_last_error": (ctypes.c_char_p, []),
     }
@@ -683,4 +688,135 @@ def commit_accepted_kv4(cu_nodes, accept_len, accept_path, tree_k, tree_v, dst_r
         kv4_cache.data_ptr(), dev_status.data_ptr(), _raw_stream(here))
     if code:
         _check(code, "commit_accepted_kv4")
+    return dev_status
+
+
+def alloc_cross_workspace(params: Params, device) -> torch.Tensor:
+    """The workspace that cross_attn_varlen needs for a plan made by make_params."""
+    n = int(load_library().tva_cross_workspace_size(ctypes.byref(params)))
+    if n == 0:
+        raise TvaError(1, "tva_cross_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+@_on_stream
+def cross_attn_varlen(q, k_cache, v_cache, cu_queries, cu_keys, max_queries, max_keys, out=None, lse=None,
+                      workspace=None, dev_status=None, softmax_scale=0.0, stream=None, params=None):
+    """Cross-attention over a ragged batch: the queries q [N, Hq, d] of sequence b (rows
+    cu_queries[b] .. cu_queries[b + 1] - 1) see all its keys, rows cu_keys[b] .. cu_keys[b + 1] - 1
+    of k_cache / v_cache [rows, Hkv, d], without a mask.  bf16, fp16 or fp32.  Returns (out [N, Hq, d],
+    lse [N, Hq] float32): 0 and -inf for a sequence without keys; rows behind the last sequence's
+    are left as they were (unspecified when ``out`` and ``lse`` are made here).
+
+    ``params`` is a plan made by make_params(q, k_cache, cu_keys, cu_queries, Hkv, max_keys,
+    max_queries) and kept; it and ``dev_status`` work as in tree_verify_attn_window_varlen."""
+    dt, i32 = q.dtype, torch.int32
+    if dt not in DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
+    if params is None or max_keys is not None:
+        max_keys = _c_int("max_keys", max_keys)
+    if params is None or max_queries is not None:
+        max_queries = _c_int("max_queries", max_queries)
+    here = _check_all(("q", q, dt), ("k_cache", k_cache, dt), ("v_cache", v_cache, dt),
+                      ("cu_queries", cu_queries, i32), ("cu_keys", cu_keys, i32))
+    if q.dim() != 3 or k_cache.dim() != 3 or k_cache.shape != v_cache.shape or k_cache.shape[2] != q.shape[2]:
+        raise ValueError("q must be [N, Hq, d], k_cache and v_cache [rows, Hkv, d]")
+    if cu_keys.dim() != 1 or cu_queries.shape != cu_keys.shape:
+        raise ValueError("cu_queries and cu_keys must hold B + 1 entries each")
+    N, Hq, d = q.shape
+    rows, Hkv, _ = k_cache.shape
+    p = params
+    if p is None:
+        p = make_params(q, k_cache, cu_keys, cu_queries, Hkv, max_keys, max_queries, softmax_scale)
+    else:
+        _check_plan(p, q, Hkv, rows, cu_keys, cu_queries, max_keys, max_queries, softmax_scale, dev_status is not None)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.get_device() != here or out.dtype is not dt or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be like q")
+    if lse is None:
+        lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
+    elif (lse.get_device() != here or lse.dtype is not torch.float32 or lse.shape != (N, Hq)
+          or not lse.is_contiguous()):
+        raise ValueError("lse must be [N, Hq] float32")
+    if workspace is None:
+        workspace = alloc_cross_workspace(p, q.device)
+    elif workspace.get_device() != here or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8, on the tensors' device")
+    dev_status = _status_word(dev_status, q.device)
+    code = load_library().cross_attn_varlen(
+        ctypes.byref(p), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), dev_status.data_ptr(), _raw_stream(here))
+    if code:
+        _check(code, "cross_attn_varlen")
+    return out, lse
+
+
+_GDN_DTYPES = (torch.float32, torch.bfloat16)
+
+
+def _check_gdn(q, k, v, beta, alpha, cu, state):
+    """The checks that the two state calls share (q is k in a commit); returns (device index, B,
+    rows, H, d)."""
+    dt, f32 = k.dtype, torch.float32
+    if dt not in _GDN_DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
+    here = _check_all(("k", k, dt), ("q", q, dt), ("v", v, dt), ("beta", beta, f32), ("alpha", alpha, f32),
+                      ("cu", cu, torch.int32), ("state", state, f32))
+    if k.dim() != 3 or q.shape != k.shape or v.shape != k.shape:
+        raise ValueError("q, k and v must be [rows, H, d], alike")
+    n, H, d = k.shape
+    if beta.shape != (n, H) or alpha.shape != (n, H):
+        raise ValueError("beta and alpha must be [rows, H]")
+    if cu.dim() != 1 or cu.shape[0] < 2:
+        raise ValueError("the sequences' bounds must hold B + 1 entries")
+    B = cu.shape[0] - 1
+    if state.shape != (B, H, d, d):
+        raise ValueError(f"state must be [{B}, {H}, {d}, {d}] float32")
+    return here, B, n, H, d
+
+
+@_on_stream
+def gdn_update_varlen(q, k, v, beta, alpha, cu_tokens, max_tokens, state, out=None, dev_status=None, stream=None):
+    """Every sequence's tokens (rows cu_tokens[b] .. cu_tokens[b + 1] - 1, oldest first) through a
+    Gated DeltaNet layer: q, k, v [n, H, d] float32 or bfloat16, beta, alpha [n, H] and the state
+    [B, H, d, d] float32.  The state is updated in place, the outputs [n, H, d] are returned; rows of
+    no sequence are left as they were.  ``max_tokens`` bounds every sequence's tokens; one
+    beyond it is skipped and reported in ``dev_status`` (int32 [1], zeroed by the caller)."""
+    max_tokens = _c_int("max_tokens", max_tokens)
+    here, B, n, H, d = _check_gdn(q, k, v, beta, alpha, cu_tokens, state)
+    if out is None:
+        out = torch.empty_like(v)
+    elif out.get_device() != here or out.dtype is not v.dtype or out.shape != v.shape or not out.is_contiguous():
+        raise ValueError("out must be like v")
+    dev_status = _status_word(dev_status, q.device)
+    code = load_library().gdn_update_varlen(
+        B, H, d, DTYPES[k.dtype], n, max_tokens, cu_tokens.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        beta.data_ptr(), alpha.data_ptr(), state.data_ptr(), out.data_ptr(), dev_status.data_ptr(), _raw_stream(here))
+    if code:
+        _check(code, "gdn_update_varlen")
+    return out
+
+
+@_on_stream
+def commit_accepted_gdn(cu_nodes, accept_len, accept_path, k, v, beta, alpha, state, max_nodes=None, dev_status=None,
+                        stream=None):
+    """Commits each sequence's accepted path (accept_longest_path's accept_len [B] and accept_path
+    [N]) into its Gated DeltaNet state [B, H, d, d], in place; cu_nodes, k, v, beta and alpha are
+    what gdn_tree_verify was given.  Returns dev_status (int32 [1], 0 = ok)."""
+    if max_nodes is not None:
+        max_nodes = _c_int("max_nodes", max_nodes)
+    here, B, n, H, d = _check_gdn(k, k, v, beta, alpha, cu_nodes, state)
+    _check_all(("k", k, k.dtype), ("accept_len", accept_len, torch.int32), ("accept_path", accept_path, torch.int32))
+    if accept_len.shape != (B,) or accept_path.shape != (n,):
+        raise ValueError("accept_len must hold B entries and accept_path one per node")
+    if max_nodes is None:
+        max_nodes = int((cu_nodes[1:] - cu_nodes[:-1]).max().item())
+    dev_status = _status_word(dev_status, k.device)
+    code = load_library().commit_accepted_gdn(
+        B, H, d, DTYPES[k.dtype], n, max(1, max_nodes), cu_nodes.data_ptr(), accept_len.data_ptr(),
+        accept_path.data_ptr(), k.data_ptr(), v.data_ptr(), beta.data_ptr(), alpha.data_ptr(), state.data_ptr(),
+        dev_status.data_ptr(), _raw_stream(here))
+    if code:
+        _check(code, "commit_accepted_gdn")
     return dev_status

@@ -32,11 +32,12 @@ namespace {
 // Writes one merged row piece: out = acc / den (CG column groups from cs * CG) in T, and
 // (for the first column set) lse = (Ms + log2 den) * ln 2 for row r (node `node`) of the
 // row group R.
-template <typename T, int D, int CG>
+template <typename T, int D, int CG, bool kCross>
 __device__ __forceinline__ void store_merged(const Problem& pr, const GroupLoc& R, int node, int r, int cs,
                                              const float4 (&acc)[CG], float den, float Ms, void* out_v,
                                              float* lse_out, int32_t* status) {
-  const float inv = 1.f / den;
+  // a query that sees no key: sum 0, output 0, log-sum-exp -inf
+  const float inv = kCross && den == 0.f ? 0.f : 1.f / den;
   const int head = R.g * pr.G + r % pr.G;
   if (!TVA_CHECK(R.s.n0 + node < pr.node_capacity && head < pr.Hq && (cs + 1) * CG * 4 <= D, status)) return;
   const size_t orow = ((size_t)(R.s.n0 + node) * pr.Hq + head) * D + (size_t)cs * CG * 4;
@@ -74,7 +75,7 @@ __device__ __forceinline__ void store_merged(const Problem& pr, const GroupLoc& 
 // covered it), so all lanes run the same loops and no shuffles are needed; the loads of
 // up to NB partials are issued in one round.  Lanes whose row is padding return without
 // touching memory; nothing here synchronises the warp.
-template <typename T, int D, int CG, int NB>
+template <typename T, int D, int CG, int NB, bool kCross>
 __device__ __forceinline__ void merge_rows(const Problem& pr, const float* o_part, const float* lse_part,
                                            const GroupLoc& R, size_t slot0, int np, int rb, int cs, int lane,
                                            void* out_v, float* lse_out, int32_t* status) {
@@ -134,7 +135,7 @@ __device__ __forceinline__ void merge_rows(const Problem& pr, const float* o_par
     M = Mr;
   }
   const float Ms = (M == -INFINITY) ? 0.f : M;
-  store_merged<T, D, CG>(pr, R, node, r, cs, acc, den, Ms, out_v, lse_out, status);
+  store_merged<T, D, CG, kCross>(pr, R, node, r, cs, acc, den, Ms, out_v, lse_out, status);
 }
 
 
@@ -163,7 +164,9 @@ __global__ void __launch_bounds__(32 * WPB) combine_kernel(CombineArgsOf<PR> a) 
   // group's partials are in consecutive slots; see partial_slot)
   long long slot0;
   int np;
-  if (pr.share == 0 && pr.align > 0) {  // the group's own workers, the first min(align, tiles) busy
+  if (PR::kCross && R.tiles == 0) {  // no keys, no partials
+    slot0 = np = 0;
+  } else if (pr.share == 0 && pr.align > 0) {  // the group's own workers, the first min(align, tiles) busy
     const int u0 = (int)qg * pr.align;
     np = R.tiles < pr.align ? R.tiles : pr.align;
     slot0 = (long long)u0 + qg;
@@ -185,7 +188,7 @@ __global__ void __launch_bounds__(32 * WPB) combine_kernel(CombineArgsOf<PR> a) 
   }
   ptx::pdl_wait();  // the partials (and every earlier write) are visible after this
   ptx::pdl_launch_dependents();
-  merge_rows<T, D, CG, NB>(pr, a.o_part, a.lse_part, R, (size_t)slot0, np, rb, cs, lane, a.out, a.lse,
+  merge_rows<T, D, CG, NB, PR::kCross>(pr, a.o_part, a.lse_part, R, (size_t)slot0, np, rb, cs, lane, a.out, a.lse,
                            a.status);
 }
 
@@ -281,5 +284,6 @@ cudaError_t launch_any(const CombineArgsOf<PR>& a, int dtype, cudaStream_t s) {
 
 cudaError_t launch_combine(const CombineArgs& a, int dtype, cudaStream_t s) { return launch_any(a, dtype, s); }
 cudaError_t launch_combine(const WinCombineArgs& a, int dtype, cudaStream_t s) { return launch_any(a, dtype, s); }
+cudaError_t launch_combine(const CrossCombineArgs& a, int dtype, cudaStream_t s) { return launch_any(a, dtype, s); }
 
 }  // namespace tva

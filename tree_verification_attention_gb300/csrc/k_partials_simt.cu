@@ -41,8 +41,10 @@ constexpr size_t simt_smem_bytes() {
   return sizeof(float) * (kRB * D + kKT * D + kKT * D + kRB * (kKT + 4)) + sizeof(uint32_t) * kMaxNodes * 4;
 }
 
-template <int D, bool kWin>
-__global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgsOf<std::conditional_t<kWin, WinProblem, Problem>> a) {
+// PR: Problem (the plain form), WinProblem (under a window) or CrossProblem (no tree).
+template <int D, class PR>
+__global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgsOf<PR> a) {
+  constexpr bool kCross = PR::kCross, kWin = PR::kWindowed && !kCross;
   extern __shared__ float smem[];
   // The products' shared-memory reads bound the kernel: they are 16 bytes wide, and a thread
   // uses each K and V value for two rows.  Chunk c (4 floats) of row r of qs is at c ^ (r mod 8), of key r of ks
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgsO
     const Loc L = S.L;
     const int tile0 = S.tile0;
     const int tile1 = S.tile0 + S.n;
-    const bool has_tree = tile0 == 0;   // the tree tile is a row group's first unit
+    const bool has_tree = !kCross && tile0 == 0;   // the tree tile is a row group's first unit
     const SeqInfo s = L.s;
     const long long slot = partial_slot(pr, u, L, pr.share != 0);
     const bool slot_ok = slot < a.slots;  // cannot fail for a consistent layout
@@ -139,8 +141,8 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgsO
       }
 
       for (int tile = tile0; tile < tile1; ++tile) {
-        const bool is_tree = tile == 0;
-        int key0 = (tile - 1) * kKeyTile, nkeys = is_tree ? s.m : min(kKeyTile, s.P - key0), sinks = 0;
+        const bool is_tree = !kCross && tile == 0;
+        int key0 = (kCross ? tile : tile - 1) * kKeyTile, nkeys = is_tree ? s.m : min(kKeyTile, s.P - key0), sinks = 0;
         if constexpr (kWin) {
           sinks = pr.sinks;
           if (!is_tree) {
@@ -282,14 +284,14 @@ __global__ void __launch_bounds__(kThreads, 3) partials_simt_kernel(PartialArgsO
   }
 }
 
-template <int D, bool kWin>
-cudaError_t launch_simt_typed(const PartialArgsOf<std::conditional_t<kWin, WinProblem, Problem>>& a, cudaStream_t s) {
+template <int D, class PR>
+cudaError_t launch_simt_typed(const PartialArgsOf<PR>& a, cudaStream_t s) {
   constexpr size_t smem = simt_smem_bytes<D>();
-  cudaError_t e = check_cuda(cudaFuncSetAttribute(partials_simt_kernel<D, kWin>,
+  cudaError_t e = check_cuda(cudaFuncSetAttribute(partials_simt_kernel<D, PR>,
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
                              "cudaFuncSetAttribute(partials_simt_kernel)");
   if (e != cudaSuccess) return e;
-  partials_simt_kernel<D, kWin><<<a.pr.U, kThreads, smem, s>>>(a);
+  partials_simt_kernel<D, PR><<<a.pr.U, kThreads, smem, s>>>(a);
   return check_cuda(cudaGetLastError(), "launch partials_simt_kernel");
 }
 
@@ -302,7 +304,7 @@ cudaError_t launch_partials_simt(const PartialArgs& a, int dtype, cudaStream_t s
     record_error("launch_partials_simt", 0, "float32 only");
     return cudaErrorInvalidValue;
   }
-  return a.pr.d == 64 ? launch_simt_typed<64, false>(a, s) : launch_simt_typed<128, false>(a, s);
+  return a.pr.d == 64 ? launch_simt_typed<64, Problem>(a, s) : launch_simt_typed<128, Problem>(a, s);
 }
 
 cudaError_t launch_partials_simt(const WinPartialArgs& a, int dtype, cudaStream_t s) {
@@ -310,7 +312,15 @@ cudaError_t launch_partials_simt(const WinPartialArgs& a, int dtype, cudaStream_
     record_error("launch_partials_simt", 0, "float32 only");
     return cudaErrorInvalidValue;
   }
-  return a.pr.d == 64 ? launch_simt_typed<64, true>(a, s) : launch_simt_typed<128, true>(a, s);
+  return a.pr.d == 64 ? launch_simt_typed<64, WinProblem>(a, s) : launch_simt_typed<128, WinProblem>(a, s);
+}
+
+cudaError_t launch_partials_simt(const CrossPartialArgs& a, int dtype, cudaStream_t s) {
+  if (dtype != 1) {
+    record_error("launch_partials_simt", 0, "float32 only");
+    return cudaErrorInvalidValue;
+  }
+  return a.pr.d == 64 ? launch_simt_typed<64, CrossProblem>(a, s) : launch_simt_typed<128, CrossProblem>(a, s);
 }
 
 }  // namespace tva

@@ -75,16 +75,13 @@ struct Cfg {
   static constexpr int kSmemBytes = kBarOff + kMiscBytes + 1024;  // + alignment slack
 };
 
-// The windowed kernels' problem, and the plain ones'.
-template <bool kWin>
-using ProblemOf = std::conditional_t<kWin, WinProblem, Problem>;
-
-template <bool kWin>
+// PR: Problem (the plain form), WinProblem (under a window) or CrossProblem (no tree).
+template <class PR>
 struct TcArgs {
-  PartialArgsOf<ProblemOf<kWin>> a;
+  PartialArgsOf<PR> a;
   int W;    // M-tiles per row group (1 or 2)
   int npt;  // nodes per M-tile: floor(128 / G)
-  // kWin: what is fetched of an M-tile's nodes and of the tree tile's rows, no more than the
+  // Not plain: what is fetched of an M-tile's nodes and of the tree tile's rows, no more than the
   // largest tree has (a TMA copy takes time for each row of its box; V rows beyond are
   // zeroed, and the logits of K rows beyond masked).  Without a window, whole boxes.
   int q_nodes, tree_rows;
@@ -103,15 +100,16 @@ __device__ __forceinline__ int q_buffer(int W, int sg) { return W == 1 ? (sg & 1
 // Earlier segments that used the same buffer.
 __device__ __forceinline__ int q_use(int W, int sg) { return W == 1 ? (sg >> 1) : sg; }
 
-template <int D, bool kBF16, bool kShare, bool kWin>
+template <int D, bool kBF16, bool kShare, class PR>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     partials_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ CUtensorMap tm_tk,
-                       const __grid_constant__ CUtensorMap tm_tv, const TcArgs<kWin> args) {
+                       const __grid_constant__ CUtensorMap tm_tv, const TcArgs<PR> args) {
   using C = Cfg<D>;
-  using PR = ProblemOf<kWin>;
+  constexpr bool kWin = PR::kWindowed;          // tiles by tile_key0 / tile_keys, V rows past them zeroed
+  constexpr bool kCross = PR::kCross;           // no tree tile: tile t here is t + 1 of those
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -240,8 +238,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           const int stage = ring % C::kStages, use = ring / C::kStages;
           if (use > 0 && !warp_wait(KV_EMPTY + 8 * stage, (use - 1) & 1, abort_flag, wait_ns))
             return false;
-          const int tile = S.tile0 + k;
-          const bool tree = tile == 0;
+          const int tile = S.tile0 + k + (kCross ? 1 : 0);
+          const bool tree = !kCross && tile == 0;
           const CUtensorMap* m = tree ? (is_v ? &tm_tv : &tm_tk) : (is_v ? &tm_v : &tm_k);
           int z = tree ? L.s.n0 : L.s.p0 + (kWin ? tile_key0(L.s, tile) : (tile - 1) * kKeyTile);
           // a tile starts inside its sequence's rows (loads past a tensor's end read zeros)
@@ -431,7 +429,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       // Under a window every tile may need the row's depth, so every segment finds it.
       uint32_t anc[4] = {0u, 0u, 0u, 0u};
       int low = 0;  // kWin: the lowest prefix key this row sees through its window
-      if (kWin || (S.tile0 == 0 && (W == 2 || w == 0))) {
+      if (!kCross && (kWin || (S.tile0 == 0 && (W == 2 || w == 0)))) {
         int* ps = par_s + w * 128;
         // kWin: PAR_READY's even phases complete when the parents are in place, its odd
         // ones when every row has read them.  Nothing else keeps a row of stream 1 from
@@ -459,8 +457,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       float m_run = -INFINITY, l_run = 0.f;
       for (int i = 0; i < n_mine; ++i) {
         const int k = (W == 2) ? i : 2 * i + w;
-        const int tile = S.tile0 + k;
-        const bool is_tree = tile == 0;
+        const int tile = S.tile0 + k + (kCross ? 1 : 0);
+        const bool is_tree = !kCross && tile == 0;
         ok = __all_sync(0xffffffffu, mbar_wait(S_FULL + 8 * w, cnt & 1, abort_flag, wait_ns));
         if (!ok) break;
         tc_fence_after();
@@ -472,7 +470,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           if (!is_tree) {
             key0 = tile_key0(L.s, tile);
             lim = tile_keys(pr, L.s, tile);
-            cut = window_cuts(pr, L.s, key0, lim);
+            cut = !kCross && window_cuts(pr, L.s, key0, lim);
           }
         }
         if constexpr (kWin) {
@@ -782,33 +780,36 @@ void tc_wait_settings(uint64_t* wait_ns, int* stall) {
 
 namespace {
 
-template <int D, bool kBF16, bool kShare, bool kWin>
-cudaError_t launch_tc_typed(const PartialArgsOf<ProblemOf<kWin>>& a, int W, int npt, cudaStream_t s) {
+template <int D, bool kBF16, bool kShare, class PR>
+cudaError_t launch_tc_typed(const PartialArgsOf<PR>& a, int W, int npt, cudaStream_t s) {
+  constexpr bool kWin = PR::kWindowed, kCross = PR::kCross;
   constexpr CUtensorMapDataType type = kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const ProblemOf<kWin>& pr = a.pr;
+  const PR& pr = a.pr;
   CUtensorMap mq, mk, mv, mtk, mtv;
-  const void* kbase = pr.kv_capacity > 0 ? a.k_cache : a.tree_k;
-  const void* vbase = pr.kv_capacity > 0 ? a.v_cache : a.tree_v;
+  // a cache of no rows is never read: any valid address stands in for it
+  const void* kbase = pr.kv_capacity > 0 ? a.k_cache : kCross ? a.q : a.tree_k;
+  const void* vbase = pr.kv_capacity > 0 ? a.v_cache : kCross ? a.q : a.tree_v;
   const int q_nodes = kWin ? std::min(npt, pr.max_nodes) : npt;
   const int tree_rows = kWin ? std::min(kKeyTile, (pr.max_nodes + 7) / 8 * 8) : kKeyTile;
   if (!make_map(&mq, type, a.q, D, pr.Hq, pr.node_capacity, pr.G, q_nodes) ||
       !make_map(&mk, type, kbase, D, pr.Hkv, pr.kv_capacity, 1, kKeyTile) ||
       !make_map(&mv, type, vbase, D, pr.Hkv, pr.kv_capacity, 1, kKeyTile) ||
-      !make_map(&mtk, type, a.tree_k, D, pr.Hkv, pr.node_capacity, 1, tree_rows) ||
-      !make_map(&mtv, type, a.tree_v, D, pr.Hkv, pr.node_capacity, 1, tree_rows))
+      (!kCross && (!make_map(&mtk, type, a.tree_k, D, pr.Hkv, pr.node_capacity, 1, tree_rows) ||
+                   !make_map(&mtv, type, a.tree_v, D, pr.Hkv, pr.node_capacity, 1, tree_rows))))
     return cudaErrorInvalidValue;
+  if (kCross) mtk = mk, mtv = mv;  // unused
   constexpr int smem = Cfg<D>::kSmemBytes;
-  cudaError_t e = check_cuda(cudaFuncSetAttribute(partials_tc_kernel<D, kBF16, kShare, kWin>,
+  cudaError_t e = check_cuda(cudaFuncSetAttribute(partials_tc_kernel<D, kBF16, kShare, PR>,
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                              "cudaFuncSetAttribute(partials_tc_kernel)");
   if (e != cudaSuccess) return e;
-  TcArgs<kWin> ta{a, W, npt, q_nodes, tree_rows, 0, 0};
+  TcArgs<PR> ta{a, W, npt, q_nodes, tree_rows, 0, 0};
   tc_wait_settings(&ta.wait_ns, &ta.stall);
-  e = launch_pdl(partials_tc_kernel<D, kBF16, kShare, kWin>, dim3(pr.U), dim3(kThreadsTc), (size_t)smem, s, mq, mk, mv, mtk,
+  e = launch_pdl(partials_tc_kernel<D, kBF16, kShare, PR>, dim3(pr.U), dim3(kThreadsTc), (size_t)smem, s, mq, mk, mv, mtk,
                  mtv, ta);
   if (e != cudaSuccess) {
     cudaFuncAttributes fa{};
-    cudaFuncGetAttributes(&fa, partials_tc_kernel<D, kBF16, kShare, kWin>);
+    cudaFuncGetAttributes(&fa, partials_tc_kernel<D, kBF16, kShare, PR>);
     char what[160];
     snprintf(what, sizeof(what), "%s; kernel regs %d, max threads %d, smem %d+%d", cudaGetErrorString(e),
              fa.numRegs, fa.maxThreadsPerBlock, (int)fa.sharedSizeBytes, smem);
@@ -824,21 +825,25 @@ void set_tc_wait_limit(unsigned long long ns, int stall) {
   g_force_stall.store(stall != 0 ? 1 : 0, std::memory_order_relaxed);
 }
 
-template <bool kShare, bool kWin>
-cudaError_t launch_tc_mode(const PartialArgsOf<ProblemOf<kWin>>& a, bool bf16, int W, int npt, cudaStream_t s) {
+template <bool kShare, class PR>
+cudaError_t launch_tc_mode(const PartialArgsOf<PR>& a, bool bf16, int W, int npt, cudaStream_t s) {
   if (bf16)
-    return a.pr.d == 64 ? launch_tc_typed<64, true, kShare, kWin>(a, W, npt, s)
-                        : launch_tc_typed<128, true, kShare, kWin>(a, W, npt, s);
-  return a.pr.d == 64 ? launch_tc_typed<64, false, kShare, kWin>(a, W, npt, s)
-                      : launch_tc_typed<128, false, kShare, kWin>(a, W, npt, s);
+    return a.pr.d == 64 ? launch_tc_typed<64, true, kShare, PR>(a, W, npt, s)
+                        : launch_tc_typed<128, true, kShare, PR>(a, W, npt, s);
+  return a.pr.d == 64 ? launch_tc_typed<64, false, kShare, PR>(a, W, npt, s)
+                      : launch_tc_typed<128, false, kShare, PR>(a, W, npt, s);
 }
 
 cudaError_t launch_partials_tc(const PartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
-  return a.pr.share != 0 ? launch_tc_mode<true, false>(a, bf16, W, npt, s) : launch_tc_mode<false, false>(a, bf16, W, npt, s);
+  return a.pr.share != 0 ? launch_tc_mode<true>(a, bf16, W, npt, s) : launch_tc_mode<false>(a, bf16, W, npt, s);
 }
 
 cudaError_t launch_partials_tc(const WinPartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
-  return a.pr.share != 0 ? launch_tc_mode<true, true>(a, bf16, W, npt, s) : launch_tc_mode<false, true>(a, bf16, W, npt, s);
+  return a.pr.share != 0 ? launch_tc_mode<true>(a, bf16, W, npt, s) : launch_tc_mode<false>(a, bf16, W, npt, s);
+}
+
+cudaError_t launch_partials_tc(const CrossPartialArgs& a, bool bf16, int W, int npt, cudaStream_t s) {
+  return a.pr.share != 0 ? launch_tc_mode<true>(a, bf16, W, npt, s) : launch_tc_mode<false>(a, bf16, W, npt, s);
 }
 
 }  // namespace tva

@@ -64,6 +64,7 @@ struct Problem {
   // second segment - epilogue, Q copy, tree tile - in the middle of its stream).
   int align;
   static constexpr bool kWindowed = false;
+  static constexpr bool kCross = false;
 };
 
 // The problem of the windowed and the 4-bit-cache forms.  The schedule below is written for
@@ -80,6 +81,13 @@ struct WinProblem : Problem {
   // them by walking the sequences, which at 32 of them cost about 2 us a time.
   const int32_t* unit_start;
   const int32_t* group_start;
+};
+
+// Cross-attention (no window): the rows are queries without keys of their own, so there is no
+// tree tile.  A row group's tile t holds the keys of prefix tile t + 1 above, and a sequence
+// without keys has no units: no worker computes anything for it, and the combine writes its rows.
+struct CrossProblem : WinProblem {
+  static constexpr bool kCross = true;
 };
 
 struct SeqInfo {
@@ -205,6 +213,11 @@ __device__ __forceinline__ long long div_ll(long long a, int b) {
 }
 
 __device__ __forceinline__ int seq_tiles(int P) { return (P + kKeyTile - 1) / kKeyTile + 1; }
+// The units of a row group (tiles of P keys, and the tree tile where there is one).
+template <class PR>
+__device__ __forceinline__ int group_tiles(const PR&, int P) {
+  return seq_tiles(P) - (PR::kCross ? 1 : 0);
+}
 __device__ __forceinline__ int seq_groups(const Problem& pr, int m) {
   return (m * pr.G + pr.RG - 1) / pr.RG;
 }
@@ -216,7 +229,8 @@ constexpr int kSumsFrom = 16;
 // Fills pr.unit_start / group_start (4 (B + 1) ints of `buf` hold the cu_* copies and the
 // sums) when they fit and the units can be counted in 32 bits.  Every thread of the block
 // must call it, after the cu_* copies are in place; it ends with a block barrier.
-__device__ __forceinline__ void stage_sums(WinProblem& pr, int* buf, int cap) {
+template <class PR>
+__device__ __forceinline__ void stage_sums(PR& pr, int* buf, int cap) {
   constexpr int kOwn = 4;  // entries per thread
   const int n = pr.B + 1;
   if (4 * n > cap || n > kOwn * (int)blockDim.x) return;  // uniform over the block
@@ -224,7 +238,7 @@ __device__ __forceinline__ void stage_sums(WinProblem& pr, int* buf, int cap) {
   int* groups = buf + 3 * n;
   for (int b = threadIdx.x; b < pr.B; b += blockDim.x) {
     const SeqInfo s = seq_info(pr, b);
-    const long long g = (long long)pr.Hkv * seq_groups(pr, s.m), u = g * seq_tiles(s.P);
+    const long long g = (long long)pr.Hkv * seq_groups(pr, s.m), u = g * group_tiles(pr, s.P);
     units[b] = u < (1LL << 30) ? (int)u : -1;  // -1: too many to count here
     groups[b] = (int)g;
   }
@@ -334,7 +348,7 @@ __device__ __forceinline__ long long total_units(const PR& pr) {
   long long T = 0;
   for (int b = 0; b < pr.B; ++b) {
     SeqInfo s = seq_info(pr, b);
-    T += (long long)pr.Hkv * seq_groups(pr, s.m) * seq_tiles(s.P);
+    T += (long long)pr.Hkv * seq_groups(pr, s.m) * group_tiles(pr, s.P);
   }
   return T;
 }
@@ -372,7 +386,7 @@ __device__ __forceinline__ Loc locate_unit(const PR& pr, long long t) {
   for (; b < pr.B; ++b) {
     SeqInfo s = seq_info(pr, b);
     int MP = seq_groups(pr, s.m);
-    int tiles = seq_tiles(s.P);
+    int tiles = group_tiles(pr, s.P);
     long long units = (long long)pr.Hkv * MP * tiles;
     if (t < acc + units) {
       long long local = t - acc;
@@ -416,7 +430,7 @@ __device__ __forceinline__ void worker_range(const PR& pr, int u, long long& t0,
   if (!shared) {
     if (pr.align > 0) {  // worker j of row group q: its share of the group's tiles
       const SeqInfo s = seq_info(pr, 0);
-      const int tiles = seq_tiles(s.P), q = u / pr.align, j = u - q * pr.align;
+      const int tiles = group_tiles(pr, s.P), q = u / pr.align, j = u - q * pr.align;
       t0 = t1 = 0;
       if (q >= pr.Hkv * seq_groups(pr, s.m)) return;
       const int base = tiles / pr.align, extra = tiles - base * pr.align;
@@ -432,7 +446,7 @@ __device__ __forceinline__ void worker_range(const PR& pr, int u, long long& t0,
     return;
   }
   const SeqInfo s = seq_info(pr, 0);
-  const int MP = seq_groups(pr, s.m), tiles = seq_tiles(s.P);
+  const int MP = seq_groups(pr, s.m), tiles = group_tiles(pr, s.P);
   const int k = u / pr.share, r = u - k * pr.share;
   t0 = t1 = 0;
   if (k >= share_teams(pr) || r >= MP) return;  // no such row group, or a spare worker
@@ -455,7 +469,7 @@ __device__ __forceinline__ bool next_segment(const PR& pr, int u, long long& t, 
     L.s = seq_info(pr, 0);
     L.b = 0;
     L.MP = seq_groups(pr, L.s.m);
-    L.tiles = seq_tiles(L.s.P);
+    L.tiles = group_tiles(pr, L.s.P);
     L.g = PR::kWindowed ? (int)div_ll(t, L.tiles) : (int)(t / L.tiles);
     L.mp = u % pr.share;
     L.tile = (int)(t - (long long)L.g * L.tiles);
@@ -523,7 +537,7 @@ __device__ __forceinline__ GroupLoc locate_group(const PR& pr, long long qg) {
   for (int b = first; b < pr.B; ++b) {
     const SeqInfo s = seq_info(pr, b);
     const int MP = seq_groups(pr, s.m);
-    const int tiles = seq_tiles(s.P);
+    const int tiles = group_tiles(pr, s.P);
     const long long nq = (long long)pr.Hkv * MP;
     if (!R.found && qg >= qacc && qg < qacc + nq) {
       const long long gi = qg - qacc;

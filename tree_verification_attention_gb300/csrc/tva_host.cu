@@ -56,11 +56,11 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 // Host-side shape checks shared by every attention entry point.
 tva_status check_shape(int B, int Hq, int Hkv, int d, int dtype, int max_prefix, int max_nodes,
-                       long long kv_cap, long long node_cap) {
+                       long long kv_cap, long long node_cap, int most_nodes = tva::kMaxNodes) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return TVA_ERR_INVALID_ARG;
   if (Hq / Hkv > 128) return TVA_ERR_UNSUPPORTED;
   if (max_prefix < 0 || max_nodes < 1 || kv_cap < 0 || node_cap < 0) return TVA_ERR_INVALID_ARG;
-  if (max_nodes > tva::kMaxNodes) return TVA_ERR_UNSUPPORTED;
+  if (max_nodes > most_nodes) return TVA_ERR_UNSUPPORTED;
   if (d != 64 && d != 128) return TVA_ERR_UNSUPPORTED;
   if (dtype != TVA_BF16 && dtype != TVA_FP32 && dtype != TVA_FP16) return TVA_ERR_UNSUPPORTED;
   // index arithmetic inside the kernels is 32-bit for row counts
@@ -69,6 +69,15 @@ tva_status check_shape(int B, int Hq, int Hkv, int d, int dtype, int max_prefix,
     return TVA_ERR_INVALID_ARG;
   return TVA_OK;
 }
+
+// Queries of one sequence in cross-attention: no ancestor bits limit them, only what the
+// workspace takes (a partial row for each query row).
+constexpr int kMaxQueries = 65536;
+
+// Row groups of one KV head up to which cross-attention forms teams (Problem::share).  U / S
+// teams of S leave up to S - 1 workers without work, and with more row groups the products
+// bound the call, not DRAM: beyond, the workers take equal ranges.
+constexpr int kMaxCrossTeam = 8;
 
 struct Layout {
   Problem pr;
@@ -85,8 +94,10 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // the single-sequence form.
 tva_status make_layout(int B, int Hq, int Hkv, int d, int dtype, int max_prefix, int max_nodes,
                        int kv_cap, int node_cap, const int32_t* cu_prefix, const int32_t* cu_nodes,
-                       int single_prefix, int single_nodes, Layout* L, bool allow_pair = true) {
-  tva_status st = check_shape(B, Hq, Hkv, d, dtype, max_prefix, max_nodes, kv_cap, node_cap);
+                       int single_prefix, int single_nodes, Layout* L, bool allow_pair = true,
+                       bool cross = false) {
+  tva_status st = check_shape(B, Hq, Hkv, d, dtype, max_prefix, max_nodes, kv_cap, node_cap,
+                              cross ? kMaxQueries : tva::kMaxNodes);
   if (st != TVA_OK) return st;
   int sms = 0;
   if (device_sms(&sms) != 0) return TVA_ERR_CUDA;
@@ -124,7 +135,7 @@ tva_status make_layout(int B, int Hq, int Hkv, int d, int dtype, int max_prefix,
   const long long groups = (long long)B * Hkv * mp_max;
   // One sequence whose KV heads have several row groups: teams of workers, one member per
   // row group, stream the same K/V tiles together, so each is read from DRAM once.
-  pr.share = (B == 1 && mp_max >= 2 && pr.U >= mp_max) ? mp_max : 0;
+  pr.share = (B == 1 && mp_max >= 2 && pr.U >= mp_max && (!cross || mp_max <= kMaxCrossTeam)) ? mp_max : 0;
   // One sequence with one row group per KV head: split each head's tiles over its own
   // U / Hkv workers when Hkv divides U (see Problem::align).
   pr.align = (B == 1 && mp_max == 1 && pr.U % Hkv == 0) ? pr.U / Hkv : 0;
@@ -251,6 +262,13 @@ tva_status check_varlen_window(const tva_params* p, int window, int sinks, const
   return check_workspace(*L, workspace, workspace_bytes);
 }
 
+// Cross-attention's layout: tva_params with queries for nodes and keys for the prefix.
+tva_status cross_layout(const tva_params* p, Layout* L) {
+  if (p == nullptr) return TVA_ERR_INVALID_ARG;
+  return make_layout(p->batch, p->num_q_heads, p->num_kv_heads, p->head_dim, (int)p->dtype, p->max_prefix_len,
+                     p->max_nodes, p->kv_capacity, p->node_capacity, p->cu_prefix, p->cu_nodes, 0, 0, L, false, true);
+}
+
 bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(x), b0 = reinterpret_cast<uintptr_t>(y);
   return nx > 0 && ny > 0 && a0 < b0 + ny && b0 < a0 + nx;
@@ -269,6 +287,29 @@ tva_status check_kv4_rows(int num_rows, int Hkv, int d, int dtype, long long kv_
   const size_t rows = (size_t)num_rows * Hkv * d * (dtype == TVA_FP32 ? 4 : 2);
   const size_t held = (size_t)kv_capacity * Hkv * tva::kv4_record_bytes(d);
   if (overlap(k, rows, cache, held) || overlap(v, rows, cache, held)) return TVA_ERR_INVALID_ARG;
+  return TVA_OK;
+}
+
+// The checks that gdn_update_varlen and commit_accepted_gdn share (`rows` token or node rows;
+// q and out null in a commit): shapes, types, pointers, and that the state, written in place,
+// and the output overlap no input.
+tva_status check_gdn_update(int B, int H, int d, int dtype, int rows, const int32_t* cu, const void* q, const void* k,
+                            const void* v, const float* beta, const float* alpha, const float* state, const void* out,
+                            const int32_t* dev_status) {
+  if (B < 1 || H < 1 || rows < 0 || (long long)B * H > (1LL << 24) || !cu || !state || !dev_status)
+    return TVA_ERR_INVALID_ARG;
+  if (rows > 0 && (!k || !v || !beta || !alpha)) return TVA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return TVA_ERR_UNSUPPORTED;
+  if (dtype != TVA_FP32 && dtype != TVA_BF16) return TVA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state) || !aligned16(out)) return TVA_ERR_INVALID_ARG;
+  const size_t row = (size_t)rows * H * d * (dtype == TVA_FP32 ? 4 : 2), gate = (size_t)rows * H * 4;
+  const size_t held = (size_t)B * H * d * d * 4;
+  if (overlap(q, q ? row : 0, state, held) || overlap(k, row, state, held) || overlap(v, row, state, held) ||
+      overlap(beta, gate, state, held) || overlap(alpha, gate, state, held))
+    return TVA_ERR_INVALID_ARG;
+  if (out && (overlap(out, row, state, held) || overlap(out, row, q, row) || overlap(out, row, k, row) ||
+              overlap(out, row, v, row) || overlap(out, row, beta, gate) || overlap(out, row, alpha, gate)))
+    return TVA_ERR_INVALID_ARG;
   return TVA_OK;
 }
 
@@ -539,6 +580,36 @@ tva_status tree_verify_attn_kv4_varlen(const tva_params* p, int window, int sink
   return run_combine_of(L, pr, (int)p->dtype, workspace, out, lse, dev_status, s);
 }
 
+size_t tva_cross_workspace_size(const tva_params* p) {
+  Layout L;
+  return cross_layout(p, &L) == TVA_OK ? L.total : 0;
+}
+
+tva_status cross_attn_varlen(const tva_params* p, const void* q, const void* k_cache, const void* v_cache, void* out,
+                             float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  if (p == nullptr || p->cu_prefix == nullptr || p->cu_nodes == nullptr || dev_status == nullptr || q == nullptr ||
+      out == nullptr || lse == nullptr || !aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache))
+    return TVA_ERR_INVALID_ARG;
+  Layout L;
+  tva_status st = cross_layout(p, &L);
+  if (st != TVA_OK) return st;
+  if (p->kv_capacity > 0 && (!k_cache || !v_cache)) return TVA_ERR_INVALID_ARG;
+  st = check_workspace(L, workspace, workspace_bytes);
+  if (st != TVA_OK) return st;
+  tva::CrossProblem pr;
+  static_cast<Problem&>(pr) = L.pr;
+  pr.window = pr.sinks = 0;
+  pr.unit_start = pr.group_start = nullptr;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int dtype = (int)p->dtype;
+  const tva::CrossPartialArgs a = partial_args(L, pr, p->softmax_scale, q, k_cache, v_cache, nullptr, nullptr, nullptr,
+                                               workspace, dev_status);
+  const cudaError_t e = dtype == TVA_FP32 ? tva::launch_partials_simt(a, dtype, s)
+                                          : tva::launch_partials_tc(a, dtype == TVA_BF16, L.W, L.npt, s);
+  if (e != cudaSuccess) return TVA_ERR_CUDA;
+  return run_combine_of(L, pr, dtype, workspace, out, lse, dev_status, s);
+}
+
 size_t tva_kv4_record_bytes(int head_dim) {
   return head_dim == 64 || head_dim == 128 ? (size_t)tva::kv4_record_bytes(head_dim) : 0;
 }
@@ -620,6 +691,33 @@ tva_status gdn_tree_verify(int batch, int num_heads, int head_dim, tva_dtype dty
   a.cu_nodes = cu_nodes; a.parent = parent; a.q = q; a.k = k; a.v = v; a.beta = beta; a.alpha = alpha;
   a.S0 = S0; a.o = out; a.status = dev_status;
   return tva::launch_gdn(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TVA_OK : TVA_ERR_CUDA;
+}
+
+tva_status gdn_update_varlen(int batch, int num_heads, int head_dim, tva_dtype dtype, int token_capacity,
+                             int max_tokens, const int32_t* cu_tokens, const void* q, const void* k, const void* v,
+                             const float* beta, const float* alpha, float* state, void* out, int32_t* dev_status,
+                             void* stream) {
+  if (max_tokens < 0 || (token_capacity > 0 && (!q || !out))) return TVA_ERR_INVALID_ARG;
+  const tva_status st = check_gdn_update(batch, num_heads, head_dim, (int)dtype, token_capacity, cu_tokens, q, k, v,
+                                         beta, alpha, state, out, dev_status);
+  if (st != TVA_OK) return st;
+  const tva::GdnUpdateArgs a{batch, num_heads, head_dim, max_tokens, token_capacity, dtype == TVA_BF16 ? 1 : 0,
+                             cu_tokens, nullptr, nullptr, q, k, v, beta, alpha, state, out, dev_status};
+  return tva::launch_gdn_recurrent(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TVA_OK : TVA_ERR_CUDA;
+}
+
+tva_status commit_accepted_gdn(int batch, int num_heads, int head_dim, tva_dtype dtype, int node_capacity,
+                               int max_nodes, const int32_t* cu_nodes, const int32_t* accept_len,
+                               const int32_t* accept_path, const void* k, const void* v, const float* beta,
+                               const float* alpha, float* state, int32_t* dev_status, void* stream) {
+  if (max_nodes < 1 || max_nodes > tva::kMaxNodes || !accept_len || (node_capacity > 0 && !accept_path))
+    return TVA_ERR_INVALID_ARG;
+  const tva_status st = check_gdn_update(batch, num_heads, head_dim, (int)dtype, node_capacity, cu_nodes, nullptr, k,
+                                         v, beta, alpha, state, nullptr, dev_status);
+  if (st != TVA_OK) return st;
+  const tva::GdnUpdateArgs a{batch, num_heads, head_dim, max_nodes, node_capacity, dtype == TVA_BF16 ? 1 : 0,
+                             cu_nodes, accept_len, accept_path, nullptr, k, v, beta, alpha, state, nullptr, dev_status};
+  return tva::launch_gdn_recurrent(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TVA_OK : TVA_ERR_CUDA;
 }
 
 }  // extern "C"

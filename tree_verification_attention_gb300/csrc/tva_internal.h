@@ -29,6 +29,7 @@ struct PartialArgsOf {
 
 using PartialArgs = PartialArgsOf<Problem>;
 using WinPartialArgs = PartialArgsOf<WinProblem>;
+using CrossPartialArgs = PartialArgsOf<CrossProblem>;  // tree_k, tree_v and parent unused
 
 template <class PR>
 struct CombineArgsOf {
@@ -43,6 +44,7 @@ struct CombineArgsOf {
 
 using CombineArgs = CombineArgsOf<Problem>;
 using WinCombineArgs = CombineArgsOf<WinProblem>;
+using CrossCombineArgs = CombineArgsOf<CrossProblem>;
 
 struct AcceptArgs {
   int B;
@@ -114,6 +116,24 @@ struct GdnArgs {
   int32_t* status;
 };
 
+// Tokens (accept_len null: sequence b's rows cu[b] .. cu[b+1]-1) or accepted paths (cu counts the
+// tree nodes, accept_path holds local ids) through the recurrence, state updated in place.
+struct GdnUpdateArgs {
+  int B, H, d, max_tokens, token_capacity;
+  int bf16;                 // q, k, v and out: bf16 (1) or fp32 (0)
+  const int32_t* cu;
+  const int32_t* accept_len;
+  const int32_t* accept_path;
+  const void* q;            // null with a path, as is out
+  const void* k;
+  const void* v;
+  const float* beta;
+  const float* alpha;
+  float* state;             // [B, H, d, d]
+  void* out;
+  int32_t* status;
+};
+
 // Records a host-side failure for tva_last_error() (thread-local).
 void record_error(const char* where, int code, const char* what);
 // Records `e` (if it is an error) and returns it unchanged.
@@ -142,9 +162,11 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 int simt_workers_per_sm();
 cudaError_t launch_partials_simt(const PartialArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_partials_simt(const WinPartialArgs& a, int dtype, cudaStream_t s);  // under a window
+cudaError_t launch_partials_simt(const CrossPartialArgs& a, int dtype, cudaStream_t s);
 // bf16 (bf16 = true) or fp16, head_dim 64 or 128; W M-tiles of npt nodes per row group
 cudaError_t launch_partials_tc(const PartialArgs& a, bool bf16, int W, int npt, cudaStream_t s);
 cudaError_t launch_partials_tc(const WinPartialArgs& a, bool bf16, int W, int npt, cudaStream_t s);  // under a window
+cudaError_t launch_partials_tc(const CrossPartialArgs& a, bool bf16, int W, int npt, cudaStream_t s);
 // The same over a 4-bit prefix cache (a.k_cache: the records; a.v_cache unused).
 cudaError_t launch_partials_kv4(const WinPartialArgs& a, bool bf16, int W, int npt, cudaStream_t s);
 // The same for one row group of at most `rows` <= 16 rows a KV head.
@@ -164,6 +186,7 @@ void tc_wait_settings(uint64_t* wait_ns, int* stall);
 void set_tc_wait_limit(unsigned long long ns, int stall);
 cudaError_t launch_combine(const CombineArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_combine(const WinCombineArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_combine(const CrossCombineArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s);
 cudaError_t launch_commit(const CommitArgs& a, cudaStream_t s);
 cudaError_t launch_append_kv4(const Kv4RowArgs& a, int dtype, cudaStream_t s);
@@ -172,5 +195,6 @@ cudaError_t launch_read_kv4(const Kv4RowArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_commit_kv4(const CommitArgs& a, int Hkv, int d, int dtype, cudaStream_t s);
 cudaError_t launch_sampling(const SamplingArgs& a, cudaStream_t s);
 cudaError_t launch_gdn(const GdnArgs& a, cudaStream_t s);
+cudaError_t launch_gdn_recurrent(const GdnUpdateArgs& a, cudaStream_t s);
 
 }  // namespace tva
