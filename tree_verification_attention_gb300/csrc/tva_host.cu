@@ -290,6 +290,10 @@ tva_status check_kv4_rows(int num_rows, int Hkv, int d, int dtype, long long kv_
   return TVA_OK;
 }
 
+// Tokens a sequence up to which bf16 calls of gdn_update_varlen run the recurrence, and beyond which
+// they run in chunks on the tensor cores.
+constexpr int kMaxRecurrent = 16;
+
 // The checks that gdn_update_varlen and commit_accepted_gdn share (`rows` token or node rows;
 // q and out null in a commit): shapes, types, pointers, and that the state, written in place,
 // and the output overlap no input.
@@ -703,7 +707,10 @@ tva_status gdn_update_varlen(int batch, int num_heads, int head_dim, tva_dtype d
   if (st != TVA_OK) return st;
   const tva::GdnUpdateArgs a{batch, num_heads, head_dim, max_tokens, token_capacity, dtype == TVA_BF16 ? 1 : 0,
                              cu_tokens, nullptr, nullptr, q, k, v, beta, alpha, state, out, dev_status};
-  return tva::launch_gdn_recurrent(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TVA_OK : TVA_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool chunks = dtype == TVA_BF16 && max_tokens > kMaxRecurrent && token_capacity > 0;
+  return (chunks ? tva::launch_gdn_chunk(a, s) : tva::launch_gdn_recurrent(a, s)) == cudaSuccess ? TVA_OK
+                                                                                                   : TVA_ERR_CUDA;
 }
 
 tva_status commit_accepted_gdn(int batch, int num_heads, int head_dim, tva_dtype dtype, int node_capacity,

@@ -196,5 +196,7 @@ cudaError_t launch_commit_kv4(const CommitArgs& a, int Hkv, int d, int dtype, cu
 cudaError_t launch_sampling(const SamplingArgs& a, cudaStream_t s);
 cudaError_t launch_gdn(const GdnArgs& a, cudaStream_t s);
 cudaError_t launch_gdn_recurrent(const GdnUpdateArgs& a, cudaStream_t s);
+// The same in chunks on the tensor cores; bf16, no path.
+cudaError_t launch_gdn_chunk(const GdnUpdateArgs& a, cudaStream_t s);
 
 }  // namespace tva
