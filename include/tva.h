@@ -172,8 +172,8 @@ void tva_release(void);
 
 /* Diagnostics, for testing the device-side timeout path; not for production use.
  * Sets, for this process and for launches made after the call, the limit of the
- * main-loop waits inside the tensor-core attention partials kernel (bf16 / fp16) in
- * nanoseconds (0 restores the default of 2 s).  With force_stall non-zero, that
+ * main-loop waits inside the tensor-core attention partials kernel (bf16 / fp16), and in the
+ * chunked form of gdn_update_varlen, in nanoseconds (0 restores the default of 2 s).  With force_stall non-zero, that
  * kernel's MMA-issuing thread first waits on a barrier that nothing completes, so the
  * wait runs out: the kernel then raises its abort flag, lets every copy and MMA it
  * started finish (those drain waits always keep the 2 s limit), frees its tensor
@@ -416,14 +416,24 @@ tva_status gdn_tree_verify(int batch, int num_heads, int head_dim, tva_dtype dty
  *                  its state bit for bit
  *   state          [B, H, d, d] fp32, read and written (zeros: a fresh sequence)
  *   out            [token_capacity, H, d]: rows of no sequence are left as they were
+ *   workspace, workspace_bytes  >= tva_gdn_workspace_size(...) bytes, 256-byte aligned; null when
+ *                  that is 0.  Its contents between calls mean nothing; calls that overlap on the
+ *                  GPU need one each
  * q, k, v, state and out are 16-byte aligned; the state and out overlap no other array.  Arrays of
- * token_capacity rows may be null when it is 0.  Arithmetic is fp32; bf16 outputs are rounded
- * once.  A sequence outside the bounds is skipped (state and output untouched) with
+ * token_capacity rows may be null when it is 0.  fp32 calls, and bf16 calls of at most 16 tokens a
+ * sequence, run the recurrence in fp32.  Longer bf16 calls run in chunks of 64 tokens on the tensor
+ * cores: fp32 sums of products whose operands are held to 16 bits or more (relative error of the
+ * state some 5e-6).  bf16 outputs are rounded once.  tva_diag_set_wait_limit applies to the chunked
+ * form.  A sequence outside the bounds is skipped (state and output untouched) with
  * TVA_ERR_INVALID_ARG in *dev_status. */
 tva_status gdn_update_varlen(int batch, int num_heads, int head_dim, tva_dtype dtype, int token_capacity,
                              int max_tokens, const int32_t* cu_tokens, const void* q, const void* k, const void* v,
-                             const float* beta, const float* alpha, float* state, void* out, int32_t* dev_status,
-                             void* stream);
+                             const float* beta, const float* alpha, float* state, void* out, void* workspace,
+                             size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Bytes of workspace gdn_update_varlen needs (0: none, or an argument out of range). */
+size_t tva_gdn_workspace_size(int batch, int num_heads, int head_dim, tva_dtype dtype, int token_capacity,
+                              int max_tokens);
 
 /* Commits each sequence's accepted path into its Gated DeltaNet state ("DFlash-TfM", Method 3: the
  * state's commit waits for the accepted branch), in place: the nodes accept_path[cu_nodes[b] + j],

@@ -32,9 +32,10 @@ def test_the_tests_recurrence_is_the_oracle_s():
 
 
 def test_update_refusals(lib):
-    def call(B=2, H=4, d=128, dtype=0, cap=64, most=32, cu=A, q=A, k=A, v=A, beta=A, alpha=A, state=S, out=O, st=A):
+    def call(B=2, H=4, d=128, dtype=0, cap=64, most=32, cu=A, q=A, k=A, v=A, beta=A, alpha=A, state=S, out=O, ws=A,
+             n=1 << 40, st=A):
         return lib.gdn_update_varlen(B, H, d, dtype, cap, most, P(cu), P(q), P(k), P(v), P(beta), P(alpha), P(state),
-                                     P(out), P(st), None)
+                                     P(out), P(ws), n, P(st), None)
     assert call(B=0) == 1 and call(H=0) == 1 and call(cap=-1) == 1 and call(most=-1) == 1
     assert call(d=96) == 2 and call(dtype=2) == 2 and call(dtype=5) == 2
     for name in ("cu", "q", "k", "v", "beta", "alpha", "state", "out", "st"):
@@ -46,6 +47,18 @@ def test_update_refusals(lib):
     for name in ("q", "k", "v", "beta", "alpha"):
         assert call(**{name: O + 64}) == 1, name       # inside the output
     assert call(B=1 << 13, H=1 << 12) == 1             # more states than a launch numbers
+    need = lib.tva_gdn_workspace_size(2, 4, 128, 0, 64, 32)
+    assert need > 0 and call(n=need - 1) == 4 and call(ws=None) == 4 and call(ws=A + 64) == 4
+
+
+def test_workspace_sizes(lib):
+    size = lib.tva_gdn_workspace_size
+    assert size(1, 4, 128, 1, 100, 100) == 0 and size(64, 32, 128, 0, 64, 1) == 0 and size(1, 4, 96, 0, 64, 64) == 0
+    assert size(0, 4, 128, 0, 64, 64) == 0 and size(1, 4, 128, 0, 64, 16) == 0
+    assert size(1, 4, 128, 0, 8, 1 << 30) == 0                      # no more than 8 rows: the recurrence
+    one = size(1, 1, 128, 0, 64, 64)
+    assert one == size(1, 1, 128, 0, 64, 1 << 30) and size(2, 3, 128, 0, 1000, 128) == 12 * one
+    assert size(64, 32, 128, 0, 1 << 20, 1 << 20) == 64 * 32 * 8 * one   # bounded, whatever the lengths
 
 
 def test_commit_refusals(lib):

@@ -22,7 +22,7 @@ __all__ = [
     "tree_verify_attn", "read_device_status", "release", "diag_set_wait_limit", "diag_use_cta_pair", "accept_longest_path",
     "tree_verify_attn_window_varlen", "tree_verify_attn_kv4_varlen", "kv4_record_bytes", "alloc_kv4_cache", "append_kv4",
     "read_kv4", "commit_accepted_kv4", "cross_attn_varlen", "alloc_cross_workspace", "gdn_update_varlen",
-    "commit_accepted_gdn", "status_string", "STATUS",
+    "gdn_workspace_size", "commit_accepted_gdn", "status_string", "STATUS",
 ]
 
 STATUS = {0: "TVA_OK", 1: "TVA_ERR_INVALID_ARG", 2: "TVA_ERR_UNSUPPORTED", 3: "TVA_ERR_BAD_TREE",
@@ -90,7 +90,8 @@ def load_library(path: str | None = None):
         "commit_accepted_kv4": (_I, [_I, _I, _I, _I, _I, _I, ctypes.c_longlong] + [_P] * 9),
         "cross_attn_varlen": (_I, [PP] + [_P] * 6 + [_SZ, _P, _P]),
         "tva_cross_workspace_size": (_SZ, [PP]),
-        "gdn_update_varlen": (_I, [_I] * 6 + [_P] * 10),
+        "gdn_update_varlen": (_I, [_I] * 6 + [_P] * 9 + [_SZ, _P, _P]),
+        "tva_gdn_workspace_size": (_SZ, [_I] * 6),
         "commit_accepted_gdn": (_I, [_I] * 6 + [_P] * 10),
         "tva_status_string": (ctypes.c_char_p, [_I]),
         "tva_last_error": (ctypes.c_char_p, []),
@@ -776,13 +777,23 @@ def _check_gdn(q, k, v, beta, alpha, cu, state):
     return here, B, n, H, d
 
 
+def gdn_workspace_size(batch, num_heads, head_dim, dtype, rows, max_tokens) -> int:
+    """Bytes of workspace that gdn_update_varlen needs for calls of these sizes (0: none)."""
+    return int(load_library().tva_gdn_workspace_size(
+        _c_int("batch", batch), _c_int("num_heads", num_heads), _c_int("head_dim", head_dim), DTYPES[dtype],
+        _c_int("rows", rows), _c_int("max_tokens", max_tokens)))
+
+
 @_on_stream
-def gdn_update_varlen(q, k, v, beta, alpha, cu_tokens, max_tokens, state, out=None, dev_status=None, stream=None):
+def gdn_update_varlen(q, k, v, beta, alpha, cu_tokens, max_tokens, state, out=None, dev_status=None, stream=None,
+                      workspace=None):
     """Every sequence's tokens (rows cu_tokens[b] .. cu_tokens[b + 1] - 1, oldest first) through a
     Gated DeltaNet layer: q, k, v [n, H, d] float32 or bfloat16, beta, alpha [n, H] and the state
     [B, H, d, d] float32.  The state is updated in place, the outputs [n, H, d] are returned; rows of
     no sequence are left as they were.  ``max_tokens`` bounds every sequence's tokens; one
-    beyond it is skipped and reported in ``dev_status`` (int32 [1], zeroed by the caller)."""
+    beyond it is skipped and reported in ``dev_status`` (int32 [1], zeroed by the caller).
+    bf16 calls of more than 16 tokens a sequence use a ``workspace`` (uint8, gdn_workspace_size
+    bytes), allocated here when not given; calls that overlap on the GPU need one each."""
     max_tokens = _c_int("max_tokens", max_tokens)
     here, B, n, H, d = _check_gdn(q, k, v, beta, alpha, cu_tokens, state)
     if out is None:
@@ -790,9 +801,17 @@ def gdn_update_varlen(q, k, v, beta, alpha, cu_tokens, max_tokens, state, out=No
     elif out.get_device() != here or out.dtype is not v.dtype or out.shape != v.shape or not out.is_contiguous():
         raise ValueError("out must be like v")
     dev_status = _status_word(dev_status, q.device)
-    code = load_library().gdn_update_varlen(
+    lib = load_library()
+    if workspace is None:
+        need = lib.tva_gdn_workspace_size(B, H, d, DTYPES[k.dtype], n, max_tokens)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    elif workspace.get_device() != here or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8, on the tensors' device")
+    code = lib.gdn_update_varlen(
         B, H, d, DTYPES[k.dtype], n, max_tokens, cu_tokens.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-        beta.data_ptr(), alpha.data_ptr(), state.data_ptr(), out.data_ptr(), dev_status.data_ptr(), _raw_stream(here))
+        beta.data_ptr(), alpha.data_ptr(), state.data_ptr(), out.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+        dev_status.data_ptr(), _raw_stream(here))
     if code:
         _check(code, "gdn_update_varlen")
     return out

@@ -11,14 +11,16 @@
 //     W = K^T diag(G_Ci) T diag(beta)    [d x C]      S' = g_C S + W r
 //     P = lower(G o Q K^T) T diag(beta)  [C x C]      O  = g o (Q S) + P r
 //
-// One CTA per (sequence, head, 32 columns of d_v), 13 warps:
-//   warps 0-3   (recurrence): X = [K; Q] S (one M = 128 product: lanes 0-63 are K rows, 64-127
-//               Q rows), r, then W r and P r.  Thread = TMEM lane; S stays in fp32 in registers,
-//               lane = row of d_k.
-//   warps 4-11  (two groups of four, chunks in turn): [K; Q] K^T, the decays, T by blocks, W and P,
-//               left in TMEM where the recurrence's products read them as their A operand.
-//   warp 12     (producer): TMA copies of K and Q tiles into three stages.
-// Each group issues its own MMAs from its first warp after a barrier of the group.
+// Two kernels.  The first makes W and P of every (sequence, head, chunk), all at once, one CTA of
+// four warps each (three resident per SM), and leaves them in the workspace as the second's shared
+// memory will hold them (48 KB at d = 128).  The second walks a sequence's chunks, one CTA per (sequence,
+// head, 64 columns of d_v): a producer warp fetches K, Q, W and P a chunk ahead, eight warps hold the
+// state in registers (fp32; thread = row of d_k = TMEM lane, 32 columns) and run
+//     X = [K; Q] S (one M = 128 product: lanes 0-63 are K rows, 64-127 Q rows) -> r -> W r, P r.
+// Long prompts go in segments of chunks, a pair of launches each, so that the workspace stays bounded.
+// One kernel that made W and P beside the walk, each CTA for its own columns, took 2.94 ms
+// for 32768 tokens of 32 heads, d = 128: four times the preparation, and 108 KB of code that ran at the
+// rate of its instruction fetches.
 //
 // Precision: K, Q and V are bf16 inputs and exact.  S, T, W, G o (Q K^T), P and r are fp32 values held
 // as two bf16 terms each, so that products have operands of 16 bits or more (a term is off by 2^-17;
@@ -27,11 +29,13 @@
 // 5e-3 with keys that repeat: there W r and P r are small sums of large terms.  Sums, decays, T and
 // the state are fp32.
 //
-// Every wait is bounded (as in the attention kernels): when one expires the abort flag is raised,
-// the groups leave their loops together at their next barrier, everything in flight is drained
-// (again bounded), TMEM is freed and TVA_ERR_TIMEOUT recorded; the state is then not written.
+// Every wait is bounded (as in the attention kernels): when one expires the abort flag is raised, the
+// warps leave their loops together at their next barrier, everything in flight is drained (again
+// bounded), TMEM is freed and TVA_ERR_TIMEOUT recorded; the state is then not written.
 #include <cuda.h>
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "tc_pipeline.cuh"
 #include "tc_ptx.cuh"
@@ -43,49 +47,19 @@ namespace {
 using namespace ptx;
 
 constexpr int kChunk = 64;
-constexpr int kCols = 32;             // columns of d_v per CTA
-constexpr int kThreadsCh = 512;      // 13 warps work; the last four share one register budget
-constexpr int kProducer = 12;
-constexpr int kSpan = kChunk * 128;   // 64 rows of 64 bf16
-constexpr int kStagesCh = 3;
+constexpr int kSpan = kChunk * 128;   // 64 rows of 64 bf16: one 128-byte swizzle span
 constexpr int kLd = kChunk + 4;       // row pitch of A / T in floats
 constexpr int kLdX = 36;              // row pitch of the blocks' intermediate product
 
-// TMEM columns: per preparing group 192 ([K; Q] K^T, then G o (Q K^T); W; P; each becomes its hi and lo
-// terms in place), then X; once X is read P r goes to its first half and W r to its second.
-constexpr uint32_t kTmGroup = 192, kTmW = 64, kTmP = 128, kTmX = 384, kTmD = 416;
-
+// What the first kernel leaves for the second, per (sequence, head, chunk): W hi, W lo [D rows of 64
+// tokens], P hi, P lo [64 rows of 64 tokens], K-major and swizzled, then g_i (64 floats).
 template <int D>
-struct Ch {
-  static constexpr int kHalves = D / 64;
-  static constexpr int kStage = kHalves * 2 * kSpan;          // per half: K rows, then Q rows
-  static constexpr int kSOff = kStagesCh * kStage;            // S: [D rows][hi 32 | lo 32]
-  static constexpr int kROff = kSOff + D * 128;               // r hi, r lo: [64 rows][32, padded to 64]
-  static constexpr int kTOff = kROff + 2 * kSpan;             // per group: T hi, lo (for P)
-  static constexpr int kZeroOff = kTOff + 2 * 2 * kSpan;      // D = 64: zeros for rows 64 .. 127 of K^T
-  static constexpr int kAOff = kZeroOff + (D == 64 ? kSpan : 0);
-  // per group: A, then T; then T hi, lo (for W)
-  static constexpr int kXOff = kAOff + 2 * kChunk * kLd * 4;
-  static constexpr int kGateOff = kXOff + 2 * 32 * kLdX * 4;
-  static constexpr int kGate = 4 * kChunk + 8;                // floats per group: alpha, beta, G_Ci; g, g_C
-  static constexpr int kBarOff = kGateOff + 2 * kGate * 4;
-  static constexpr int kSmem = kBarOff + 256 + 1024;
+struct Image {
+  static constexpr int kW = D * 128;
+  static constexpr int kP = 2 * kW;
+  static constexpr int kG = kP + 2 * kSpan;
+  static constexpr int kBytes = kG + kChunk * 4;
 };
-
-// Barrier `id` over a group of 128 threads; true in all of them when `ok` is in all.
-__device__ __forceinline__ bool group_all(int id, bool ok) {
-  uint32_t r;
-  __syncwarp();
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.and.pred p, %2, 128, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(r)
-      : "r"((uint32_t)ok), "r"(id)
-      : "memory");
-  return r != 0;
-}
 
 // Two fp32 values as two packed bf16 terms each: hi + lo.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
@@ -95,50 +69,448 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
 
 struct ChunkArgs {
   GdnUpdateArgs a;
+  uint8_t* images;       // [B][segment][H]
+  int chunk0, span;      // first chunk and chunks of each sequence in this pair of launches
+  int segment;           // images a sequence and head has room for
   uint64_t wait_ns;
-  int stall;   // test hook: the recurrence first waits on a barrier that nothing completes
+  int stall;   // test hook: the state kernel first waits on a barrier that nothing completes
+};
+
+__device__ __forceinline__ bool sequence_ok(const GdnUpdateArgs& a, int t0, int n) {
+  return t0 >= 0 && n >= 0 && n <= a.max_tokens && (long long)t0 + n <= a.token_capacity;
+}
+
+// ------------------------------------------------------------------ W and P of one chunk
+
+constexpr int kThreadsPr = 128;
+constexpr uint32_t kTmWork = 64;   // TMEM: [K; Q] K^T, then G o (Q K^T) hi and lo, at 0; then W, then P
+
+template <int D>
+struct Pr {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kKQ = kHalves * 2 * kSpan;       // per half: K rows, then Q rows
+  static constexpr int kAOff = kKQ;                     // A, then T; then T hi, lo (for W)
+  static constexpr int kTOff = kAOff + kChunk * kLd * 4;   // T hi, lo (for P)
+  static constexpr int kXOff = kTOff + 2 * kSpan;
+  static constexpr int kGateOff = kXOff + 32 * kLdX * 4;   // alpha, beta, G_Ci
+  static constexpr int kBarOff = kGateOff + 3 * kChunk * 4;
+  static constexpr int kSmem = kBarOff + 64 + 1024;
+  static_assert(kChunk * kLd * 4 % 1024 == 0 && kChunk * kLd * 4 >= 2 * kSpan, "T's terms over A");
+  static_assert(Image<D>::kBytes <= kTOff, "the image over K, Q and T's terms for W");
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreadsCh, 1)
-    gdn_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const ChunkArgs args) {
-  using C = Ch<D>;
+__global__ void __launch_bounds__(kThreadsPr, 3)
+    gdn_chunk_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                             const ChunkArgs args) {
+  using C = Pr<D>;
+  using I = Image<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const GdnUpdateArgs& a = args.a;
   const uint64_t wait_ns = args.wait_ns;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int t = threadIdx.x, w = t >> 5, lane = t & 31;
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t KQ_FULL = sbase + C::kBarOff, P_DONE = KQ_FULL + 8, DRAIN = KQ_FULL + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 24);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + 28);
+
+  pdl_wait();
+  pdl_launch_dependents();
+  const int h = blockIdx.x % a.H, bc = blockIdx.x / a.H;
+  const int b = bc / args.span, c = args.chunk0 + bc % args.span;
+  const int t0 = __ldg(a.cu + b), n = __ldg(a.cu + b + 1) - t0;
+  if (!sequence_ok(a, t0, n) || c * kChunk >= n) return;   // the state kernel reports bad bounds
+  const int cnt = min(kChunk, n - c * kChunk);
+
+  if (t == 0) {
+    mbar_init(KQ_FULL, 1);
+    mbar_init(P_DONE, 1);
+    mbar_init(DRAIN, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  float* As = reinterpret_cast<float*>(smem + C::kAOff);
+  float* Xs = reinterpret_cast<float*>(smem + C::kXOff);
+  float* al_s = reinterpret_cast<float*>(smem + C::kGateOff);   // alpha
+  float* be_s = al_s + kChunk;                                  // beta
+  float* en_s = be_s + kChunk;                                  // G_Ci
+  // gates (rows past the sequence's end: no decay, nothing written)
+  float al = 1.f, be = 0.f;
+  if (t < cnt) {
+    const size_t at = (size_t)(t0 + c * kChunk + t) * a.H + h;
+    al = __ldg(a.alpha + at);
+    be = __ldg(a.beta + at);
+  }
+  if (t < kChunk) {
+    al_s[t] = al;
+    be_s[t] = be;
+  }
+  if (w == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 128);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t lane_base = (uint32_t)(w * 32) << 16;
+  if (w == 0) {
+    int z = t0 + c * kChunk;
+    if (!TVA_CHECK(z >= 0 && z < a.token_capacity, a.status)) z = 0;
+    mbar_expect_tx_elect(KQ_FULL, (uint32_t)C::kKQ);
+    for (int hf = 0; hf < C::kHalves; ++hf) {
+      tma_load_3d_elect(sbase + hf * 2 * kSpan, &tm_k, 64 * hf, h, z, KQ_FULL);
+      tma_load_3d_elect(sbase + hf * 2 * kSpan + kSpan, &tm_q, 64 * hf, h, z, KQ_FULL);
+    }
+  }
+  constexpr uint32_t idesc_a = idesc_bf16(128, 64, false);                 // [K; Q] K^T: both K-major
+  constexpr uint32_t idesc_w = idesc_bf16(128, 64, true) | (1u << 15);     // K^T T: A along M, B along N
+  constexpr uint32_t idesc_p = idesc_bf16(128, 64, true);                  // A in TMEM
+  const uint32_t desc_hi = (uint32_t)(sdesc_sw128(0, 16, 1024) >> 32);     // the LBO field is in the low word
+  // products of the decays from the chunk's start and to its end: 64 threads, a scan each way
+  float pre = al;
+  if (t < 64) {
+    float suf = t < 63 ? al_s[t + 1] : 1.f;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float x = __shfl_up_sync(0xffffffffu, pre, o), y = __shfl_down_sync(0xffffffffu, suf, o);
+      if (lane >= o) pre *= x;
+      if (lane + o < 32) suf *= y;
+    }
+    // across the two warps: the other one's 32 factors, multiplied by every lane's share
+    float other = t < 32 ? al_s[32 + lane] : al_s[lane];
+    if (t < 32 && lane == 0) other = 1.f;   // al_s[32] is already in warp 0's suffixes
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) other *= __shfl_xor_sync(0xffffffffu, other, o);
+    if (t < 32) suf *= other;
+    else pre *= other;
+    en_s[t] = suf;
+  }
+  bool ok = mbar_wait(KQ_FULL, 0, abort_flag, wait_ns);
+  if (cnt < kChunk) {
+    // rows of K and Q past the end belong to other sequences or to none: zeros instead
+    for (int e = t; e < C::kHalves * 2 * 8 * (kChunk - cnt); e += kThreadsPr) {
+      const int r = cnt + (e >> 3) % (kChunk - cnt), part = (e >> 3) / (kChunk - cnt);
+      *reinterpret_cast<uint4*>(smem + part * kSpan + r * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_async_shared();
+  }
+  ok = __syncthreads_and(ok);
+  if (ok && w == 0) {
+    tc_fence_after();
+    const uint32_t lo = (uint32_t)sdesc_sw128(sbase, 16, 1024);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const uint32_t o = (uint32_t)((ks >> 2) * 2 * kSpan + (ks & 3) * 32) >> 4;
+      mma_ss_elect(tmem, desc_join(lo + o, desc_hi), desc_join(lo + o, desc_hi), idesc_a, ks > 0);
+    }
+    tc_commit_elect(P_DONE);
+  }
+  const int row = t & 63;   // this lane's token row (of K for t < 64, of Q above)
+  if (ok) ok = mbar_wait(P_DONE, 0, abort_flag, wait_ns);
+  tc_fence_after();
+  {
+    uint32_t d[64];
+    tmem_ld32(tmem + lane_base, d);
+    tmem_ld32(tmem + lane_base + 32, d + 32);
+    tmem_wait_ld32(d);
+    tie32(d + 32);
+    // row `row` of beta_i G_ij k_i.k_j (j < i), or of G_ij q_i.k_j (j <= i)
+    const bool qrow = t >= 64;
+    float p = qrow ? 1.f : be;
+    const int last = qrow ? row : row - 1;
+#pragma unroll
+    for (int j4 = 60; j4 >= 0; j4 -= 4) {
+      const float4 a4 = *reinterpret_cast<const float4*>(al_s + j4);
+      const float next = j4 < 60 ? al_s[j4 + 4] : 1.f;
+      const float f[4] = {a4.y, a4.z, a4.w, next};   // alpha of token j + 1
+#pragma unroll
+      for (int e = 3; e >= 0; --e) {
+        const int j = j4 + e;
+        if (j < row) p *= f[e];
+        d[j] = j <= last ? __float_as_uint(__uint_as_float(d[j]) * p) : 0u;
+      }
+    }
+    if (!qrow) {
+#pragma unroll
+      for (int j = 0; j < 64; j += 4)
+        *reinterpret_cast<uint4*>(As + row * kLd + j) = make_uint4(d[j], d[j + 1], d[j + 2], d[j + 3]);
+#pragma unroll
+      for (int j = 0; j < 64; ++j) d[j] = 0u;
+    } else {
+      uint32_t o[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        split2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]), d[j], o[j]);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) d[32 + j] = o[j];
+    }
+    tmem_st32(tmem + lane_base, d);   // lower(G o Q K^T) in lanes 64 .. 127, zeros above
+    tmem_st32(tmem + lane_base + 32, d + 32);
+    tmem_wait_st();
+    tc_fence_before();
+  }
+  __syncthreads();
+  // ---- T = (I + A)^-1: 16-row diagonal blocks by substitution (a column per lane), then the
+  // blocks below them, T21 = -T22 (A21 T11), at 16 and at 32 rows
+  {
+    const int o = 16 * w, cc = lane & 15;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s0 = i == cc ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+      for (int j = 0; j < i; j += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(As + (o + i) * kLd + o + j);
+        s0 = fmaf(-v.x, x[j], s0);
+        if (j + 1 < i) s1 = fmaf(-v.y, x[j + 1], s1);
+        if (j + 2 < i) s0 = fmaf(-v.z, x[j + 2], s0);
+        if (j + 3 < i) s1 = fmaf(-v.w, x[j + 3], s1);
+      }
+      x[i] = s0 + s1;
+    }
+    __syncwarp();
+    if (lane < 16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) As[(o + i) * kLd + o + cc] = x[i];
+    }
+  }
+  __syncthreads();
+  {
+    const int o = 32 * (w >> 1), tt = t & 63, i = tt >> 2, c4 = 4 * (tt & 3);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float x = As[(o + 16 + i) * kLd + o + k];
+      const float4 v = *reinterpret_cast<const float4*>(As + (o + k) * kLd + o + c4);
+      s.x = fmaf(x, v.x, s.x); s.y = fmaf(x, v.y, s.y); s.z = fmaf(x, v.z, s.z); s.w = fmaf(x, v.w, s.w);
+    }
+    float* X = Xs + (w >> 1) * 16 * kLdX;
+    *reinterpret_cast<float4*>(X + i * kLdX + c4) = s;
+    __syncthreads();
+    s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float x = -As[(o + 16 + i) * kLd + o + 16 + k];
+      const float4 v = *reinterpret_cast<const float4*>(X + k * kLdX + c4);
+      s.x = fmaf(x, v.x, s.x); s.y = fmaf(x, v.y, s.y); s.z = fmaf(x, v.z, s.z); s.w = fmaf(x, v.w, s.w);
+    }
+    *reinterpret_cast<float4*>(As + (o + 16 + i) * kLd + o + c4) = s;
+  }
+  __syncthreads();
+  {
+    // 32 x 32 x 32: rows i and i + 16, four columns a thread, on packed pairs of columns
+    const int i = t >> 3, c4 = 4 * (t & 7);
+    auto product = [&](const float* L, const float* R, int ldr, float sign, float4& o0, float4& o1) {
+      uint64_t s00 = 0, s01 = 0, s10 = 0, s11 = 0;
+#pragma unroll
+      for (int k = 0; k < 32; k += 4) {
+        const float4 x0 = *reinterpret_cast<const float4*>(L + i * kLd + k);
+        const float4 x1 = *reinterpret_cast<const float4*>(L + (i + 16) * kLd + k);
+        const float y0[4] = {x0.x, x0.y, x0.z, x0.w}, y1[4] = {x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(R + (k + e) * ldr + c4);
+          const uint64_t p0 = f2_pack(y0[e], y0[e]), p1 = f2_pack(y1[e], y1[e]);
+          s00 = f2_fma(p0, v.x, s00);
+          s01 = f2_fma(p0, v.y, s01);
+          s10 = f2_fma(p1, v.x, s10);
+          s11 = f2_fma(p1, v.y, s11);
+        }
+      }
+      f2_unpack(s00, o0.x, o0.y);
+      f2_unpack(s01, o0.z, o0.w);
+      f2_unpack(s10, o1.x, o1.y);
+      f2_unpack(s11, o1.z, o1.w);
+      o0.x *= sign; o0.y *= sign; o0.z *= sign; o0.w *= sign;
+      o1.x *= sign; o1.y *= sign; o1.z *= sign; o1.w *= sign;
+    };
+    float4 o0, o1;
+    product(As + 32 * kLd, As, kLd, 1.f, o0, o1);                 // A21 T11
+    *reinterpret_cast<float4*>(Xs + i * kLdX + c4) = o0;
+    *reinterpret_cast<float4*>(Xs + (i + 16) * kLdX + c4) = o1;
+    __syncthreads();
+    product(As + 32 * kLd + 32, Xs, kLdX, -1.f, o0, o1);          // -T22 (A21 T11)
+    *reinterpret_cast<float4*>(As + (32 + i) * kLd + c4) = o0;
+    *reinterpret_cast<float4*>(As + (48 + i) * kLd + c4) = o1;
+  }
+  __syncthreads();
+  {
+    // T diag(beta) (for P) and diag(G_Ci) T diag(beta) (for W, over A's place), two terms each:
+    // row i is the products' k = i, its columns lie along N
+    const int i = t >> 1, j0 = 32 * (t & 1);
+    const float en = en_s[i];
+    float x[32];
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(As + i * kLd + j0 + j);
+      const float4 bb = *reinterpret_cast<const float4*>(be_s + j0 + j);
+      x[j] = v.x * bb.x; x[j + 1] = v.y * bb.y; x[j + 2] = v.z * bb.z; x[j + 3] = v.w * bb.w;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t hi[4], lo[4];
+      const int at = i * 128 + (((j0 >> 3) + q) ^ (i & 7)) * 16;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1], hi[e], lo[e]);
+      *reinterpret_cast<uint4*>(smem + C::kTOff + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(smem + C::kTOff + kSpan + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split2(x[8 * q + 2 * e] * en, x[8 * q + 2 * e + 1] * en, hi[e], lo[e]);
+      *reinterpret_cast<uint4*>(smem + C::kAOff + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(smem + C::kAOff + kSpan + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    fence_async_shared();
+  }
+  ok = __syncthreads_and(ok);
+  if (ok && w == 0) {
+    tc_fence_after();
+    // rows 64 .. 127 of K^T: the second half (d = 64: Q's, whose products are not read)
+    const uint32_t klo = (uint32_t)sdesc_sw128(sbase, D == 128 ? 2 * kSpan : kSpan, 1024);
+    const uint32_t wlo = (uint32_t)sdesc_sw128(sbase + C::kAOff, 16, 1024);
+#pragma unroll
+    for (int part = 0; part < 2; ++part)   // hi and lo terms
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        mma_ss_elect(tmem + kTmWork, desc_join(klo + (ks * 2048 >> 4), desc_hi),
+                     desc_join(wlo + ((part * kSpan + ks * 2048) >> 4), desc_hi), idesc_w, part > 0 || ks > 0);
+    tc_commit_elect(P_DONE);
+  }
+  if (ok) ok = mbar_wait(P_DONE, 1, abort_flag, wait_ns);
+  tc_fence_after();
+  uint32_t d[64];
+  tmem_ld32(tmem + kTmWork + lane_base, d);
+  tmem_ld32(tmem + kTmWork + lane_base + 32, d + 32);
+  tmem_wait_ld32(d);
+  tie32(d + 32);
+  tc_fence_before();
+  ok = __syncthreads_and(ok);
+  if (ok && w == 0) {   // P while W is written out
+    tc_fence_after();
+    const uint32_t plo = (uint32_t)sdesc_sw128(sbase + C::kTOff, 16, 1024);
+#pragma unroll
+    for (int part = 0; part < 3; ++part)   // hi hi, hi lo, lo hi
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        mma_ts_elect(tmem + kTmWork, tmem + (part == 2 ? 32 : 0) + ks * 8,
+                     desc_join(plo + (((part == 1 ? kSpan : 0) + ks * 2048) >> 4), desc_hi), idesc_p, part > 0 || ks > 0);
+    tc_commit_elect(P_DONE);
+  }
+  // a row of 64 tokens in two terms, over K, Q and T
+  auto write_row = [&](uint8_t* hi_row, uint8_t* lo_row, int r) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        split2(__uint_as_float(d[8 * q + 2 * e]), __uint_as_float(d[8 * q + 2 * e + 1]), hi[e], lo[e]);
+      const int at = (q ^ (r & 7)) * 16;
+      *reinterpret_cast<uint4*>(hi_row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(lo_row + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+  };
+  if (t < D) write_row(smem + t * 128, smem + I::kW + t * 128, t);
+  if (t < kChunk) *reinterpret_cast<float*>(smem + I::kG + 4 * t) = pre;
+  if (ok) ok = mbar_wait(P_DONE, 0, abort_flag, wait_ns);
+  tc_fence_after();
+  if (t >= kChunk) {   // P is in lanes 64 .. 127
+    tmem_ld32(tmem + kTmWork + lane_base, d);
+    tmem_ld32(tmem + kTmWork + lane_base + 32, d + 32);
+    tmem_wait_ld32(d);
+    tie32(d + 32);
+    write_row(smem + I::kP + row * 128, smem + I::kP + kSpan + row * 128, row);
+  }
+  fence_async_shared();
+  tc_fence_before();
+  ok = __syncthreads_and(ok);
+  if (!ok && w == 0) {   // a wait ran out: what is in flight lands before the CTA ends
+    tc_commit_elect(DRAIN);
+    drain_wait(DRAIN, 0);
+    drain_wait(KQ_FULL, 0);
+  }
+  if (t == 0) {
+    if (ok) {
+      const size_t slot = ((size_t)b * args.segment + (c - args.chunk0)) * a.H + h;
+      bulk_store(args.images + slot * I::kBytes, sbase, I::kBytes);
+    } else {
+      set_status(a.status, kStatusTimeout);
+    }
+  }
+  __syncthreads();
+  if (w == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 128);
+  }
+}
+
+// ------------------------------------------------------------------ the walk from state to state
+
+constexpr int kCols = 64;             // columns of d_v per CTA, 32 per thread
+constexpr int kThreadsSt = 288;
+constexpr int kProducerSt = 8;
+constexpr uint32_t kTmX = 0, kTmD = 64, kTmO = 128;   // TMEM columns: X, W r, P r
+
+template <int D>
+struct St {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kKQ = kHalves * 2 * kSpan;
+  static constexpr int kStages = D == 128 ? 2 : 3;
+  static constexpr int kStage = (kKQ + Image<D>::kBytes + 1023) / 1024 * 1024;
+  static constexpr int kSOff = kStages * kStage;        // S hi, lo: [D rows of d_k][64 columns]
+  static constexpr int kROff = kSOff + 2 * D * 128;     // r hi, lo: [64 tokens][64 columns]
+  static constexpr int kBarOff = kROff + 2 * kSpan;
+  static constexpr int kSmem = kBarOff + 128 + 1024;
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
+};
+
+// Barrier over the 256 threads that hold the state; true in all of them when `ok` is in all.
+__device__ __forceinline__ bool group_all(bool ok) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.and.pred p, 1, 256, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsSt, 1)
+    gdn_chunk_state_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                           const ChunkArgs args) {
+  using C = St<D>;
+  using I = Image<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const GdnUpdateArgs& a = args.a;
+  const uint64_t wait_ns = args.wait_ns;
+  const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + C::kBarOff;
-  const uint32_t KQ_FULL = bars, KQ_EMPTY = bars + 24, READY = bars + 48, OUT_EMPTY = bars + 64, P_DONE = bars + 80,
-                 X_DONE = bars + 96, D_DONE = bars + 104, O_DONE = bars + 112, DRAIN = bars + 120;   // DRAIN [3]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 160);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + 164);
+  const uint32_t FULL = bars, EMPTY = bars + 24, X_DONE = bars + 48, D_DONE = bars + 56, O_DONE = bars + 64,
+                 DRAIN = bars + 72;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 80);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + 84);
 
-  if (warp == kProducer && lane == 0) {
+  if (tid == kProducerSt * 32) {
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
-    for (int s = 0; s < kStagesCh; ++s) {
-      mbar_init(KQ_FULL + 8 * s, 1);
-      mbar_init(KQ_EMPTY + 8 * s, 1);
-    }
-    for (int g = 0; g < 2; ++g) {
-      mbar_init(READY + 8 * g, 128);
-      mbar_init(OUT_EMPTY + 8 * g, 1);
-      mbar_init(P_DONE + 8 * g, 1);
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(FULL + 8 * s, 1);
+      mbar_init(EMPTY + 8 * s, 1);
     }
     mbar_init(X_DONE, 1);
     mbar_init(D_DONE, 1);
     mbar_init(O_DONE, 1);
-    for (int g = 0; g < 3; ++g) mbar_init(DRAIN + 8 * g, 1);
+    mbar_init(DRAIN, 1);
     *abort_flag = 0;
     fence_mbar_init();
-  }
-  if constexpr (D == 64) {
-    for (int e = tid; e < kSpan / 16; e += kThreadsCh)
-      *reinterpret_cast<uint4*>(smem + C::kZeroOff + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
-    fence_async_shared();
   }
   pdl_wait();
   pdl_launch_dependents();
@@ -147,15 +519,15 @@ __global__ void __launch_bounds__(kThreadsCh, 1)
   const int b = bh / a.H, h = bh % a.H;
   const int t0 = __ldg(a.cu + b);
   const int n = __ldg(a.cu + b + 1) - t0;
-  if (!(t0 >= 0 && n >= 0 && n <= a.max_tokens && (long long)t0 + n <= a.token_capacity)) {
+  if (!sequence_ok(a, t0, n)) {
     if (tid == 0) set_status(a.status, kStatusInvalidArg);
     return;   // uniform over the CTA
   }
-  if (n == 0) return;
-  const int chunks = (n + kChunk - 1) / kChunk;
-
-  if (warp == kProducer) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
+  const int chunks = min(args.span, (n + kChunk - 1) / kChunk - args.chunk0);   // in this segment
+  if (chunks <= 0) return;
+  const int first = args.chunk0 * kChunk;   // the segment's first token
+  if (warp == kProducerSt) {
+    tmem_alloc(smem_u32(tmem_slot), 256);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -163,462 +535,153 @@ __global__ void __launch_bounds__(kThreadsCh, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp >= kProducer) {
+  if (warp == kProducerSt) {
     // ------------------------------------------------------------------ producer
-    reg_dec<24>();
-    bool ok = warp == kProducer;
-    int c = 0;
-    for (; ok && c < chunks; ++c) {
-      const int st = c % kStagesCh, use = c / kStagesCh;
-      if (use > 0 && !(ok = warp_wait(KQ_EMPTY + 8 * st, (use - 1) & 1, abort_flag, wait_ns))) break;
-      int z = t0 + c * kChunk;
-      if (!TVA_CHECK(z >= 0 && z < a.token_capacity, a.status)) z = 0;
-      mbar_expect_tx_elect(KQ_FULL + 8 * st, (uint32_t)C::kStage);
-      for (int hf = 0; hf < C::kHalves; ++hf) {
-        const uint32_t at = sbase + st * C::kStage + hf * 2 * kSpan;
-        tma_load_3d_elect(at, &tm_k, 64 * hf, h, z, KQ_FULL + 8 * st);
-        tma_load_3d_elect(at + kSpan, &tm_q, 64 * hf, h, z, KQ_FULL + 8 * st);
-      }
-    }
-    for (int i = max(0, c - kStagesCh); i < c; ++i)   // every copy has landed before the CTA ends
-      drain_wait(KQ_FULL + 8 * (i % kStagesCh), (i / kStagesCh) & 1);
-  } else if (warp >= 4) {
-    reg_inc<160>();   // 3 x 128 x 160 + 128 x 24 of the block's 512 x 128 registers
-    // ------------------------------------------------------------------ W and P of every other chunk
-    const int g = (warp - 4) >> 2, t = (tid - 128) & 127, w = t >> 5;
-    const int bar_id = 2 + g;
-    const uint32_t tw = tmem + kTmGroup * g;
-    const uint32_t lane_base = (uint32_t)(w * 32) << 16;
-    float* As = reinterpret_cast<float*>(smem + C::kAOff) + g * kChunk * kLd;
-    float* Xs = reinterpret_cast<float*>(smem + C::kXOff) + g * 32 * kLdX;
-    float* al_s = reinterpret_cast<float*>(smem + C::kGateOff) + g * C::kGate;   // alpha
-    float* be_s = al_s + kChunk;                                                 // beta
-    float* en_s = be_s + kChunk;                                                 // G_Ci
-    float* ga_s = en_s + kChunk;                                                 // g_i, then g_C
-    uint8_t* Tp = smem + C::kTOff + g * 2 * kSpan;
-    const uint32_t tp = sbase + C::kTOff + g * 2 * kSpan;
-    uint8_t* Tw = reinterpret_cast<uint8_t*>(As);
-    const uint32_t tws = sbase + C::kAOff + g * kChunk * kLd * 4;
-    static_assert(kChunk * kLd * 4 % 1024 == 0 && kChunk * kLd * 4 >= 2 * kSpan, "T's terms over A");
-    constexpr uint32_t idesc_a = idesc_bf16(128, 64, false);                 // [K; Q] K^T: both K-major
-    constexpr uint32_t idesc_w = idesc_bf16(128, 64, true) | (1u << 15);     // K^T T: A along M, B along N
-    constexpr uint32_t idesc_p = idesc_bf16(128, 64, true);                  // A in TMEM
-    const uint32_t kmaj_hi = (uint32_t)(sdesc_sw128(0, 16, 1024) >> 32);
-    const uint32_t mnmaj_hi = (uint32_t)(sdesc_sw128(0, 16, 1024) >> 32);    // the LBO field is in the low word
-    uint32_t ph = 0;   // parity of P_DONE
     bool ok = true;
-    const int row = t & 63;         // this lane's token row (of K for t < 64, of Q above)
-    for (int c = g; c < chunks; c += 2) {
-      const int st = c % kStagesCh, cnt = min(kChunk, n - c * kChunk);
-      const uint32_t kq = sbase + st * C::kStage;
-      // gates (rows past the sequence's end: no decay, nothing written)
-      float al = 1.f, be = 0.f;
-      if (t < 64 && t < cnt) {
-        const size_t at = (size_t)(t0 + c * kChunk + t) * a.H + h;
-        al = __ldg(a.alpha + at);
-        be = __ldg(a.beta + at);
+    int c = 0;
+    const uint8_t* image = args.images + ((size_t)b * args.segment * a.H + h) * I::kBytes;
+    for (; c < chunks; ++c) {
+      const int st = c % C::kStages, use = c / C::kStages;
+      if (use > 0 && !(ok = warp_wait(EMPTY + 8 * st, (use - 1) & 1, abort_flag, wait_ns))) break;
+      int z = t0 + first + c * kChunk;
+      if (!TVA_CHECK(z >= 0 && z < a.token_capacity, a.status)) z = 0;
+      const uint32_t at = sbase + st * C::kStage;
+      mbar_expect_tx_elect(FULL + 8 * st, (uint32_t)(C::kKQ + I::kBytes));
+      for (int hf = 0; hf < C::kHalves; ++hf) {
+        tma_load_3d_elect(at + hf * 2 * kSpan, &tm_k, 64 * hf, h, z, FULL + 8 * st);
+        tma_load_3d_elect(at + hf * 2 * kSpan + kSpan, &tm_q, 64 * hf, h, z, FULL + 8 * st);
       }
-      ok = mbar_wait(KQ_FULL + 8 * st, (c / kStagesCh) & 1, abort_flag, wait_ns) && ok;
-      if (cnt < kChunk) {
-        // rows of K and Q past the end belong to other sequences or to none: zeros instead
-        for (int e = t; e < C::kHalves * 2 * 8 * (kChunk - cnt); e += 128) {
-          const int r = cnt + (e >> 3) % (kChunk - cnt), part = (e >> 3) / (kChunk - cnt);
-          *reinterpret_cast<uint4*>(smem + st * C::kStage + part * kSpan + r * 128 + (e & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_async_shared();
-      }
-      if (t < 64) {
-        al_s[t] = al;
-        be_s[t] = be;
-      }
-      ok = group_all(bar_id, ok);
-      if (!ok) break;
-      if (w == 0) {
-        tc_fence_after();
-        const uint32_t lo = (uint32_t)sdesc_sw128(kq, 16, 1024);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t o = (uint32_t)((ks >> 2) * 2 * kSpan + (ks & 3) * 32) >> 4;
-          mma_ss_elect(tw, desc_join(lo + o, kmaj_hi), desc_join(lo + o, kmaj_hi), idesc_a, ks > 0);
-        }
-        tc_commit_elect(P_DONE + 8 * g);
-      }
-      // products of the decays from the chunk's start and to its end: 64 threads, a scan each way
-      float pre = al, suf = 1.f;
-      if (t < 64) {
-        suf = t < 63 ? al_s[t + 1] : 1.f;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float x = __shfl_up_sync(0xffffffffu, pre, o), y = __shfl_down_sync(0xffffffffu, suf, o);
-          if (lane >= o) pre *= x;
-          if (lane + o < 32) suf *= y;
-        }
-        // across the two warps: the other one's 32 factors, multiplied by every lane's share
-        float other = t < 32 ? al_s[32 + lane] : al_s[lane];
-        if (t < 32 && lane == 0) other = 1.f;   // al_s[32] is already in warp 0's suffixes
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) other *= __shfl_xor_sync(0xffffffffu, other, o);
-        if (t < 32) suf *= other;
-        else pre *= other;
-        en_s[t] = suf;
-      }
-      ok = mbar_wait(P_DONE + 8 * g, ph, abort_flag, wait_ns);
-      ph ^= 1;
-      tc_fence_after();
-      {
-        uint32_t d[64];
-        tmem_ld32(tw + lane_base, d);
-        tmem_ld32(tw + lane_base + 32, d + 32);
-        tmem_wait_ld32(d);
-        tie32(d + 32);
-        // row `row` of beta_i G_ij k_i.k_j (j < i), or of G_ij q_i.k_j (j <= i)
-        const bool qrow = t >= 64;
-        float p = qrow ? 1.f : be;
-        const int last = qrow ? row : row - 1;
-#pragma unroll
-        for (int j4 = 60; j4 >= 0; j4 -= 4) {
-          const float4 a4 = *reinterpret_cast<const float4*>(al_s + j4);
-          const float next = j4 < 60 ? al_s[j4 + 4] : 1.f;
-          const float f[4] = {a4.y, a4.z, a4.w, next};   // alpha of token j + 1
-#pragma unroll
-          for (int e = 3; e >= 0; --e) {
-            const int j = j4 + e;
-            if (j < row) p *= f[e];
-            d[j] = j <= last ? __float_as_uint(__uint_as_float(d[j]) * p) : 0u;
-          }
-        }
-        if (!qrow) {
-#pragma unroll
-          for (int j = 0; j < 64; j += 4)
-            *reinterpret_cast<uint4*>(As + row * kLd + j) = make_uint4(d[j], d[j + 1], d[j + 2], d[j + 3]);
-#pragma unroll
-          for (int j = 0; j < 64; ++j) d[j] = 0u;
-        } else {
-          uint32_t o[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            split2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]), d[j], o[j]);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) d[32 + j] = o[j];
-        }
-        tmem_st32(tw + lane_base, d);   // lower(G o Q K^T) in lanes 64 .. 127, zeros above
-        tmem_st32(tw + lane_base + 32, d + 32);
-        tmem_wait_st();
-        tc_fence_before();
-      }
-      ok = group_all(bar_id, ok);
-      if (!ok) break;
-      // ---- T = (I + A)^-1: 16-row diagonal blocks by substitution (a column per lane), then the
-      // blocks below them, T21 = -T22 (A21 T11), at 16 and at 32 rows
-      {
-        const int o = 16 * w, cc = lane & 15;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float s0 = i == cc ? 1.f : 0.f, s1 = 0.f;
-#pragma unroll
-          for (int j = 0; j < i; j += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(As + (o + i) * kLd + o + j);
-            s0 = fmaf(-v.x, x[j], s0);
-            if (j + 1 < i) s1 = fmaf(-v.y, x[j + 1], s1);
-            if (j + 2 < i) s0 = fmaf(-v.z, x[j + 2], s0);
-            if (j + 3 < i) s1 = fmaf(-v.w, x[j + 3], s1);
-          }
-          x[i] = s0 + s1;
-        }
-        __syncwarp();
-        if (lane < 16) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) As[(o + i) * kLd + o + cc] = x[i];
-        }
-      }
-      group_all(bar_id, true);
-      {
-        const int o = 32 * (w >> 1), tt = t & 63, i = tt >> 2, c4 = 4 * (tt & 3);
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float x = As[(o + 16 + i) * kLd + o + k];
-          const float4 v = *reinterpret_cast<const float4*>(As + (o + k) * kLd + o + c4);
-          s.x = fmaf(x, v.x, s.x); s.y = fmaf(x, v.y, s.y); s.z = fmaf(x, v.z, s.z); s.w = fmaf(x, v.w, s.w);
-        }
-        float* X = Xs + (w >> 1) * 16 * kLdX;
-        *reinterpret_cast<float4*>(X + i * kLdX + c4) = s;
-        group_all(bar_id, true);
-        s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float x = -As[(o + 16 + i) * kLd + o + 16 + k];
-          const float4 v = *reinterpret_cast<const float4*>(X + k * kLdX + c4);
-          s.x = fmaf(x, v.x, s.x); s.y = fmaf(x, v.y, s.y); s.z = fmaf(x, v.z, s.z); s.w = fmaf(x, v.w, s.w);
-        }
-        *reinterpret_cast<float4*>(As + (o + 16 + i) * kLd + o + c4) = s;
-      }
-      group_all(bar_id, true);
-      {
-        // 32 x 32 x 32: rows i and i + 16, four columns a thread, on packed pairs of columns
-        const int i = t >> 3, c4 = 4 * (t & 7);
-        auto product = [&](const float* L, const float* R, int ldr, float sign, float4& o0, float4& o1) {
-          uint64_t s00 = 0, s01 = 0, s10 = 0, s11 = 0;
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float4 x0 = *reinterpret_cast<const float4*>(L + i * kLd + k);
-            const float4 x1 = *reinterpret_cast<const float4*>(L + (i + 16) * kLd + k);
-            const float y0[4] = {x0.x, x0.y, x0.z, x0.w}, y1[4] = {x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(R + (k + e) * ldr + c4);
-              const uint64_t p0 = f2_pack(y0[e], y0[e]), p1 = f2_pack(y1[e], y1[e]);
-              s00 = f2_fma(p0, v.x, s00);
-              s01 = f2_fma(p0, v.y, s01);
-              s10 = f2_fma(p1, v.x, s10);
-              s11 = f2_fma(p1, v.y, s11);
-            }
-          }
-          f2_unpack(s00, o0.x, o0.y);
-          f2_unpack(s01, o0.z, o0.w);
-          f2_unpack(s10, o1.x, o1.y);
-          f2_unpack(s11, o1.z, o1.w);
-          o0.x *= sign; o0.y *= sign; o0.z *= sign; o0.w *= sign;
-          o1.x *= sign; o1.y *= sign; o1.z *= sign; o1.w *= sign;
-        };
-        float4 o0, o1;
-        product(As + 32 * kLd, As, kLd, 1.f, o0, o1);                 // A21 T11
-        *reinterpret_cast<float4*>(Xs + i * kLdX + c4) = o0;
-        *reinterpret_cast<float4*>(Xs + (i + 16) * kLdX + c4) = o1;
-        group_all(bar_id, true);
-        product(As + 32 * kLd + 32, Xs, kLdX, -1.f, o0, o1);          // -T22 (A21 T11)
-        *reinterpret_cast<float4*>(As + (32 + i) * kLd + c4) = o0;
-        *reinterpret_cast<float4*>(As + (48 + i) * kLd + c4) = o1;
-      }
-      group_all(bar_id, true);
-      {
-        // T diag(beta) (for P) and diag(G_Ci) T diag(beta) (for W, over A's place), two terms each:
-        // row i is the products' k = i, its columns lie along N
-        const int i = t >> 1, j0 = 32 * (t & 1);
-        const float en = en_s[i];
-        float x[32];
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(As + i * kLd + j0 + j);
-          const float4 bb = *reinterpret_cast<const float4*>(be_s + j0 + j);
-          x[j] = v.x * bb.x; x[j + 1] = v.y * bb.y; x[j + 2] = v.z * bb.z; x[j + 3] = v.w * bb.w;
-        }
-        group_all(bar_id, true);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t hi[4], lo[4];
-          const int at = i * 128 + (((j0 >> 3) + q) ^ (i & 7)) * 16;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) split2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1], hi[e], lo[e]);
-          *reinterpret_cast<uint4*>(Tp + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(Tp + kSpan + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) split2(x[8 * q + 2 * e] * en, x[8 * q + 2 * e + 1] * en, hi[e], lo[e]);
-          *reinterpret_cast<uint4*>(Tw + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(Tw + kSpan + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-        fence_async_shared();
-      }
-      // the recurrence is done with this group's previous W, P and decays
-      if (c >= 2) ok = mbar_wait(OUT_EMPTY + 8 * g, ((c >> 1) - 1) & 1, abort_flag, wait_ns);
-      ok = group_all(bar_id, ok);
-      if (!ok) break;
-      if (w == 0) {
-        tc_fence_after();
-        const uint32_t lbo = D == 128 ? 2u * kSpan : sbase + C::kZeroOff - kq;   // rows 64 .. of K^T
-        const uint32_t klo = (uint32_t)sdesc_sw128(kq, lbo, 1024);
-        const uint32_t wlo = (uint32_t)sdesc_sw128(tws, 16, 1024), plo = (uint32_t)sdesc_sw128(tp, 16, 1024);
-#pragma unroll
-        for (int part = 0; part < 2; ++part)   // hi and lo terms
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_ss_elect(tw + kTmW, desc_join(klo + (ks * 2048 >> 4), mnmaj_hi),
-                         desc_join(wlo + ((part * kSpan + ks * 2048) >> 4), mnmaj_hi), idesc_w, part > 0 || ks > 0);
-#pragma unroll
-        for (int part = 0; part < 3; ++part)   // hi hi, hi lo, lo hi
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_ts_elect(tw + kTmP, tw + (part == 2 ? 32 : 0) + ks * 8,
-                         desc_join(plo + (((part == 1 ? kSpan : 0) + ks * 2048) >> 4), mnmaj_hi), idesc_p,
-                         part > 0 || ks > 0);
-        tc_commit_elect(P_DONE + 8 * g);
-      }
-      if (t < 64) ga_s[t] = pre;
-      if (t == 63) ga_s[64] = pre;
-      ok = mbar_wait(P_DONE + 8 * g, ph, abort_flag, wait_ns);
-      ph ^= 1;
-      tc_fence_after();
-      {
-        uint32_t d[64], o[32];
-        tmem_ld32(tw + kTmW + lane_base, d);
-        tmem_ld32(tw + kTmW + lane_base + 32, d + 32);
-        tmem_wait_ld32(d);
-        tie32(d + 32);
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          split2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]), d[j], o[j]);
-        tmem_st32(tw + kTmW + lane_base, d);
-        tmem_st32(tw + kTmW + lane_base + 32, o);
-        tmem_ld32(tw + kTmP + lane_base, d);
-        tmem_ld32(tw + kTmP + lane_base + 32, d + 32);
-        tmem_wait_ld32(d);
-        tie32(d + 32);
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          split2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]), d[j], o[j]);
-        tmem_st32(tw + kTmP + lane_base, d);
-        tmem_st32(tw + kTmP + lane_base + 32, o);
-        tmem_wait_st();
-        tc_fence_before();
-      }
-      mbar_arrive(READY + 8 * g);
+      bulk_load_elect(at + C::kKQ, image + (size_t)c * a.H * I::kBytes, I::kBytes, FULL + 8 * st);
     }
-    if (w == 0) {
-      tc_commit_elect(DRAIN + 8 * g);
-      drain_wait(DRAIN + 8 * g, 0);
-    }
+    for (int i = max(0, c - C::kStages); i < c; ++i)   // every copy has landed before the CTA ends
+      drain_wait(FULL + 8 * (i % C::kStages), (i / C::kStages) & 1);
   } else {
-    // ------------------------------------------------------------------ recurrence
-    reg_inc<160>();
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    const bool krow = tid < 64;
-    const int row = tid & 63;
-    constexpr uint32_t idesc_x = idesc_bf16(128, 64, true);
-    constexpr uint32_t idesc_d = idesc_bf16(128, kCols, true);
+    // ------------------------------------------------------------------ the state's holders
+    const int wg = warp >> 2, r128 = tid & 127;   // columns 32 wg .. of the slice; row of d_k and TMEM lane
+    const uint32_t lane_base = ((uint32_t)((warp & 3) * 32) << 16) + 32 * wg;
+    const bool krow = r128 < 64;
+    const int row = r128 & 63;
+    constexpr uint32_t idesc = idesc_bf16(128, kCols, true);   // A K-major, B along N
     const uint32_t hi_word = (uint32_t)(sdesc_sw128(0, 16, 1024) >> 32);
     const uint32_t s_lo = (uint32_t)sdesc_sw128(sbase + C::kSOff, 16, 1024);
     const uint32_t r_lo = (uint32_t)sdesc_sw128(sbase + C::kROff, 16, 1024);
     const size_t hs = (size_t)a.H * D;
-    float* Sg = a.state + (((size_t)b * a.H + h) * D + (tid < D ? tid : 0)) * D + cs * kCols;
-    float S[kCols];
+    const int col = cs * kCols + 32 * wg;
+    float* Sg = a.state + (((size_t)b * a.H + h) * D + (r128 < D ? r128 : 0)) * D + col;
+    float S[32];
 #pragma unroll
-    for (int j = 0; j < kCols; j += 4) {
-      const float4 v = tid < D ? *reinterpret_cast<const float4*>(Sg + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < 32; j += 4) {
+      const float4 v = r128 < D ? *reinterpret_cast<const float4*>(Sg + j) : make_float4(0.f, 0.f, 0.f, 0.f);
       S[j] = v.x; S[j + 1] = v.y; S[j + 2] = v.z; S[j + 3] = v.w;
     }
-    const __nv_bfloat16* Vg = static_cast<const __nv_bfloat16*>(a.v) + (size_t)t0 * hs + (size_t)h * D + cs * kCols;
-    __nv_bfloat16* Og = static_cast<__nv_bfloat16*>(a.out) + (size_t)t0 * hs + (size_t)h * D + cs * kCols;
+    const __nv_bfloat16* Vg = static_cast<const __nv_bfloat16*>(a.v) + (size_t)(t0 + first) * hs + (size_t)h * D + col;
+    __nv_bfloat16* Og = static_cast<__nv_bfloat16*>(a.out) + (size_t)(t0 + first) * hs + (size_t)h * D + col;
+    const int left = n - first;   // tokens from the segment's first one on
     uint4 vr[4];
     auto fetch_v = [&](int c) {   // this lane's row of chunk c's V (K lanes)
-      if (krow && c * kChunk + row < n) {
+      if (krow && c < chunks && c * kChunk + row < left) {
         const uint4* src = reinterpret_cast<const uint4*>(Vg + (size_t)(c * kChunk + row) * hs);
 #pragma unroll
         for (int q = 0; q < 4; ++q) vr[q] = __ldg(src + q);
       }
     };
-    // this lane's row of S in two terms, as k = row of a product, columns along N: hi 32, lo 32
-    auto stage_s = [&]() {
-      if (tid < D) {
+    // 32 columns of a row in two terms: the row is the products' k, its columns lie along N
+    auto stage_row = [&](uint8_t* hi_row, int lo_off, int r, const float* x) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t hi[4], lo[4];
+      for (int q = 0; q < 4; ++q) {
+        uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) split2(S[8 * q + 2 * e], S[8 * q + 2 * e + 1], hi[e], lo[e]);
-          uint8_t* at = smem + C::kSOff + tid * 128;
-          *reinterpret_cast<uint4*>(at + ((q ^ (tid & 7)) * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(at + (((4 + q) ^ (tid & 7)) * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
+        for (int e = 0; e < 4; ++e) split2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1], hi[e], lo[e]);
+        uint8_t* at = hi_row + (((4 * wg + q) ^ (r & 7)) * 16);
+        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at + lo_off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
       fence_async_shared();
     };
     fetch_v(0);
-    stage_s();
-    float oq[kCols];        // Q lanes: g_i S^T q_i of the chunk
-    uint32_t od[kCols];     // and its P r
+    if (r128 < D) stage_row(smem + C::kSOff + r128 * 128, D * 128, r128, S);
+    uint32_t o2[16];     // Q lanes: the chunk's outputs, bf16 pairs
     // Test hook: DRAIN's phase completes only through this group's own commit below.
-    bool ok = args.stall ? mbar_wait(DRAIN + 16, 0, abort_flag, wait_ns) : true;
+    bool ok = args.stall ? mbar_wait(DRAIN, 0, abort_flag, wait_ns) : true;
     auto write_out = [&](int c) {
-      if (krow || c * kChunk + row >= n) return;
+      if (krow || c * kChunk + row >= left) return;
       uint4* dst = reinterpret_cast<uint4*>(Og + (size_t)(c * kChunk + row) * hs);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t p[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 8 * q + 2 * e;
-          p[e] = pack_bf16x2(oq[j] + __uint_as_float(od[j]), oq[j + 1] + __uint_as_float(od[j + 1]));
-        }
-        dst[q] = make_uint4(p[0], p[1], p[2], p[3]);
-      }
+      for (int q = 0; q < 4; ++q) dst[q] = make_uint4(o2[4 * q], o2[4 * q + 1], o2[4 * q + 2], o2[4 * q + 3]);
     };
+    // W (or P) r, W and r in two terms each: hi hi, hi lo, lo hi
+    auto issue_r = [&](uint32_t d_tmem, uint32_t a_lo, int a_bytes) {
+#pragma unroll
+      for (int part = 0; part < 3; ++part)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_ss_elect(d_tmem, desc_join(a_lo + (uint32_t)(((part == 2 ? a_bytes : 0) + ks * 32) >> 4), hi_word),
+                       desc_join(r_lo + (uint32_t)(((part == 1 ? kSpan : 0) + ks * 2048) >> 4), hi_word), idesc,
+                       part > 0 || ks > 0);
+    };
+#pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
-      const int g = c & 1, st = c % kStagesCh, cnt = min(kChunk, n - c * kChunk);
-      const float* ga_s = reinterpret_cast<const float*>(smem + C::kGateOff) + g * C::kGate + 3 * kChunk;
-      const uint32_t tw = tmem + kTmGroup * g;
-      ok = mbar_wait(READY + 8 * g, (c >> 1) & 1, abort_flag, wait_ns) && ok;
-      ok = group_all(1, ok);
+      const int st = c % C::kStages;
+      const uint32_t stage = sbase + st * C::kStage;
+      ok = mbar_wait(FULL + 8 * st, (c / C::kStages) & 1, abort_flag, wait_ns) && ok;
+      ok = group_all(ok);
       if (!ok) break;
       if (warp == 0) {
         tc_fence_after();
-        const uint32_t kq = (uint32_t)sdesc_sw128(sbase + st * C::kStage, 16, 1024);
+        const uint32_t kq = (uint32_t)sdesc_sw128(stage, 16, 1024);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t o = (uint32_t)((ks >> 2) * 2 * kSpan + (ks & 3) * 32) >> 4;
-          mma_ss_elect(tmem + kTmX, desc_join(kq + o, hi_word), desc_join(s_lo + (ks * 2048 >> 4), hi_word), idesc_x, ks > 0);
-        }
+        for (int part = 0; part < 2; ++part)   // S hi, S lo
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t o = (uint32_t)((ks >> 2) * 2 * kSpan + (ks & 3) * 32) >> 4;
+            mma_ss_elect(tmem + kTmX, desc_join(kq + o, hi_word),
+                         desc_join(s_lo + (uint32_t)((part * D * 128 + ks * 2048) >> 4), hi_word), idesc,
+                         part > 0 || ks > 0);
+          }
         tc_commit_elect(X_DONE);
       }
       if (c > 0) write_out(c - 1);   // while the product runs
-      const float ga = ga_s[row], gc = ga_s[64];
+      const float* ga_s = reinterpret_cast<const float*>(smem + st * C::kStage + C::kKQ + I::kG);
+      const float ga = ga_s[row], gc = ga_s[kChunk - 1];
       ok = mbar_wait(X_DONE, c & 1, abort_flag, wait_ns);
       tc_fence_after();
+      float oq[32];   // Q lanes: g_i S^T q_i
       {
-        uint32_t x[64];
+        uint32_t x[32];
         tmem_ld32(tmem + kTmX + lane_base, x);
-        tmem_ld32(tmem + kTmX + lane_base + 32, x + 32);
         tmem_wait_ld32(x);
-        tie32(x + 32);
         if (krow) {
-          const bool live = row < cnt;
+          const bool live = c * kChunk + row < left;
+          float r[32];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            uint32_t hi[4], lo[4];
             const uint32_t vw[4] = {vr[q].x, vr[q].y, vr[q].z, vr[q].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int j = 8 * q + 2 * e;
-              const float x0 = __uint_as_float(x[j]) + __uint_as_float(x[32 + j]);
-              const float x1 = __uint_as_float(x[j + 1]) + __uint_as_float(x[33 + j]);
-              const float r0 = live ? fmaf(-ga, x0, bf16_lo(vw[e])) : 0.f;
-              const float r1 = live ? fmaf(-ga, x1, bf16_hi(vw[e])) : 0.f;
-              split2(r0, r1, hi[e], lo[e]);
+              r[j] = live ? fmaf(-ga, __uint_as_float(x[j]), bf16_lo(vw[e])) : 0.f;
+              r[j + 1] = live ? fmaf(-ga, __uint_as_float(x[j + 1]), bf16_hi(vw[e])) : 0.f;
             }
-            uint8_t* at = smem + C::kROff + row * 128 + ((q ^ (row & 7)) * 16);
-            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(at + kSpan) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
-          fence_async_shared();
+          stage_row(smem + C::kROff + row * 128, kSpan, row, r);
           fetch_v(c + 1);
         } else {
 #pragma unroll
-          for (int j = 0; j < kCols; ++j) oq[j] = ga * (__uint_as_float(x[j]) + __uint_as_float(x[32 + j]));
+          for (int j = 0; j < 32; ++j) oq[j] = ga * __uint_as_float(x[j]);
         }
       }
       tc_fence_before();
-      ok = group_all(1, ok);
+      ok = group_all(ok);
       if (!ok) break;
       if (warp == 0) {
         tc_fence_after();
-#pragma unroll
-        for (int part = 0; part < 3; ++part) {   // W_hi r_hi, W_hi r_lo, W_lo r_hi
-          const uint32_t at = tw + kTmW + (part == 2 ? 32 : 0), rb = r_lo + (part == 1 ? kSpan >> 4 : 0);
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_ts_elect(tmem + kTmD, at + ks * 8, desc_join(rb + (ks * 2048 >> 4), hi_word), idesc_d, part > 0 || ks > 0);
-        }
+        const uint32_t w_lo = (uint32_t)sdesc_sw128(stage + C::kKQ, 16, 1024);
+        issue_r(tmem + kTmD, w_lo, I::kW);
         tc_commit_elect(D_DONE);
-#pragma unroll
-        for (int part = 0; part < 3; ++part) {   // P likewise
-          const uint32_t at = tw + kTmP + (part == 2 ? 32 : 0), rb = r_lo + (part == 1 ? kSpan >> 4 : 0);
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_ts_elect(tmem + kTmX, at + ks * 8, desc_join(rb + (ks * 2048 >> 4), hi_word), idesc_d, part > 0 || ks > 0);
-        }
+        // P stands in rows 64 .. 127 of its operand; the bytes before it make rows that are not read
+        issue_r(tmem + kTmO, w_lo + ((I::kP - kSpan) >> 4), kSpan);
         tc_commit_elect(O_DONE);
-        tc_commit_elect(OUT_EMPTY + 8 * g);
-        tc_commit_elect(KQ_EMPTY + 8 * st);
+        tc_commit_elect(EMPTY + 8 * st);
       }
       ok = mbar_wait(D_DONE, c & 1, abort_flag, wait_ns);
       tc_fence_after();
@@ -627,27 +690,35 @@ __global__ void __launch_bounds__(kThreadsCh, 1)
         tmem_ld32(tmem + kTmD + lane_base, x);
         tmem_wait_ld32(x);
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) S[j] = fmaf(gc, S[j], __uint_as_float(x[j]));
+        for (int j = 0; j < 32; ++j) S[j] = fmaf(gc, S[j], __uint_as_float(x[j]));
       }
-      stage_s();
+      if (r128 < D) stage_row(smem + C::kSOff + r128 * 128, D * 128, r128, S);
       ok = mbar_wait(O_DONE, c & 1, abort_flag, wait_ns) && ok;
       tc_fence_after();
-      tmem_ld32(tmem + kTmX + lane_base, od);
-      tmem_wait_ld32(od);
+      {
+        uint32_t x[32];
+        tmem_ld32(tmem + kTmO + lane_base, x);
+        tmem_wait_ld32(x);
+        if (!krow) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            o2[j] = pack_bf16x2(oq[2 * j] + __uint_as_float(x[2 * j]), oq[2 * j + 1] + __uint_as_float(x[2 * j + 1]));
+        }
+      }
       tc_fence_before();
     }
-    ok = group_all(1, ok && !*abort_flag);
+    ok = group_all(ok && !*abort_flag);
     if (ok) {
       write_out(chunks - 1);
-      if (tid < D) {
+      if (r128 < D) {
 #pragma unroll
-        for (int j = 0; j < kCols; j += 4)
+        for (int j = 0; j < 32; j += 4)
           *reinterpret_cast<float4*>(Sg + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
       }
     }
     if (warp == 0) {
-      tc_commit_elect(DRAIN + 16);
-      drain_wait(DRAIN + 16, 0);
+      tc_commit_elect(DRAIN);
+      drain_wait(DRAIN, 0);
     }
   }
   // ------------------------------------------------------------------ teardown
@@ -655,34 +726,60 @@ __global__ void __launch_bounds__(kThreadsCh, 1)
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort_flag) set_status(a.status, kStatusTimeout);
-  if (warp == kProducer) {
+  if (warp == kProducerSt) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 256);
   }
 }
 
+// Chunks of each sequence per pair of launches: all of them when that takes no more than kSlots
+// images (0.8 GB at d = 128), else as many as that allows, but at least 8 - a pair of launches
+// costs some 10 us beside the work.
+constexpr long long kSlots = 16384;
+int segment_chunks(int B, int H, int max_tokens) {
+  const int all = (max_tokens + kChunk - 1) / kChunk;
+  return (int)std::min<long long>(all, std::max<long long>(8, kSlots / ((long long)B * H)));
+}
+
 template <int D>
-cudaError_t launch_chunk_typed(const GdnUpdateArgs& a, cudaStream_t s) {
+cudaError_t launch_chunk_typed(const GdnUpdateArgs& a, void* workspace, cudaStream_t s) {
   CUtensorMap mq, mk;
   if (!make_map(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, D, a.H, a.token_capacity, 1, kChunk) ||
       !make_map(&mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.k, D, a.H, a.token_capacity, 1, kChunk))
     return cudaErrorInvalidValue;
-  constexpr int smem = Ch<D>::kSmem;
-  static_assert(smem <= 232448, "shared memory of one CTA");
-  cudaError_t e = check_cuda(cudaFuncSetAttribute(gdn_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
-                             "cudaFuncSetAttribute(gdn_chunk_kernel)");
+  cudaError_t e = check_cuda(cudaFuncSetAttribute(gdn_chunk_prepare_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  Pr<D>::kSmem),
+                             "cudaFuncSetAttribute(gdn_chunk_prepare_kernel)");
   if (e != cudaSuccess) return e;
-  ChunkArgs ca{a, 0, 0};
+  e = check_cuda(cudaFuncSetAttribute(gdn_chunk_state_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, St<D>::kSmem),
+                 "cudaFuncSetAttribute(gdn_chunk_state_kernel)");
+  if (e != cudaSuccess) return e;
+  const int all = (a.max_tokens + kChunk - 1) / kChunk, segment = segment_chunks(a.B, a.H, a.max_tokens);
+  ChunkArgs ca{a, static_cast<uint8_t*>(workspace), 0, 0, segment, 0, 0};
   tc_wait_settings(&ca.wait_ns, &ca.stall);
-  return check_cuda(launch_pdl(gdn_chunk_kernel<D>, dim3((unsigned)((long long)a.B * a.H * (D / kCols))),
-                               dim3(kThreadsCh), (size_t)smem, s, mq, mk, ca),
-                    "launch gdn_chunk_kernel");
+  for (int c0 = 0; c0 < all; c0 += segment) {
+    ca.chunk0 = c0;
+    ca.span = std::min(segment, all - c0);
+    e = check_cuda(launch_pdl(gdn_chunk_prepare_kernel<D>, dim3((unsigned)((long long)a.B * a.H * ca.span)),
+                              dim3(kThreadsPr), (size_t)Pr<D>::kSmem, s, mq, mk, ca),
+                   "launch gdn_chunk_prepare_kernel");
+    if (e != cudaSuccess) return e;
+    e = check_cuda(launch_pdl(gdn_chunk_state_kernel<D>, dim3((unsigned)((long long)a.B * a.H * (D / kCols))),
+                              dim3(kThreadsSt), (size_t)St<D>::kSmem, s, mq, mk, ca),
+                   "launch gdn_chunk_state_kernel");
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t launch_gdn_chunk(const GdnUpdateArgs& a, cudaStream_t s) {
-  return a.d == 64 ? launch_chunk_typed<64>(a, s) : launch_chunk_typed<128>(a, s);
+size_t gdn_chunk_workspace(int B, int H, int d, int max_tokens) {
+  return (size_t)B * H * segment_chunks(B, H, max_tokens) * (d == 64 ? Image<64>::kBytes : Image<128>::kBytes);
+}
+
+cudaError_t launch_gdn_chunk(const GdnUpdateArgs& a, void* workspace, cudaStream_t s) {
+  return a.d == 64 ? launch_chunk_typed<64>(a, workspace, s) : launch_chunk_typed<128>(a, workspace, s);
 }
 
 }  // namespace tva

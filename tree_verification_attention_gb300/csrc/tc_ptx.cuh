@@ -146,6 +146,24 @@ __device__ __forceinline__ void tma_load_3d_hint_elect(uint32_t dst, const CUten
       : "memory");
 }
 
+// Contiguous copies (16-byte aligned, a multiple of 16 bytes): global to shared memory, completing on
+// an mbarrier, by one elected lane of a converged warp; shared memory to global, complete on return.
+__device__ __forceinline__ void bulk_load_elect(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}\n" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile(
+      "cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
+      "cp.async.bulk.commit_group;\n\t"
+      "cp.async.bulk.wait_group 0;" ::"l"(dst),
+      "r"(src), "r"(bytes)
+      : "memory");
+}
+
 // Starts fetching a box into L2 only (no shared memory, no completion tracking).
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(

@@ -1,5 +1,6 @@
 // tva_host.cu - the C ABI (include/tva.h): argument checks, workspace layout and
 // kernel launches.  No torch types cross this boundary.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -293,6 +294,12 @@ tva_status check_kv4_rows(int num_rows, int Hkv, int d, int dtype, long long kv_
 // Tokens a sequence up to which bf16 calls of gdn_update_varlen run the recurrence, and beyond which
 // they run in chunks on the tensor cores.
 constexpr int kMaxRecurrent = 16;
+
+// Workspace of gdn_update_varlen; 0: the recurrence, which needs none.
+size_t gdn_workspace(int B, int H, int d, int dtype, int rows, int max_tokens) {
+  const int longest = std::min(max_tokens, rows);
+  return dtype == TVA_BF16 && longest > kMaxRecurrent ? tva::gdn_chunk_workspace(B, H, d, longest) : 0;
+}
 
 // The checks that gdn_update_varlen and commit_accepted_gdn share (`rows` token or node rows;
 // q and out null in a commit): shapes, types, pointers, and that the state, written in place,
@@ -697,20 +704,30 @@ tva_status gdn_tree_verify(int batch, int num_heads, int head_dim, tva_dtype dty
   return tva::launch_gdn(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TVA_OK : TVA_ERR_CUDA;
 }
 
+size_t tva_gdn_workspace_size(int batch, int num_heads, int head_dim, tva_dtype dtype, int token_capacity,
+                              int max_tokens) {
+  if (batch < 1 || num_heads < 1 || (long long)batch * num_heads > (1LL << 24) || (head_dim != 64 && head_dim != 128))
+    return 0;
+  return gdn_workspace(batch, num_heads, head_dim, (int)dtype, token_capacity, max_tokens);
+}
+
 tva_status gdn_update_varlen(int batch, int num_heads, int head_dim, tva_dtype dtype, int token_capacity,
                              int max_tokens, const int32_t* cu_tokens, const void* q, const void* k, const void* v,
-                             const float* beta, const float* alpha, float* state, void* out, int32_t* dev_status,
-                             void* stream) {
+                             const float* beta, const float* alpha, float* state, void* out, void* workspace,
+                             size_t workspace_bytes, int32_t* dev_status, void* stream) {
   if (max_tokens < 0 || (token_capacity > 0 && (!q || !out))) return TVA_ERR_INVALID_ARG;
   const tva_status st = check_gdn_update(batch, num_heads, head_dim, (int)dtype, token_capacity, cu_tokens, q, k, v,
                                          beta, alpha, state, out, dev_status);
   if (st != TVA_OK) return st;
-  const tva::GdnUpdateArgs a{batch, num_heads, head_dim, max_tokens, token_capacity, dtype == TVA_BF16 ? 1 : 0,
+  const int longest = std::min(max_tokens, token_capacity);   // a longer sequence is out of bounds either way
+  const tva::GdnUpdateArgs a{batch, num_heads, head_dim, longest, token_capacity, dtype == TVA_BF16 ? 1 : 0,
                              cu_tokens, nullptr, nullptr, q, k, v, beta, alpha, state, out, dev_status};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool chunks = dtype == TVA_BF16 && max_tokens > kMaxRecurrent && token_capacity > 0;
-  return (chunks ? tva::launch_gdn_chunk(a, s) : tva::launch_gdn_recurrent(a, s)) == cudaSuccess ? TVA_OK
-                                                                                                   : TVA_ERR_CUDA;
+  const size_t need = gdn_workspace(batch, num_heads, head_dim, (int)dtype, token_capacity, max_tokens);
+  if (need == 0) return tva::launch_gdn_recurrent(a, s) == cudaSuccess ? TVA_OK : TVA_ERR_CUDA;
+  if (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return TVA_ERR_WORKSPACE;
+  return tva::launch_gdn_chunk(a, workspace, s) == cudaSuccess ? TVA_OK : TVA_ERR_CUDA;
 }
 
 tva_status commit_accepted_gdn(int batch, int num_heads, int head_dim, tva_dtype dtype, int node_capacity,

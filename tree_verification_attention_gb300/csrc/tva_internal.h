@@ -196,7 +196,8 @@ cudaError_t launch_commit_kv4(const CommitArgs& a, int Hkv, int d, int dtype, cu
 cudaError_t launch_sampling(const SamplingArgs& a, cudaStream_t s);
 cudaError_t launch_gdn(const GdnArgs& a, cudaStream_t s);
 cudaError_t launch_gdn_recurrent(const GdnUpdateArgs& a, cudaStream_t s);
-// The same in chunks on the tensor cores; bf16, no path.
-cudaError_t launch_gdn_chunk(const GdnUpdateArgs& a, cudaStream_t s);
+// The same in chunks on the tensor cores; bf16, no path.  Workspace: gdn_chunk_workspace bytes.
+cudaError_t launch_gdn_chunk(const GdnUpdateArgs& a, void* workspace, cudaStream_t s);
+size_t gdn_chunk_workspace(int B, int H, int d, int max_tokens);
 
 }  // namespace tva
