@@ -448,8 +448,9 @@ __global__ void __launch_bounds__(kThreadsPr, 3)
 // ------------------------------------------------------------------ the walk from state to state
 
 constexpr int kCols = 64;             // columns of d_v per CTA, 32 per thread
-constexpr int kThreadsSt = 288;
+constexpr int kThreadsSt = 320;
 constexpr int kProducerSt = 8;
+constexpr int kMmaSt = 9;
 constexpr uint32_t kTmX = 0, kTmD = 64, kTmO = 128;   // TMEM columns: X, W r, P r
 
 template <int D>
@@ -465,21 +466,6 @@ struct St {
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
-// Barrier over the 256 threads that hold the state; true in all of them when `ok` is in all.
-__device__ __forceinline__ bool group_all(bool ok) {
-  uint32_t r;
-  __syncwarp();
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.and.pred p, 1, 256, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(r)
-      : "r"((uint32_t)ok)
-      : "memory");
-  return r != 0;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreadsSt, 1)
     gdn_chunk_state_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -494,9 +480,9 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + C::kBarOff;
   const uint32_t FULL = bars, EMPTY = bars + 24, X_DONE = bars + 48, D_DONE = bars + 56, O_DONE = bars + 64,
-                 DRAIN = bars + 72;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 80);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + 84);
+                 DRAIN = bars + 72, S_READY = bars + 80, R_READY = bars + 88;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 96);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + 100);
 
   if (tid == kProducerSt * 32) {
     prefetch_tmap(&tm_q);
@@ -509,6 +495,8 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
     mbar_init(D_DONE, 1);
     mbar_init(O_DONE, 1);
     mbar_init(DRAIN, 1);
+    mbar_init(S_READY, 256);
+    mbar_init(R_READY, 256);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -555,16 +543,64 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
     }
     for (int i = max(0, c - C::kStages); i < c; ++i)   // every copy has landed before the CTA ends
       drain_wait(FULL + 8 * (i % C::kStages), (i / C::kStages) & 1);
-  } else {
-    // ------------------------------------------------------------------ the state's holders
-    const int wg = warp >> 2, r128 = tid & 127;   // columns 32 wg .. of the slice; row of d_k and TMEM lane
-    const uint32_t lane_base = ((uint32_t)((warp & 3) * 32) << 16) + 32 * wg;
-    const bool krow = r128 < 64;
-    const int row = r128 & 63;
+  } else if (warp == kMmaSt) {
+    // ------------------------------------------------------------------ MMA issuer
+    // A converged warp of its own: issued from one of the state's warps, between its barriers, an MMA
+    // took 55 to 100 clocks to issue instead of about as long as it runs.
     constexpr uint32_t idesc = idesc_bf16(128, kCols, true);   // A K-major, B along N
     const uint32_t hi_word = (uint32_t)(sdesc_sw128(0, 16, 1024) >> 32);
     const uint32_t s_lo = (uint32_t)sdesc_sw128(sbase + C::kSOff, 16, 1024);
     const uint32_t r_lo = (uint32_t)sdesc_sw128(sbase + C::kROff, 16, 1024);
+    const uint32_t st_lo = (uint32_t)sdesc_sw128(sbase, 16, 1024);
+    // W (or P) r, W and r in two terms each: hi hi, hi lo, lo hi
+    auto issue_r = [&](uint32_t d_tmem, uint32_t a_lo, int a_bytes) {
+#pragma unroll
+      for (int part = 0; part < 3; ++part)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_ss_elect(d_tmem, desc_join(a_lo + (uint32_t)(((part == 2 ? a_bytes : 0) + ks * 32) >> 4), hi_word),
+                       desc_join(r_lo + (uint32_t)(((part == 1 ? kSpan : 0) + ks * 2048) >> 4), hi_word), idesc,
+                       part > 0 || ks > 0);
+    };
+    // Test hook: DRAIN's phase completes only through this warp's own commit below.
+    bool ok = !(args.stall && !warp_wait(DRAIN, 0, abort_flag, wait_ns));
+    for (int c = 0; ok && c < chunks; ++c) {
+      const int st = c % C::kStages;
+      const uint32_t stage = st_lo + (uint32_t)(st * C::kStage >> 4);
+      if (!(ok = warp_wait(FULL + 8 * st, (c / C::kStages) & 1, abort_flag, wait_ns))) break;
+      if (!(ok = warp_wait(S_READY, c & 1, abort_flag, wait_ns))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int part = 0; part < 2; ++part)   // S hi, S lo
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t o = (uint32_t)((ks >> 2) * 2 * kSpan + (ks & 3) * 32) >> 4;
+          mma_ss_elect(tmem + kTmX, desc_join(stage + o, hi_word),
+                       desc_join(s_lo + (uint32_t)((part * D * 128 + ks * 2048) >> 4), hi_word), idesc,
+                       part > 0 || ks > 0);
+        }
+      tc_commit_elect(X_DONE);
+      if (!(ok = warp_wait(R_READY, c & 1, abort_flag, wait_ns))) break;
+      tc_fence_after();
+      const uint32_t w_lo = stage + (C::kKQ >> 4);
+      issue_r(tmem + kTmD, w_lo, I::kW);
+      tc_commit_elect(D_DONE);
+      // P stands in rows 64 .. 127 of its operand; the bytes before it make rows that are not read
+      issue_r(tmem + kTmO, w_lo + ((I::kP - kSpan) >> 4), kSpan);
+      tc_commit_elect(O_DONE);
+      tc_commit_elect(EMPTY + 8 * st);
+    }
+    tc_commit_elect(DRAIN);
+    drain_wait(DRAIN, 0);
+  } else {
+    // ------------------------------------------------------------------ the state's holders
+    // No barrier among them: what a thread reads of TMEM or writes to shared memory is ordered by the
+    // products' own barriers.  X is issued when all have staged S (S_READY), so have read the
+    // last X and W r; P r is overwritten once all have staged r (R_READY), so have read it.
+    const int wg = warp >> 2, r128 = tid & 127;   // columns 32 wg .. of the slice; row of d_k and TMEM lane
+    const uint32_t lane_base = ((uint32_t)((warp & 3) * 32) << 16) + 32 * wg;
+    const bool krow = r128 < 64;
+    const int row = r128 & 63;
     const size_t hs = (size_t)a.H * D;
     const int col = cs * kCols + 32 * wg;
     float* Sg = a.state + (((size_t)b * a.H + h) * D + (r128 < D ? r128 : 0)) * D + col;
@@ -601,51 +637,43 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
     fetch_v(0);
     if (r128 < D) stage_row(smem + C::kSOff + r128 * 128, D * 128, r128, S);
     uint32_t o2[16];     // Q lanes: the chunk's outputs, bf16 pairs
-    // Test hook: DRAIN's phase completes only through this group's own commit below.
-    bool ok = args.stall ? mbar_wait(DRAIN, 0, abort_flag, wait_ns) : true;
+    bool ok = true;
     auto write_out = [&](int c) {
       if (krow || c * kChunk + row >= left) return;
       uint4* dst = reinterpret_cast<uint4*>(Og + (size_t)(c * kChunk + row) * hs);
 #pragma unroll
       for (int q = 0; q < 4; ++q) dst[q] = make_uint4(o2[4 * q], o2[4 * q + 1], o2[4 * q + 2], o2[4 * q + 3]);
     };
-    // W (or P) r, W and r in two terms each: hi hi, hi lo, lo hi
-    auto issue_r = [&](uint32_t d_tmem, uint32_t a_lo, int a_bytes) {
+    tc_fence_before();
+    mbar_arrive(S_READY);
+    float oq[32];   // Q lanes: g_i S^T q_i
+    auto finish_out = [&]() {   // this lane's outputs of the last chunk: its P r added
+      uint32_t x[32];
+      tmem_ld32(tmem + kTmO + lane_base, x);
+      tmem_wait_ld32(x);
+      if (!krow) {
 #pragma unroll
-      for (int part = 0; part < 3; ++part)
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_ss_elect(d_tmem, desc_join(a_lo + (uint32_t)(((part == 2 ? a_bytes : 0) + ks * 32) >> 4), hi_word),
-                       desc_join(r_lo + (uint32_t)(((part == 1 ? kSpan : 0) + ks * 2048) >> 4), hi_word), idesc,
-                       part > 0 || ks > 0);
+        for (int j = 0; j < 16; ++j)
+          o2[j] = pack_bf16x2(oq[2 * j] + __uint_as_float(x[2 * j]), oq[2 * j + 1] + __uint_as_float(x[2 * j + 1]));
+      }
     };
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
       const int st = c % C::kStages;
-      const uint32_t stage = sbase + st * C::kStage;
-      ok = mbar_wait(FULL + 8 * st, (c / C::kStages) & 1, abort_flag, wait_ns) && ok;
-      ok = group_all(ok);
-      if (!ok) break;
-      if (warp == 0) {
+      if (c > 0) {   // the last chunk's outputs, while X is computed
+        ok = __all_sync(0xffffffffu, mbar_wait(O_DONE, (c - 1) & 1, abort_flag, wait_ns));
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t kq = (uint32_t)sdesc_sw128(stage, 16, 1024);
-#pragma unroll
-        for (int part = 0; part < 2; ++part)   // S hi, S lo
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t o = (uint32_t)((ks >> 2) * 2 * kSpan + (ks & 3) * 32) >> 4;
-            mma_ss_elect(tmem + kTmX, desc_join(kq + o, hi_word),
-                         desc_join(s_lo + (uint32_t)((part * D * 128 + ks * 2048) >> 4), hi_word), idesc,
-                         part > 0 || ks > 0);
-          }
-        tc_commit_elect(X_DONE);
+        finish_out();
+        write_out(c - 1);
       }
-      if (c > 0) write_out(c - 1);   // while the product runs
+      ok = __all_sync(0xffffffffu, mbar_wait(FULL + 8 * st, (c / C::kStages) & 1, abort_flag, wait_ns));
+      if (!ok) break;
       const float* ga_s = reinterpret_cast<const float*>(smem + st * C::kStage + C::kKQ + I::kG);
       const float ga = ga_s[row], gc = ga_s[kChunk - 1];
-      ok = mbar_wait(X_DONE, c & 1, abort_flag, wait_ns);
+      ok = __all_sync(0xffffffffu, mbar_wait(X_DONE, c & 1, abort_flag, wait_ns));
+      if (!ok) break;
       tc_fence_after();
-      float oq[32];   // Q lanes: g_i S^T q_i
       {
         uint32_t x[32];
         tmem_ld32(tmem + kTmX + lane_base, x);
@@ -664,26 +692,16 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
             }
           }
           stage_row(smem + C::kROff + row * 128, kSpan, row, r);
-          fetch_v(c + 1);
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) oq[j] = ga * __uint_as_float(x[j]);
         }
       }
       tc_fence_before();
-      ok = group_all(ok);
+      mbar_arrive(R_READY);
+      fetch_v(c + 1);
+      ok = __all_sync(0xffffffffu, mbar_wait(D_DONE, c & 1, abort_flag, wait_ns));
       if (!ok) break;
-      if (warp == 0) {
-        tc_fence_after();
-        const uint32_t w_lo = (uint32_t)sdesc_sw128(stage + C::kKQ, 16, 1024);
-        issue_r(tmem + kTmD, w_lo, I::kW);
-        tc_commit_elect(D_DONE);
-        // P stands in rows 64 .. 127 of its operand; the bytes before it make rows that are not read
-        issue_r(tmem + kTmO, w_lo + ((I::kP - kSpan) >> 4), kSpan);
-        tc_commit_elect(O_DONE);
-        tc_commit_elect(EMPTY + 8 * st);
-      }
-      ok = mbar_wait(D_DONE, c & 1, abort_flag, wait_ns);
       tc_fence_after();
       {
         uint32_t x[32];
@@ -693,32 +711,19 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
         for (int j = 0; j < 32; ++j) S[j] = fmaf(gc, S[j], __uint_as_float(x[j]));
       }
       if (r128 < D) stage_row(smem + C::kSOff + r128 * 128, D * 128, r128, S);
-      ok = mbar_wait(O_DONE, c & 1, abort_flag, wait_ns) && ok;
-      tc_fence_after();
-      {
-        uint32_t x[32];
-        tmem_ld32(tmem + kTmO + lane_base, x);
-        tmem_wait_ld32(x);
-        if (!krow) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            o2[j] = pack_bf16x2(oq[2 * j] + __uint_as_float(x[2 * j]), oq[2 * j + 1] + __uint_as_float(x[2 * j + 1]));
-        }
-      }
       tc_fence_before();
+      if (c + 1 < chunks) mbar_arrive(S_READY);
     }
-    ok = group_all(ok && !*abort_flag);
-    if (ok) {
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(O_DONE, (chunks - 1) & 1, abort_flag, wait_ns));
+    if (ok && !*abort_flag) {
+      tc_fence_after();
+      finish_out();
       write_out(chunks - 1);
       if (r128 < D) {
 #pragma unroll
         for (int j = 0; j < 32; j += 4)
           *reinterpret_cast<float4*>(Sg + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
       }
-    }
-    if (warp == 0) {
-      tc_commit_elect(DRAIN);
-      drain_wait(DRAIN, 0);
     }
   }
   // ------------------------------------------------------------------ teardown
