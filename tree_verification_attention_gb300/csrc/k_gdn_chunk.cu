@@ -12,7 +12,7 @@
 //     P = lower(G o Q K^T) T diag(beta)  [C x C]      O  = g o (Q S) + P r
 //
 // Two kernels.  The first makes W and P of every (sequence, head, chunk), all at once, one CTA of
-// four warps each (three resident per SM), and leaves them in the workspace as the second's shared
+// four warps each (four resident per SM), and leaves them in the workspace as the second's shared
 // memory will hold them (48 KB at d = 128).  The second walks a sequence's chunks, one CTA per (sequence,
 // head, 64 columns of d_v): a producer warp fetches K, Q, W and P a chunk ahead, eight warps hold the
 // state in registers (fp32; thread = row of d_k = TMEM lane, 32 columns) and run
@@ -90,17 +90,18 @@ struct Pr {
   static constexpr int kHalves = D / 64;
   static constexpr int kKQ = kHalves * 2 * kSpan;       // per half: K rows, then Q rows
   static constexpr int kAOff = kKQ;                     // A, then T; then T hi, lo (for W)
-  static constexpr int kTOff = kAOff + kChunk * kLd * 4;   // T hi, lo (for P)
-  static constexpr int kXOff = kTOff + 2 * kSpan;
+  // T hi, lo (for P) over Q, whose products are done by then.  On their way out: W hi over K, W lo
+  // over T's terms for W, P over T's terms for P
+  static constexpr int kTHi = kSpan, kTLo = D == 128 ? 3 * kSpan : kAOff + kChunk * kLd * 4;
+  static constexpr int kXOff = kAOff + kChunk * kLd * 4 + (D == 128 ? 0 : kSpan);
   static constexpr int kGateOff = kXOff + 32 * kLdX * 4;   // alpha, beta, G_Ci
   static constexpr int kBarOff = kGateOff + 3 * kChunk * 4;
   static constexpr int kSmem = kBarOff + 64 + 1024;
   static_assert(kChunk * kLd * 4 % 1024 == 0 && kChunk * kLd * 4 >= 2 * kSpan, "T's terms over A");
-  static_assert(Image<D>::kBytes <= kTOff, "the image over K, Q and T's terms for W");
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreadsPr, 3)
+__global__ void __launch_bounds__(kThreadsPr, 4)
     gdn_chunk_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                              const ChunkArgs args) {
   using C = Pr<D>;
@@ -123,12 +124,22 @@ __global__ void __launch_bounds__(kThreadsPr, 3)
   if (!sequence_ok(a, t0, n) || c * kChunk >= n) return;   // the state kernel reports bad bounds
   const int cnt = min(kChunk, n - c * kChunk);
 
-  if (t == 0) {
-    mbar_init(KQ_FULL, 1);
-    mbar_init(P_DONE, 1);
-    mbar_init(DRAIN, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
+  if (w == 0) {   // the copies start before anything else
+    if (lane == 0) {
+      mbar_init(KQ_FULL, 1);
+      mbar_init(P_DONE, 1);
+      mbar_init(DRAIN, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    int z = t0 + c * kChunk;
+    if (!TVA_CHECK(z >= 0 && z < a.token_capacity, a.status)) z = 0;
+    mbar_expect_tx_elect(KQ_FULL, (uint32_t)C::kKQ);
+    for (int hf = 0; hf < C::kHalves; ++hf) {
+      tma_load_3d_elect(sbase + hf * 2 * kSpan, &tm_k, 64 * hf, h, z, KQ_FULL);
+      tma_load_3d_elect(sbase + hf * 2 * kSpan + kSpan, &tm_q, 64 * hf, h, z, KQ_FULL);
+    }
   }
   float* As = reinterpret_cast<float*>(smem + C::kAOff);
   float* Xs = reinterpret_cast<float*>(smem + C::kXOff);
@@ -155,15 +166,6 @@ __global__ void __launch_bounds__(kThreadsPr, 3)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t lane_base = (uint32_t)(w * 32) << 16;
-  if (w == 0) {
-    int z = t0 + c * kChunk;
-    if (!TVA_CHECK(z >= 0 && z < a.token_capacity, a.status)) z = 0;
-    mbar_expect_tx_elect(KQ_FULL, (uint32_t)C::kKQ);
-    for (int hf = 0; hf < C::kHalves; ++hf) {
-      tma_load_3d_elect(sbase + hf * 2 * kSpan, &tm_k, 64 * hf, h, z, KQ_FULL);
-      tma_load_3d_elect(sbase + hf * 2 * kSpan + kSpan, &tm_q, 64 * hf, h, z, KQ_FULL);
-    }
-  }
   constexpr uint32_t idesc_a = idesc_bf16(128, 64, false);                 // [K; Q] K^T: both K-major
   constexpr uint32_t idesc_w = idesc_bf16(128, 64, true) | (1u << 15);     // K^T T: A along M, B along N
   constexpr uint32_t idesc_p = idesc_bf16(128, 64, true);                  // A in TMEM
@@ -339,7 +341,7 @@ __global__ void __launch_bounds__(kThreadsPr, 3)
   {
     // T diag(beta) (for P) and diag(G_Ci) T diag(beta) (for W, over A's place), two terms each:
     // row i is the products' k = i, its columns lie along N
-    const int i = t >> 1, j0 = 32 * (t & 1);
+    const int i = t & 63, j0 = 32 * (t >> 6);
     const float en = en_s[i];
     float x[32];
 #pragma unroll
@@ -355,8 +357,8 @@ __global__ void __launch_bounds__(kThreadsPr, 3)
       const int at = i * 128 + (((j0 >> 3) + q) ^ (i & 7)) * 16;
 #pragma unroll
       for (int e = 0; e < 4; ++e) split2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1], hi[e], lo[e]);
-      *reinterpret_cast<uint4*>(smem + C::kTOff + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(smem + C::kTOff + kSpan + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      *reinterpret_cast<uint4*>(smem + C::kTHi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(smem + C::kTLo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) split2(x[8 * q + 2 * e] * en, x[8 * q + 2 * e + 1] * en, hi[e], lo[e]);
       *reinterpret_cast<uint4*>(smem + C::kAOff + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -389,16 +391,16 @@ __global__ void __launch_bounds__(kThreadsPr, 3)
   ok = __syncthreads_and(ok);
   if (ok && w == 0) {   // P while W is written out
     tc_fence_after();
-    const uint32_t plo = (uint32_t)sdesc_sw128(sbase + C::kTOff, 16, 1024);
+    const uint32_t plo = (uint32_t)sdesc_sw128(sbase, 16, 1024);
 #pragma unroll
     for (int part = 0; part < 3; ++part)   // hi hi, hi lo, lo hi
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
         mma_ts_elect(tmem + kTmWork, tmem + (part == 2 ? 32 : 0) + ks * 8,
-                     desc_join(plo + (((part == 1 ? kSpan : 0) + ks * 2048) >> 4), desc_hi), idesc_p, part > 0 || ks > 0);
+                     desc_join(plo + (((part == 1 ? C::kTLo : C::kTHi) + ks * 2048) >> 4), desc_hi), idesc_p, part > 0 || ks > 0);
     tc_commit_elect(P_DONE);
   }
-  // a row of 64 tokens in two terms, over K, Q and T
+  // a row of 64 tokens in two terms
   auto write_row = [&](uint8_t* hi_row, uint8_t* lo_row, int r) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
@@ -411,8 +413,8 @@ __global__ void __launch_bounds__(kThreadsPr, 3)
       *reinterpret_cast<uint4*>(lo_row + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   };
-  if (t < D) write_row(smem + t * 128, smem + I::kW + t * 128, t);
-  if (t < kChunk) *reinterpret_cast<float*>(smem + I::kG + 4 * t) = pre;
+  if (t < D) write_row(smem + (t < 64 ? 0 : 2 * kSpan) + (t & 63) * 128, smem + C::kAOff + t * 128, t);
+  if (t < kChunk) al_s[t] = pre;
   if (ok) ok = mbar_wait(P_DONE, 0, abort_flag, wait_ns);
   tc_fence_after();
   if (t >= kChunk) {   // P is in lanes 64 .. 127
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kThreadsPr, 3)
     tmem_ld32(tmem + kTmWork + lane_base + 32, d + 32);
     tmem_wait_ld32(d);
     tie32(d + 32);
-    write_row(smem + I::kP + row * 128, smem + I::kP + kSpan + row * 128, row);
+    write_row(smem + C::kTHi + row * 128, smem + C::kTLo + row * 128, row);
   }
   fence_async_shared();
   tc_fence_before();
@@ -429,16 +431,18 @@ __global__ void __launch_bounds__(kThreadsPr, 3)
     tc_commit_elect(DRAIN);
     drain_wait(DRAIN, 0);
     drain_wait(KQ_FULL, 0);
+    if (t == 0) set_status(a.status, kStatusTimeout);
   }
-  if (t == 0) {
-    if (ok) {
-      const size_t slot = ((size_t)b * args.segment + (c - args.chunk0)) * a.H + h;
-      bulk_store(args.images + slot * I::kBytes, sbase, I::kBytes);
-    } else {
-      set_status(a.status, kStatusTimeout);
-    }
+  if (!ok) __syncthreads();   // uniform over the CTA
+  if (ok && t == 0) {
+    uint8_t* image = args.images + (((size_t)b * args.segment + (c - args.chunk0)) * a.H + h) * I::kBytes;
+    for (int hf = 0; hf < C::kHalves; ++hf) bulk_store(image + hf * kSpan, sbase + hf * 2 * kSpan, kSpan);
+    bulk_store(image + I::kW, sbase + C::kAOff, I::kW);
+    bulk_store(image + I::kP, sbase + C::kTHi, kSpan);
+    bulk_store(image + I::kP + kSpan, sbase + C::kTLo, kSpan);
+    bulk_store(image + I::kG, sbase + C::kGateOff, kChunk * 4);
+    bulk_stores_done();
   }
-  __syncthreads();
   if (w == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 128);

@@ -147,7 +147,8 @@ __device__ __forceinline__ void tma_load_3d_hint_elect(uint32_t dst, const CUten
 }
 
 // Contiguous copies (16-byte aligned, a multiple of 16 bytes): global to shared memory, completing on
-// an mbarrier, by one elected lane of a converged warp; shared memory to global, complete on return.
+// an mbarrier, by one elected lane of a converged warp; shared memory to global, by the thread that
+// then waits until all of its own are complete.
 __device__ __forceinline__ void bulk_load_elect(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -155,13 +156,12 @@ __device__ __forceinline__ void bulk_load_elect(uint32_t dst, const void* src, u
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
+
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile(
-      "cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
-      "cp.async.bulk.commit_group;\n\t"
-      "cp.async.bulk.wait_group 0;" ::"l"(dst),
-      "r"(src), "r"(bytes)
-      : "memory");
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_stores_done() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // Starts fetching a box into L2 only (no shared memory, no completion tracking).
