@@ -451,30 +451,41 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
 
 // ------------------------------------------------------------------ the walk from state to state
 
-constexpr int kCols = 64;             // columns of d_v per CTA, 32 per thread
-constexpr int kThreadsSt = 320;
-constexpr int kProducerSt = 8;
-constexpr int kMmaSt = 9;
 constexpr uint32_t kTmX = 0, kTmD = 64, kTmO = 128;   // TMEM columns: X, W r, P r
 
-template <int D>
+// NS columns of d_v per CTA, 16 per thread.  With 64 columns S and r are two tiles, of the hi and the lo
+// terms (rows of 64 columns).  With 32 a row of one tile holds both, so that one product of N = 64 does for
+// both (an MMA of N = 32 takes as long: reading its A operand bounds it) and their sums are added after.
+template <int D, int NS>
 struct St {
+  static constexpr bool kPair = NS == 32;
+  static constexpr int kHolders = 8 * NS;   // threads that hold the state
+  static constexpr int kProducer = kHolders / 32, kMma = kProducer + 1, kThreads = kHolders + 64;
   static constexpr int kHalves = D / 64;
   static constexpr int kKQ = kHalves * 2 * kSpan;
   static constexpr int kStages = D == 128 ? 2 : 3;
   static constexpr int kStage = (kKQ + Image<D>::kBytes + 1023) / 1024 * 1024;
-  static constexpr int kSOff = kStages * kStage;        // S hi, lo: [D rows of d_k][64 columns]
-  static constexpr int kROff = kSOff + 2 * D * 128;     // r hi, lo: [64 tokens][64 columns]
-  static constexpr int kBarOff = kROff + 2 * kSpan;
+  static constexpr int kSOff = kStages * kStage;                      // S: [D rows of d_k]
+  static constexpr int kROff = kSOff + (kPair ? 1 : 2) * D * 128;     // r: [64 tokens]
+  static constexpr int kBarOff = kROff + (kPair ? 1 : 2) * kSpan;
   static constexpr int kSmem = kBarOff + 128 + 1024;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreadsSt, 1)
+// A pair of fp32 values in two terms.
+__device__ __forceinline__ void split2(uint64_t x2, uint32_t& hi, uint32_t& lo) {
+  float a, b;
+  f2_unpack(x2, a, b);
+  hi = pack_bf16x2(a, b);
+  f2_unpack(f2_fma(f2_pack(bf16_lo(hi), bf16_hi(hi)), f2_pack(-1.f, -1.f), x2), a, b);
+  lo = pack_bf16x2(a, b);
+}
+
+template <int D, int NS>
+__global__ void __launch_bounds__(St<D, NS>::kThreads, 1)
     gdn_chunk_state_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                            const ChunkArgs args) {
-  using C = St<D>;
+  using C = St<D, NS>;
   using I = Image<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -488,7 +499,7 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 96);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + 100);
 
-  if (tid == kProducerSt * 32) {
+  if (tid == C::kProducer * 32) {
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
     for (int s = 0; s < C::kStages; ++s) {
@@ -499,14 +510,14 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
     mbar_init(D_DONE, 1);
     mbar_init(O_DONE, 1);
     mbar_init(DRAIN, 1);
-    mbar_init(S_READY, 256);
-    mbar_init(R_READY, 256);
+    mbar_init(S_READY, C::kHolders);
+    mbar_init(R_READY, C::kHolders);
     *abort_flag = 0;
     fence_mbar_init();
   }
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int CS = D / kCols;
+  constexpr int CS = D / NS;
   const int cs = blockIdx.x % CS, bh = blockIdx.x / CS;
   const int b = bh / a.H, h = bh % a.H;
   const int t0 = __ldg(a.cu + b);
@@ -518,7 +529,7 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
   const int chunks = min(args.span, (n + kChunk - 1) / kChunk - args.chunk0);   // in this segment
   if (chunks <= 0) return;
   const int first = args.chunk0 * kChunk;   // the segment's first token
-  if (warp == kProducerSt) {
+  if (warp == C::kProducer) {
     tmem_alloc(smem_u32(tmem_slot), 256);
     tmem_relinquish();
   }
@@ -527,7 +538,7 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == kProducerSt) {
+  if (warp == C::kProducer) {
     // ------------------------------------------------------------------ producer
     bool ok = true;
     int c = 0;
@@ -547,11 +558,12 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
     }
     for (int i = max(0, c - C::kStages); i < c; ++i)   // every copy has landed before the CTA ends
       drain_wait(FULL + 8 * (i % C::kStages), (i / C::kStages) & 1);
-  } else if (warp == kMmaSt) {
+  } else if (warp == C::kMma) {
     // ------------------------------------------------------------------ MMA issuer
     // A converged warp of its own: issued from one of the state's warps, between its barriers, an MMA
     // took 55 to 100 clocks to issue instead of about as long as it runs.
-    constexpr uint32_t idesc = idesc_bf16(128, kCols, true);   // A K-major, B along N
+    constexpr uint32_t idesc = idesc_bf16(128, 64, true);   // A K-major, B along N
+    constexpr uint32_t idesc_half = idesc_bf16(128, 32, true);
     const uint32_t hi_word = (uint32_t)(sdesc_sw128(0, 16, 1024) >> 32);
     const uint32_t s_lo = (uint32_t)sdesc_sw128(sbase + C::kSOff, 16, 1024);
     const uint32_t r_lo = (uint32_t)sdesc_sw128(sbase + C::kROff, 16, 1024);
@@ -559,12 +571,14 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
     // W (or P) r, W and r in two terms each: hi hi, hi lo, lo hi
     auto issue_r = [&](uint32_t d_tmem, uint32_t a_lo, int a_bytes) {
 #pragma unroll
-      for (int part = 0; part < 3; ++part)
+      for (int part = 0; part < 3; ++part) {
+        if (C::kPair && part == 1) continue;   // in the first product's other columns
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           mma_ss_elect(d_tmem, desc_join(a_lo + (uint32_t)(((part == 2 ? a_bytes : 0) + ks * 32) >> 4), hi_word),
-                       desc_join(r_lo + (uint32_t)(((part == 1 ? kSpan : 0) + ks * 2048) >> 4), hi_word), idesc,
-                       part > 0 || ks > 0);
+                       desc_join(r_lo + (uint32_t)(((part == 1 ? kSpan : 0) + ks * 2048) >> 4), hi_word),
+                       C::kPair && part == 2 ? idesc_half : idesc, part > 0 || ks > 0);
+      }
     };
     // Test hook: DRAIN's phase completes only through this warp's own commit below.
     bool ok = !(args.stall && !warp_wait(DRAIN, 0, abort_flag, wait_ns));
@@ -575,7 +589,7 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
       if (!(ok = warp_wait(S_READY, c & 1, abort_flag, wait_ns))) break;
       tc_fence_after();
 #pragma unroll
-      for (int part = 0; part < 2; ++part)   // S hi, S lo
+      for (int part = 0; part < (C::kPair ? 1 : 2); ++part)   // S hi, S lo
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t o = (uint32_t)((ks >> 2) * 2 * kSpan + (ks & 3) * 32) >> 4;
@@ -601,64 +615,86 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
     // No barrier among them: what a thread reads of TMEM or writes to shared memory is ordered by the
     // products' own barriers.  X is issued when all have staged S (S_READY), so have read the
     // last X and W r; P r is overwritten once all have staged r (R_READY), so have read it.
-    const int wg = warp >> 2, r128 = tid & 127;   // columns 32 wg .. of the slice; row of d_k and TMEM lane
-    const uint32_t lane_base = ((uint32_t)((warp & 3) * 32) << 16) + 32 * wg;
+    const int wg = warp >> 2, r128 = tid & 127;   // columns 16 wg .. of the slice; row of d_k and TMEM lane
+    const uint32_t lane_base = ((uint32_t)((warp & 3) * 32) << 16) + 16 * wg;
     const bool krow = r128 < 64;
     const int row = r128 & 63;
     const size_t hs = (size_t)a.H * D;
-    const int col = cs * kCols + 32 * wg;
+    const int col = cs * NS + 16 * wg;
     float* Sg = a.state + (((size_t)b * a.H + h) * D + (r128 < D ? r128 : 0)) * D + col;
-    float S[32];
+    uint64_t S2[8];   // this row's 16 columns, in pairs
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      const float4 v = r128 < D ? *reinterpret_cast<const float4*>(Sg + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-      S[j] = v.x; S[j + 1] = v.y; S[j + 2] = v.z; S[j + 3] = v.w;
+    for (int q = 0; q < 4; ++q) {
+      const float4 v = r128 < D ? *reinterpret_cast<const float4*>(Sg + 4 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
+      S2[2 * q] = f2_pack(v.x, v.y);
+      S2[2 * q + 1] = f2_pack(v.z, v.w);
     }
     const __nv_bfloat16* Vg = static_cast<const __nv_bfloat16*>(a.v) + (size_t)(t0 + first) * hs + (size_t)h * D + col;
     __nv_bfloat16* Og = static_cast<__nv_bfloat16*>(a.out) + (size_t)(t0 + first) * hs + (size_t)h * D + col;
     const int left = n - first;   // tokens from the segment's first one on
-    uint4 vr[4];
+    uint4 vr[2];
     auto fetch_v = [&](int c) {   // this lane's row of chunk c's V (K lanes)
       if (krow && c < chunks && c * kChunk + row < left) {
         const uint4* src = reinterpret_cast<const uint4*>(Vg + (size_t)(c * kChunk + row) * hs);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) vr[q] = __ldg(src + q);
+        vr[0] = __ldg(src);
+        vr[1] = __ldg(src + 1);
       }
     };
-    // 32 columns of a row in two terms: the row is the products' k, its columns lie along N
-    auto stage_row = [&](uint8_t* hi_row, int lo_off, int r, const float* x) {
+    // 16 columns of a row in two terms: the row is the products' k, its columns lie along N
+    auto stage_row = [&](int off, int lo_off, int r, const uint64_t* x2) {
+      uint8_t* at = smem + off + r * 128;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 2; ++q) {
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1], hi[e], lo[e]);
-        uint8_t* at = hi_row + (((4 * wg + q) ^ (r & 7)) * 16);
-        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(at + lo_off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        for (int e = 0; e < 4; ++e) split2(x2[4 * q + e], hi[e], lo[e]);
+        const int ch = 2 * wg + q;
+        *reinterpret_cast<uint4*>(at + ((ch ^ (r & 7)) * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at + (C::kPair ? ((ch + 4) ^ (r & 7)) * 16 : lo_off + ((ch ^ (r & 7)) * 16))) =
+            make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
       fence_async_shared();
     };
+    // 16 columns of a product (the two halves' sum where S or r stood side by side), in pairs
+    auto load = [&](uint32_t tm, uint64_t* x2) {
+      uint32_t x[16];
+      tmem_ld16(tmem + tm + lane_base, x);
+      if constexpr (C::kPair) {
+        uint32_t y[16];
+        tmem_ld16(tmem + tm + 32 + lane_base, y);
+        tmem_wait_ld16(x);
+        tie16(y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          x2[j] = f2_add(f2_pack(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])),
+                         f2_pack(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])));
+      } else {
+        tmem_wait_ld16(x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x2[j] = f2_pack(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+      }
+    };
     fetch_v(0);
-    if (r128 < D) stage_row(smem + C::kSOff + r128 * 128, D * 128, r128, S);
-    uint32_t o2[16];     // Q lanes: the chunk's outputs, bf16 pairs
+    if (r128 < D) stage_row(C::kSOff, D * 128, r128, S2);
     bool ok = true;
-    auto write_out = [&](int c) {
+    tc_fence_before();
+    mbar_arrive(S_READY);
+    uint64_t oq[8];   // Q lanes: g_i S^T q_i
+    auto write_out = [&](int c) {   // the chunk's outputs: its P r added
+      uint64_t x2[8];
+      load(kTmO, x2);
       if (krow || c * kChunk + row >= left) return;
       uint4* dst = reinterpret_cast<uint4*>(Og + (size_t)(c * kChunk + row) * hs);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) dst[q] = make_uint4(o2[4 * q], o2[4 * q + 1], o2[4 * q + 2], o2[4 * q + 3]);
-    };
-    tc_fence_before();
-    mbar_arrive(S_READY);
-    float oq[32];   // Q lanes: g_i S^T q_i
-    auto finish_out = [&]() {   // this lane's outputs of the last chunk: its P r added
-      uint32_t x[32];
-      tmem_ld32(tmem + kTmO + lane_base, x);
-      tmem_wait_ld32(x);
-      if (!krow) {
+      for (int q = 0; q < 2; ++q) {
+        uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          o2[j] = pack_bf16x2(oq[2 * j] + __uint_as_float(x[2 * j]), oq[2 * j + 1] + __uint_as_float(x[2 * j + 1]));
+        for (int e = 0; e < 4; ++e) {
+          float lo, hi;
+          f2_unpack(f2_add(oq[4 * q + e], x2[4 * q + e]), lo, hi);
+          w[e] = pack_bf16x2(lo, hi);
+        }
+        dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     };
 #pragma unroll 1
@@ -668,8 +704,8 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(O_DONE, (c - 1) & 1, abort_flag, wait_ns));
         if (!ok) break;
         tc_fence_after();
-        finish_out();
         write_out(c - 1);
+        __syncwarp();
       }
       ok = __all_sync(0xffffffffu, mbar_wait(FULL + 8 * st, (c / C::kStages) & 1, abort_flag, wait_ns));
       if (!ok) break;
@@ -678,28 +714,22 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(X_DONE, c & 1, abort_flag, wait_ns));
       if (!ok) break;
       tc_fence_after();
-      {
-        uint32_t x[32];
-        tmem_ld32(tmem + kTmX + lane_base, x);
-        tmem_wait_ld32(x);
-        if (krow) {
-          const bool live = c * kChunk + row < left;
-          float r[32];
+      uint64_t x2[8];
+      load(kTmX, x2);
+      if (krow) {   // uniform over the warp
+        const uint64_t g2 = f2_pack(-ga, -ga);
+        const uint32_t vw[8] = {vr[0].x, vr[0].y, vr[0].z, vr[0].w, vr[1].x, vr[1].y, vr[1].z, vr[1].w};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t vw[4] = {vr[q].x, vr[q].y, vr[q].z, vr[q].w};
+        for (int j = 0; j < 8; ++j) x2[j] = f2_fma(g2, x2[j], f2_pack(bf16_lo(vw[j]), bf16_hi(vw[j])));
+        if (c * kChunk + row >= left) {   // past the end: K holds other rows there
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = 8 * q + 2 * e;
-              r[j] = live ? fmaf(-ga, __uint_as_float(x[j]), bf16_lo(vw[e])) : 0.f;
-              r[j + 1] = live ? fmaf(-ga, __uint_as_float(x[j + 1]), bf16_hi(vw[e])) : 0.f;
-            }
-          }
-          stage_row(smem + C::kROff + row * 128, kSpan, row, r);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) oq[j] = ga * __uint_as_float(x[j]);
+          for (int j = 0; j < 8; ++j) x2[j] = 0;
         }
+        stage_row(C::kROff, kSpan, row, x2);
+      } else {
+        const uint64_t g2 = f2_pack(ga, ga);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) oq[j] = f2_mul(g2, x2[j]);
       }
       tc_fence_before();
       mbar_arrive(R_READY);
@@ -707,26 +737,26 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(D_DONE, c & 1, abort_flag, wait_ns));
       if (!ok) break;
       tc_fence_after();
-      {
-        uint32_t x[32];
-        tmem_ld32(tmem + kTmD + lane_base, x);
-        tmem_wait_ld32(x);
+      load(kTmD, x2);
+      const uint64_t gc2 = f2_pack(gc, gc);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) S[j] = fmaf(gc, S[j], __uint_as_float(x[j]));
-      }
-      if (r128 < D) stage_row(smem + C::kSOff + r128 * 128, D * 128, r128, S);
+      for (int j = 0; j < 8; ++j) S2[j] = f2_fma(gc2, S2[j], x2[j]);
+      if (r128 < D) stage_row(C::kSOff, D * 128, r128, S2);
       tc_fence_before();
       if (c + 1 < chunks) mbar_arrive(S_READY);
     }
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(O_DONE, (chunks - 1) & 1, abort_flag, wait_ns));
-    if (ok && !*abort_flag) {
+    if (ok && __all_sync(0xffffffffu, !*abort_flag)) {
       tc_fence_after();
-      finish_out();
       write_out(chunks - 1);
       if (r128 < D) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 4)
-          *reinterpret_cast<float4*>(Sg + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+        for (int q = 0; q < 4; ++q) {
+          float4 v;
+          f2_unpack(S2[2 * q], v.x, v.y);
+          f2_unpack(S2[2 * q + 1], v.z, v.w);
+          *reinterpret_cast<float4*>(Sg + 4 * q) = v;
+        }
       }
     }
   }
@@ -735,7 +765,7 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort_flag) set_status(a.status, kStatusTimeout);
-  if (warp == kProducerSt) {
+  if (warp == C::kProducer) {
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }
@@ -744,10 +774,23 @@ __global__ void __launch_bounds__(kThreadsSt, 1)
 // Chunks of each sequence per pair of launches: all of them when that takes no more than kSlots
 // images (0.8 GB at d = 128), else as many as that allows, but at least 8 - a pair of launches
 // costs some 10 us beside the work.
+constexpr int kSms = 152;
 constexpr long long kSlots = 16384;
 int segment_chunks(int B, int H, int max_tokens) {
   const int all = (max_tokens + kChunk - 1) / kChunk;
   return (int)std::min<long long>(all, std::max<long long>(8, kSlots / ((long long)B * H)));
+}
+
+template <int D, int NS>
+cudaError_t launch_state(const ChunkArgs& ca, const CUtensorMap& mq, const CUtensorMap& mk, cudaStream_t s) {
+  using C = St<D, NS>;
+  const cudaError_t e = check_cuda(
+      cudaFuncSetAttribute(gdn_chunk_state_kernel<D, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem),
+      "cudaFuncSetAttribute(gdn_chunk_state_kernel)");
+  if (e != cudaSuccess) return e;
+  return check_cuda(launch_pdl(gdn_chunk_state_kernel<D, NS>, dim3((unsigned)((long long)ca.a.B * ca.a.H * (D / NS))),
+                               dim3(C::kThreads), (size_t)C::kSmem, s, mq, mk, ca),
+                    "launch gdn_chunk_state_kernel");
 }
 
 template <int D>
@@ -760,10 +803,10 @@ cudaError_t launch_chunk_typed(const GdnUpdateArgs& a, void* workspace, cudaStre
                                                   Pr<D>::kSmem),
                              "cudaFuncSetAttribute(gdn_chunk_prepare_kernel)");
   if (e != cudaSuccess) return e;
-  e = check_cuda(cudaFuncSetAttribute(gdn_chunk_state_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, St<D>::kSmem),
-                 "cudaFuncSetAttribute(gdn_chunk_state_kernel)");
-  if (e != cudaSuccess) return e;
   const int all = (a.max_tokens + kChunk - 1) / kChunk, segment = segment_chunks(a.B, a.H, a.max_tokens);
+  // A chunk takes a CTA of 32 columns less time than one of 64, but not half of it: 32 columns while
+  // every CTA then has an SM of its own.
+  const bool narrow = (long long)a.B * a.H * (D / 32) <= kSms;
   ChunkArgs ca{a, static_cast<uint8_t*>(workspace), 0, 0, segment, 0, 0};
   tc_wait_settings(&ca.wait_ns, &ca.stall);
   for (int c0 = 0; c0 < all; c0 += segment) {
@@ -773,9 +816,7 @@ cudaError_t launch_chunk_typed(const GdnUpdateArgs& a, void* workspace, cudaStre
                               dim3(kThreadsPr), (size_t)Pr<D>::kSmem, s, mq, mk, ca),
                    "launch gdn_chunk_prepare_kernel");
     if (e != cudaSuccess) return e;
-    e = check_cuda(launch_pdl(gdn_chunk_state_kernel<D>, dim3((unsigned)((long long)a.B * a.H * (D / kCols))),
-                              dim3(kThreadsSt), (size_t)St<D>::kSmem, s, mq, mk, ca),
-                   "launch gdn_chunk_state_kernel");
+    e = narrow ? launch_state<D, 32>(ca, mq, mk, s) : launch_state<D, 64>(ca, mq, mk, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
