@@ -62,10 +62,14 @@ struct Image {
 };
 
 // Two fp32 values as two packed bf16 terms each: hi + lo.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void split2(uint64_t x2, uint32_t& hi, uint32_t& lo) {
+  float a, b;
+  f2_unpack(x2, a, b);
   hi = pack_bf16x2(a, b);
-  lo = pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi));
+  f2_unpack(f2_fma(f2_pack(bf16_lo(hi), bf16_hi(hi)), f2_pack(-1.f, -1.f), x2), a, b);
+  lo = pack_bf16x2(a, b);
 }
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) { split2(f2_pack(a, b), hi, lo); }
 
 struct ChunkArgs {
   GdnUpdateArgs a;
@@ -213,43 +217,53 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
   if (ok) ok = mbar_wait(P_DONE, 0, abort_flag, wait_ns);
   tc_fence_after();
   {
+    // row `row` of beta_i G_ij k_i.k_j (j < i), or of G_ij q_i.k_j (j <= i); warps of the rows below 32
+    // have none of the columns from 32 on
     uint32_t d[64];
     tmem_ld32(tmem + lane_base, d);
     tmem_ld32(tmem + lane_base + 32, d + 32);
     tmem_wait_ld32(d);
     tie32(d + 32);
-    // row `row` of beta_i G_ij k_i.k_j (j < i), or of G_ij q_i.k_j (j <= i)
     const bool qrow = t >= 64;
     float p = qrow ? 1.f : be;
     const int last = qrow ? row : row - 1;
+    auto decay = [&](int j0) {   // columns j0 + 31 .. j0
 #pragma unroll
-    for (int j4 = 60; j4 >= 0; j4 -= 4) {
-      const float4 a4 = *reinterpret_cast<const float4*>(al_s + j4);
-      const float next = j4 < 60 ? al_s[j4 + 4] : 1.f;
-      const float f[4] = {a4.y, a4.z, a4.w, next};   // alpha of token j + 1
+      for (int j4 = 28; j4 >= 0; j4 -= 4) {
+        const float4 a4 = *reinterpret_cast<const float4*>(al_s + j0 + j4);
+        const float next = j0 + j4 < 60 ? al_s[j0 + j4 + 4] : 1.f;
+        const float f[4] = {a4.y, a4.z, a4.w, next};   // alpha of token j + 1
 #pragma unroll
-      for (int e = 3; e >= 0; --e) {
-        const int j = j4 + e;
-        if (j < row) p *= f[e];
-        d[j] = j <= last ? __float_as_uint(__uint_as_float(d[j]) * p) : 0u;
+        for (int e = 3; e >= 0; --e) {
+          const int j = j0 + j4 + e;
+          if (j < row) p *= f[e];
+          d[j] = j <= last ? __float_as_uint(__uint_as_float(d[j]) * p) : 0u;
+        }
       }
+    };
+    if (w & 1) {
+      decay(32);
+    } else {
+#pragma unroll
+      for (int j = 32; j < 64; ++j) d[j] = 0u;
     }
+    decay(0);
     if (!qrow) {
 #pragma unroll
       for (int j = 0; j < 64; j += 4)
         *reinterpret_cast<uint4*>(As + row * kLd + j) = make_uint4(d[j], d[j + 1], d[j + 2], d[j + 3]);
 #pragma unroll
-      for (int j = 0; j < 64; ++j) d[j] = 0u;
+      for (int j = 0; j < 32; ++j) d[j] = 0u;
+      tmem_st32(tmem + lane_base, d);
+      tmem_st32(tmem + lane_base + 32, d);
     } else {
-      uint32_t o[32];
+      uint32_t lo[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        split2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]), d[j], o[j]);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) d[32 + j] = o[j];
+        split2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]), d[j], lo[j]);
+      tmem_st32(tmem + lane_base, d);   // lower(G o Q K^T) in lanes 64 .. 127, zeros above
+      tmem_st32(tmem + lane_base + 32, lo);
     }
-    tmem_st32(tmem + lane_base, d);   // lower(G o Q K^T) in lanes 64 .. 127, zeros above
-    tmem_st32(tmem + lane_base + 32, d + 32);
     tmem_wait_st();
     tc_fence_before();
   }
@@ -281,39 +295,42 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
   __syncthreads();
   {
     const int o = 32 * (w >> 1), tt = t & 63, i = tt >> 2, c4 = 4 * (tt & 3);
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float x = As[(o + 16 + i) * kLd + o + k];
-      const float4 v = *reinterpret_cast<const float4*>(As + (o + k) * kLd + o + c4);
-      s.x = fmaf(x, v.x, s.x); s.y = fmaf(x, v.y, s.y); s.z = fmaf(x, v.z, s.z); s.w = fmaf(x, v.w, s.w);
-    }
     float* X = Xs + (w >> 1) * 16 * kLdX;
-    *reinterpret_cast<float4*>(X + i * kLdX + c4) = s;
-    __syncthreads();
-    s = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto product = [&](const float* L, const float* R, int ldr) {   // row i of L, columns c4 .. of R
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int k = 0; k < 16; k += 4) {
+        const float4 x4 = *reinterpret_cast<const float4*>(L + i * kLd + k);
+        const float x[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float x = -As[(o + 16 + i) * kLd + o + 16 + k];
-      const float4 v = *reinterpret_cast<const float4*>(X + k * kLdX + c4);
-      s.x = fmaf(x, v.x, s.x); s.y = fmaf(x, v.y, s.y); s.z = fmaf(x, v.z, s.z); s.w = fmaf(x, v.w, s.w);
-    }
-    *reinterpret_cast<float4*>(As + (o + 16 + i) * kLd + o + c4) = s;
+        for (int e = 0; e < 4; ++e) {
+          const float4 v = *reinterpret_cast<const float4*>(R + (k + e) * ldr + c4);
+          s.x = fmaf(x[e], v.x, s.x); s.y = fmaf(x[e], v.y, s.y); s.z = fmaf(x[e], v.z, s.z); s.w = fmaf(x[e], v.w, s.w);
+        }
+      }
+      return s;
+    };
+    *reinterpret_cast<float4*>(X + i * kLdX + c4) = product(As + (o + 16) * kLd + o, As + o * kLd + o, kLd);
+    __syncthreads();
+    const float4 s = product(As + (o + 16) * kLd + o + 16, X, kLdX);
+    *reinterpret_cast<float4*>(As + (o + 16 + i) * kLd + o + c4) = make_float4(-s.x, -s.y, -s.z, -s.w);
   }
   __syncthreads();
   {
-    // 32 x 32 x 32: rows i and i + 16, four columns a thread, on packed pairs of columns
-    const int i = t >> 3, c4 = 4 * (t & 7);
-    auto product = [&](const float* L, const float* R, int ldr, float sign, float4& o0, float4& o1) {
+    // 32 x 32 x 32 on packed pairs of columns.  A21 T11: warp w takes the columns 8 w .. 8 w + 7, whose
+    // rows of T11 begin at 8 w; -T22 (A21 T11): the rows 8 w .. 8 w + 7, whose columns of T22 end there.
+    {
+      const int i = lane >> 1, c4 = 8 * w + 4 * (lane & 1);
+      const float* L = As + (32 + i) * kLd;
       uint64_t s00 = 0, s01 = 0, s10 = 0, s11 = 0;
-#pragma unroll
-      for (int k = 0; k < 32; k += 4) {
-        const float4 x0 = *reinterpret_cast<const float4*>(L + i * kLd + k);
-        const float4 x1 = *reinterpret_cast<const float4*>(L + (i + 16) * kLd + k);
+#pragma unroll 2
+      for (int k = 8 * w; k < 32; k += 4) {
+        const float4 x0 = *reinterpret_cast<const float4*>(L + k);
+        const float4 x1 = *reinterpret_cast<const float4*>(L + 16 * kLd + k);
         const float y0[4] = {x0.x, x0.y, x0.z, x0.w}, y1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(R + (k + e) * ldr + c4);
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(As + (k + e) * kLd + c4);
           const uint64_t p0 = f2_pack(y0[e], y0[e]), p1 = f2_pack(y1[e], y1[e]);
           s00 = f2_fma(p0, v.x, s00);
           s01 = f2_fma(p0, v.y, s01);
@@ -321,21 +338,31 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
           s11 = f2_fma(p1, v.y, s11);
         }
       }
-      f2_unpack(s00, o0.x, o0.y);
-      f2_unpack(s01, o0.z, o0.w);
-      f2_unpack(s10, o1.x, o1.y);
-      f2_unpack(s11, o1.z, o1.w);
-      o0.x *= sign; o0.y *= sign; o0.z *= sign; o0.w *= sign;
-      o1.x *= sign; o1.y *= sign; o1.z *= sign; o1.w *= sign;
-    };
-    float4 o0, o1;
-    product(As + 32 * kLd, As, kLd, 1.f, o0, o1);                 // A21 T11
-    *reinterpret_cast<float4*>(Xs + i * kLdX + c4) = o0;
-    *reinterpret_cast<float4*>(Xs + (i + 16) * kLdX + c4) = o1;
+      *reinterpret_cast<ulonglong2*>(Xs + i * kLdX + c4) = make_ulonglong2(s00, s01);
+      *reinterpret_cast<ulonglong2*>(Xs + (i + 16) * kLdX + c4) = make_ulonglong2(s10, s11);
+    }
     __syncthreads();
-    product(As + 32 * kLd + 32, Xs, kLdX, -1.f, o0, o1);          // -T22 (A21 T11)
-    *reinterpret_cast<float4*>(As + (32 + i) * kLd + c4) = o0;
-    *reinterpret_cast<float4*>(As + (48 + i) * kLd + c4) = o1;
+    {
+      const int i = 8 * w + (lane >> 2), c4 = 4 * (lane & 3);   // columns c4 .. and c4 + 16 ..
+      uint64_t s00 = 0, s01 = 0, s10 = 0, s11 = 0;
+#pragma unroll 2
+      for (int k = 0; k < 8 * w + 8; k += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(As + (32 + i) * kLd + 32 + k);
+        const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const ulonglong2 v0 = *reinterpret_cast<const ulonglong2*>(Xs + (k + e) * kLdX + c4);
+          const ulonglong2 v1 = *reinterpret_cast<const ulonglong2*>(Xs + (k + e) * kLdX + c4 + 16);
+          const uint64_t m = f2_pack(-y[e], -y[e]);
+          s00 = f2_fma(m, v0.x, s00);
+          s01 = f2_fma(m, v0.y, s01);
+          s10 = f2_fma(m, v1.x, s10);
+          s11 = f2_fma(m, v1.y, s11);
+        }
+      }
+      *reinterpret_cast<ulonglong2*>(As + (32 + i) * kLd + c4) = make_ulonglong2(s00, s01);
+      *reinterpret_cast<ulonglong2*>(As + (32 + i) * kLd + c4 + 16) = make_ulonglong2(s10, s11);
+    }
   }
   __syncthreads();
   {
@@ -471,15 +498,6 @@ struct St {
   static constexpr int kSmem = kBarOff + 128 + 1024;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
-
-// A pair of fp32 values in two terms.
-__device__ __forceinline__ void split2(uint64_t x2, uint32_t& hi, uint32_t& lo) {
-  float a, b;
-  f2_unpack(x2, a, b);
-  hi = pack_bf16x2(a, b);
-  f2_unpack(f2_fma(f2_pack(bf16_lo(hi), bf16_hi(hi)), f2_pack(-1.f, -1.f), x2), a, b);
-  lo = pack_bf16x2(a, b);
-}
 
 template <int D, int NS>
 __global__ void __launch_bounds__(St<D, NS>::kThreads, 1)
