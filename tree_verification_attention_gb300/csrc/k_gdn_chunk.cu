@@ -71,6 +71,10 @@ __device__ __forceinline__ void split2(uint64_t x2, uint32_t& hi, uint32_t& lo) 
 }
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) { split2(f2_pack(a, b), hi, lo); }
 
+// Block barrier; true when `ok` is in every thread.  The vote tells the compiler that the answer is the
+// same throughout a warp, so that what follows keeps its operands in uniform registers.
+__device__ __forceinline__ bool all_threads(bool ok) { return __all_sync(0xffffffffu, __syncthreads_and(ok)); }
+
 struct ChunkArgs {
   GdnUpdateArgs a;
   uint8_t* images;       // [B][segment][H]
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
     }
     fence_async_shared();
   }
-  ok = __syncthreads_and(ok);
+  ok = all_threads(ok);
   if (ok && w == 0) {
     tc_fence_after();
     const uint32_t lo = (uint32_t)sdesc_sw128(sbase, 16, 1024);
@@ -393,7 +397,7 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
     }
     fence_async_shared();
   }
-  ok = __syncthreads_and(ok);
+  ok = all_threads(ok);
   if (ok && w == 0) {
     tc_fence_after();
     // rows 64 .. 127 of K^T: the second half (d = 64: Q's, whose products are not read)
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
   tmem_wait_ld32(d);
   tie32(d + 32);
   tc_fence_before();
-  ok = __syncthreads_and(ok);
+  ok = all_threads(ok);
   if (ok && w == 0) {   // P while W is written out
     tc_fence_after();
     const uint32_t plo = (uint32_t)sdesc_sw128(sbase, 16, 1024);
@@ -453,7 +457,7 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
   }
   fence_async_shared();
   tc_fence_before();
-  ok = __syncthreads_and(ok);
+  ok = all_threads(ok);
   if (!ok && w == 0) {   // a wait ran out: what is in flight lands before the CTA ends
     tc_commit_elect(DRAIN);
     drain_wait(DRAIN, 0);
