@@ -108,6 +108,37 @@ struct Pr {
   static_assert(kChunk * kLd * 4 % 1024 == 0 && kChunk * kLd * 4 >= 2 * kSpan, "T's terms over A");
 };
 
+// d += L R over k0 <= k < k1 for a 16 x 8 product (L: 16 rows of pitch ldl, R: rows k of pitch ldr), by
+// one warp: lane 4 g + t holds rows g, g + 8 and columns 2 t, 2 t + 1.  Operands are too small for the
+// tcgen05 forms' 128 rows.  Three tf32 products of two terms each (the first holds the top 11 bits,
+// the second the rest, of which the product takes 11; low times low, 2^-22, is left out): as good as
+// fp32, and a third of the shared-memory reads of fp32 products from registers, which bounded the kernel.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const float (&a)[4], const float (&b)[2]) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])),
+                 "r"(__float_as_uint(a[3])), "r"(__float_as_uint(b[0])), "r"(__float_as_uint(b[1])));
+}
+__device__ __forceinline__ float top11(float x) { return __uint_as_float(__float_as_uint(x) & 0xffffe000u); }
+__device__ __forceinline__ void block_product(const float* L, int ldl, const float* R, int ldr, int k0, int k1, int lane,
+                                              float (&d)[4]) {
+  const float* l = L + (lane >> 2) * ldl + (lane & 3);
+  const float* r = R + (lane & 3) * ldr + (lane >> 2);
+#pragma unroll 2
+  for (int k = k0; k < k1; k += 8) {
+    const float a[4] = {l[k], l[8 * ldl + k], l[k + 4], l[8 * ldl + k + 4]};
+    const float b[2] = {r[k * ldr], r[(k + 4) * ldr]};
+    float ah[4], al[4], bh[2], bl[2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { ah[e] = top11(a[e]); al[e] = a[e] - ah[e]; }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) { bh[e] = top11(b[e]); bl[e] = b[e] - bh[e]; }
+    mma_tf32(d, al, bh);
+    mma_tf32(d, ah, bl);
+    mma_tf32(d, ah, bh);
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreadsPr, 4)
     gdn_chunk_prepare_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -297,75 +328,42 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
     }
   }
   __syncthreads();
+  const int gq = lane >> 2, tq = 2 * (lane & 3);   // this lane's first row and columns of a 16 x 8 product
   {
-    const int o = 32 * (w >> 1), tt = t & 63, i = tt >> 2, c4 = 4 * (tt & 3);
-    float* X = Xs + (w >> 1) * 16 * kLdX;
-    auto product = [&](const float* L, const float* R, int ldr) {   // row i of L, columns c4 .. of R
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-      for (int k = 0; k < 16; k += 4) {
-        const float4 x4 = *reinterpret_cast<const float4*>(L + i * kLd + k);
-        const float x[4] = {x4.x, x4.y, x4.z, x4.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 v = *reinterpret_cast<const float4*>(R + (k + e) * ldr + c4);
-          s.x = fmaf(x[e], v.x, s.x); s.y = fmaf(x[e], v.y, s.y); s.z = fmaf(x[e], v.z, s.z); s.w = fmaf(x[e], v.w, s.w);
-        }
-      }
-      return s;
-    };
-    *reinterpret_cast<float4*>(X + i * kLdX + c4) = product(As + (o + 16) * kLd + o, As + o * kLd + o, kLd);
+    const int o = 32 * (w >> 1), n0 = 8 * (w & 1);   // two blocks of 32 rows; columns of their 16
+    float* X = Xs + (w >> 1) * 16 * kLdX + gq * kLdX + n0 + tq;
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    block_product(As + (o + 16) * kLd + o, kLd, As + o * kLd + o + n0, kLd, 0, 16, lane, d);   // A21 T11
+    *reinterpret_cast<float2*>(X) = make_float2(d[0], d[1]);
+    *reinterpret_cast<float2*>(X + 8 * kLdX) = make_float2(d[2], d[3]);
     __syncthreads();
-    const float4 s = product(As + (o + 16) * kLd + o + 16, X, kLdX);
-    *reinterpret_cast<float4*>(As + (o + 16 + i) * kLd + o + c4) = make_float4(-s.x, -s.y, -s.z, -s.w);
+    d[0] = d[1] = d[2] = d[3] = 0.f;
+    block_product(As + (o + 16) * kLd + o + 16, kLd, Xs + (w >> 1) * 16 * kLdX + n0, kLdX, 0, 16, lane, d);
+    float* T21 = As + (o + 16 + gq) * kLd + o + n0 + tq;
+    *reinterpret_cast<float2*>(T21) = make_float2(-d[0], -d[1]);
+    *reinterpret_cast<float2*>(T21 + 8 * kLd) = make_float2(-d[2], -d[3]);
   }
   __syncthreads();
   {
-    // 32 x 32 x 32 on packed pairs of columns.  A21 T11: warp w takes the columns 8 w .. 8 w + 7, whose
-    // rows of T11 begin at 8 w; -T22 (A21 T11): the rows 8 w .. 8 w + 7, whose columns of T22 end there.
-    {
-      const int i = lane >> 1, c4 = 8 * w + 4 * (lane & 1);
-      const float* L = As + (32 + i) * kLd;
-      uint64_t s00 = 0, s01 = 0, s10 = 0, s11 = 0;
-#pragma unroll 2
-      for (int k = 8 * w; k < 32; k += 4) {
-        const float4 x0 = *reinterpret_cast<const float4*>(L + k);
-        const float4 x1 = *reinterpret_cast<const float4*>(L + 16 * kLd + k);
-        const float y0[4] = {x0.x, x0.y, x0.z, x0.w}, y1[4] = {x1.x, x1.y, x1.z, x1.w};
+    // 32 x 32 x 32: warp w takes 16 rows and 16 columns; T11 has nothing above, T22 nothing right of, its
+    // diagonal
+    const int m0 = 16 * (w & 1), n0 = 16 * (w >> 1);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(As + (k + e) * kLd + c4);
-          const uint64_t p0 = f2_pack(y0[e], y0[e]), p1 = f2_pack(y1[e], y1[e]);
-          s00 = f2_fma(p0, v.x, s00);
-          s01 = f2_fma(p0, v.y, s01);
-          s10 = f2_fma(p1, v.x, s10);
-          s11 = f2_fma(p1, v.y, s11);
-        }
-      }
-      *reinterpret_cast<ulonglong2*>(Xs + i * kLdX + c4) = make_ulonglong2(s00, s01);
-      *reinterpret_cast<ulonglong2*>(Xs + (i + 16) * kLdX + c4) = make_ulonglong2(s10, s11);
+    for (int nt = 0; nt < 16; nt += 8) {   // A21 T11
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      block_product(As + (32 + m0) * kLd, kLd, As + n0 + nt, kLd, n0, 32, lane, d);
+      float* X = Xs + (m0 + gq) * kLdX + n0 + nt + tq;
+      *reinterpret_cast<float2*>(X) = make_float2(d[0], d[1]);
+      *reinterpret_cast<float2*>(X + 8 * kLdX) = make_float2(d[2], d[3]);
     }
     __syncthreads();
-    {
-      const int i = 8 * w + (lane >> 2), c4 = 4 * (lane & 3);   // columns c4 .. and c4 + 16 ..
-      uint64_t s00 = 0, s01 = 0, s10 = 0, s11 = 0;
-#pragma unroll 2
-      for (int k = 0; k < 8 * w + 8; k += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(As + (32 + i) * kLd + 32 + k);
-        const float y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const ulonglong2 v0 = *reinterpret_cast<const ulonglong2*>(Xs + (k + e) * kLdX + c4);
-          const ulonglong2 v1 = *reinterpret_cast<const ulonglong2*>(Xs + (k + e) * kLdX + c4 + 16);
-          const uint64_t m = f2_pack(-y[e], -y[e]);
-          s00 = f2_fma(m, v0.x, s00);
-          s01 = f2_fma(m, v0.y, s01);
-          s10 = f2_fma(m, v1.x, s10);
-          s11 = f2_fma(m, v1.y, s11);
-        }
-      }
-      *reinterpret_cast<ulonglong2*>(As + (32 + i) * kLd + c4) = make_ulonglong2(s00, s01);
-      *reinterpret_cast<ulonglong2*>(As + (32 + i) * kLd + c4 + 16) = make_ulonglong2(s10, s11);
+    for (int nt = 0; nt < 16; nt += 8) {   // -T22 (A21 T11)
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      block_product(As + (32 + m0) * kLd + 32, kLd, Xs + n0 + nt, kLdX, 0, m0 + 16, lane, d);
+      float* T21 = As + (32 + m0 + gq) * kLd + n0 + nt + tq;
+      *reinterpret_cast<float2*>(T21) = make_float2(-d[0], -d[1]);
+      *reinterpret_cast<float2*>(T21 + 8 * kLd) = make_float2(-d[2], -d[3]);
     }
   }
   __syncthreads();
