@@ -58,7 +58,7 @@ def test_workspace_sizes(lib):
     assert size(1, 4, 128, 0, 8, 1 << 30) == 0                      # no more than 8 rows: the recurrence
     one = size(1, 1, 128, 0, 64, 64)
     assert one == size(1, 1, 128, 0, 64, 1 << 30) and size(2, 3, 128, 0, 1000, 128) == 12 * one
-    assert size(64, 32, 128, 0, 1 << 20, 1 << 20) == 64 * 32 * 8 * one   # bounded, whatever the lengths
+    assert size(64, 32, 128, 0, 1 << 20, 1 << 20) == 64 * 32 * 8 * 2 * one   # bounded, whatever the lengths
 
 
 def test_commit_refusals(lib):

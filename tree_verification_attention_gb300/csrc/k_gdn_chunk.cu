@@ -17,7 +17,8 @@
 // head, 64 columns of d_v): a producer warp fetches K, Q, W and P a chunk ahead, eight warps hold the
 // state in registers (fp32; thread = row of d_k = TMEM lane, 32 columns) and run
 //     X = [K; Q] S (one M = 128 product: lanes 0-63 are K rows, 64-127 Q rows) -> r -> W r, P r.
-// Long prompts go in segments of chunks, a pair of launches each, so that the workspace stays bounded.
+// Long prompts go in segments of chunks, a pair of launches each, so that the workspace stays bounded; a
+// segment is prepared beside the walk through the one before it.
 // One kernel that made W and P beside the walk, each CTA for its own columns, took 2.94 ms
 // for 32768 tokens of 32 heads, d = 128: four times the preparation, and 108 KB of code that ran at the
 // rate of its instruction fetches.
@@ -155,12 +156,21 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 24);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + 28);
 
-  pdl_wait();
+  // The first segment waits for what stands before the call.  A later one needs nothing of the walk that
+  // is still at work on the segment before it - the call's inputs are final, and its images go to
+  // the other half of the workspace, last read by the walk before that one, which this one has waited for - so it
+  // starts beside it, on what that leaves free; but the grid ends after that walk, because the next
+  // one, which waits for this grid alone, continues its state: the last CTA sees to that.
+  const bool early = args.chunk0 != 0, last_cta = early && blockIdx.x == gridDim.x - 1;
+  if (!early) pdl_wait();
   pdl_launch_dependents();
   const int h = blockIdx.x % a.H, bc = blockIdx.x / a.H;
   const int b = bc / args.span, c = args.chunk0 + bc % args.span;
   const int t0 = __ldg(a.cu + b), n = __ldg(a.cu + b + 1) - t0;
-  if (!sequence_ok(a, t0, n) || c * kChunk >= n) return;   // the state kernel reports bad bounds
+  if (!sequence_ok(a, t0, n) || c * kChunk >= n) {   // the state kernel reports bad bounds
+    if (last_cta) pdl_wait();
+    return;
+  }
   const int cnt = min(kChunk, n - c * kChunk);
 
   if (w == 0) {   // the copies start before anything else
@@ -476,6 +486,7 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
     tc_fence_after();
     tmem_dealloc(tmem, 128);
   }
+  if (last_cta) pdl_wait();
 }
 
 // ------------------------------------------------------------------ the walk from state to state
@@ -792,10 +803,11 @@ __global__ void __launch_bounds__(St<D, NS>::kThreads, 1)
 }
 
 // Chunks of each sequence per pair of launches: all of them when that takes no more than kSlots
-// images (0.8 GB at d = 128), else as many as that allows, but at least 8 - a pair of launches
-// costs some 10 us beside the work.
+// images (0.4 GB at d = 128), else as many as that allows, but at least 8 (32768 tokens of 32 heads:
+// segments of 32, 64, 128 and 256 chunks 1086, 1016, 984 and 987 us; without the overlap of a segment's preparation
+// and the walk before it 1201, 1123, 1070 and 1045).
 constexpr int kSms = 152;
-constexpr long long kSlots = 16384;
+constexpr long long kSlots = 8192;
 int segment_chunks(int B, int H, int max_tokens) {
   const int all = (max_tokens + kChunk - 1) / kChunk;
   return (int)std::min<long long>(all, std::max<long long>(8, kSlots / ((long long)B * H)));
@@ -827,9 +839,11 @@ cudaError_t launch_chunk_typed(const GdnUpdateArgs& a, void* workspace, cudaStre
   // A chunk takes a CTA of 32 columns less time than one of 64, but not half of it: 32 columns while
   // every CTA then has an SM of its own.
   const bool narrow = (long long)a.B * a.H * (D / 32) <= kSms;
-  ChunkArgs ca{a, static_cast<uint8_t*>(workspace), 0, 0, segment, 0, 0};
+  ChunkArgs ca{a, nullptr, 0, 0, segment, 0, 0};
   tc_wait_settings(&ca.wait_ns, &ca.stall);
-  for (int c0 = 0; c0 < all; c0 += segment) {
+  const size_t half = (size_t)a.B * a.H * segment * Image<D>::kBytes;   // segments take the halves in turn
+  for (int c0 = 0, i = 0; c0 < all; c0 += segment, ++i) {
+    ca.images = static_cast<uint8_t*>(workspace) + (i & 1) * half;
     ca.chunk0 = c0;
     ca.span = std::min(segment, all - c0);
     e = check_cuda(launch_pdl(gdn_chunk_prepare_kernel<D>, dim3((unsigned)((long long)a.B * a.H * ca.span)),
@@ -845,7 +859,8 @@ cudaError_t launch_chunk_typed(const GdnUpdateArgs& a, void* workspace, cudaStre
 }  // namespace
 
 size_t gdn_chunk_workspace(int B, int H, int d, int max_tokens) {
-  return (size_t)B * H * segment_chunks(B, H, max_tokens) * (d == 64 ? Image<64>::kBytes : Image<128>::kBytes);
+  const int segment = segment_chunks(B, H, max_tokens);
+  return (size_t)B * H * segment * (segment * kChunk < max_tokens ? 2 : 1) * (d == 64 ? Image<64>::kBytes : Image<128>::kBytes);
 }
 
 cudaError_t launch_gdn_chunk(const GdnUpdateArgs& a, void* workspace, cudaStream_t s) {
