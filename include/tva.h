@@ -420,8 +420,8 @@ tva_status gdn_tree_verify(int batch, int num_heads, int head_dim, tva_dtype dty
  *                  that is 0.  Its contents between calls mean nothing; calls that overlap on the
  *                  GPU need one each
  * q, k, v, state and out are 16-byte aligned; the state and out overlap no other array.  Arrays of
- * token_capacity rows may be null when it is 0.  fp32 calls, and bf16 calls of at most 16 tokens a
- * sequence, run the recurrence in fp32.  Longer bf16 calls run in chunks of 64 tokens on the tensor
+ * token_capacity rows may be null when it is 0.  fp32 calls, and bf16 calls of at most 24 tokens a
+ * sequence (40 at d = 64), run the recurrence in fp32.  Longer bf16 calls run in chunks of 64 tokens on the tensor
  * cores: fp32 sums of products whose operands are held to 16 bits or more (relative error of the
  * state some 5e-6).  bf16 outputs are rounded once.  tva_diag_set_wait_limit applies to the chunked
  * form.  A sequence outside the bounds is skipped (state and output untouched) with

@@ -54,7 +54,7 @@ def test_update_refusals(lib):
 def test_workspace_sizes(lib):
     size = lib.tva_gdn_workspace_size
     assert size(1, 4, 128, 1, 100, 100) == 0 and size(64, 32, 128, 0, 64, 1) == 0 and size(1, 4, 96, 0, 64, 64) == 0
-    assert size(0, 4, 128, 0, 64, 64) == 0 and size(1, 4, 128, 0, 64, 16) == 0
+    assert size(0, 4, 128, 0, 64, 64) == 0 and size(1, 4, 128, 0, 64, 24) == 0 and size(1, 4, 64, 0, 64, 40) == 0
     assert size(1, 4, 128, 0, 8, 1 << 30) == 0                      # no more than 8 rows: the recurrence
     one = size(1, 1, 128, 0, 64, 64)
     assert one == size(1, 1, 128, 0, 64, 1 << 30) and size(2, 3, 128, 0, 1000, 128) == 12 * one

@@ -792,8 +792,8 @@ def gdn_update_varlen(q, k, v, beta, alpha, cu_tokens, max_tokens, state, out=No
     [B, H, d, d] float32.  The state is updated in place, the outputs [n, H, d] are returned; rows of
     no sequence are left as they were.  ``max_tokens`` bounds every sequence's tokens; one
     beyond it is skipped and reported in ``dev_status`` (int32 [1], zeroed by the caller).
-    bf16 calls of more than 16 tokens a sequence use a ``workspace`` (uint8, gdn_workspace_size
-    bytes), allocated here when not given; calls that overlap on the GPU need one each."""
+    bf16 calls of long sequences use a ``workspace`` (uint8, gdn_workspace_size bytes, 0: none),
+    allocated here when not given; calls that overlap on the GPU need one each."""
     max_tokens = _c_int("max_tokens", max_tokens)
     here, B, n, H, d = _check_gdn(q, k, v, beta, alpha, cu_tokens, state)
     if out is None:

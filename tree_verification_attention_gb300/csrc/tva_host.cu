@@ -292,13 +292,15 @@ tva_status check_kv4_rows(int num_rows, int Hkv, int d, int dtype, long long kv_
 }
 
 // Tokens a sequence up to which bf16 calls of gdn_update_varlen run the recurrence, and beyond which
-// they run in chunks on the tensor cores.
-constexpr int kMaxRecurrent = 16;
+// they run in chunks on the tensor cores.  Measured, recurrence / chunks: d = 128, 32 heads, 1 sequence 24
+// tokens 12.7 / 12.7 us, 32 tokens 16.3 / 12.8; 16 sequences 51 / 61 and 67 / 61; 64 sequences 208 / 240 and
+// 280 / 243; d = 64, 16 heads, 8 sequences 32 tokens 10.7 / 13.3, 48 tokens 15.2 / 13.5.
+int max_recurrent(int d) { return d == 64 ? 40 : 24; }
 
 // Workspace of gdn_update_varlen; 0: the recurrence, which needs none.
 size_t gdn_workspace(int B, int H, int d, int dtype, int rows, int max_tokens) {
   const int longest = std::min(max_tokens, rows);
-  return dtype == TVA_BF16 && longest > kMaxRecurrent ? tva::gdn_chunk_workspace(B, H, d, longest) : 0;
+  return dtype == TVA_BF16 && longest > max_recurrent(d) ? tva::gdn_chunk_workspace(B, H, d, longest) : 0;
 }
 
 // The checks that gdn_update_varlen and commit_accepted_gdn share (`rows` token or node rows;
