@@ -37,6 +37,7 @@ def test_update_refusals(lib):
         return lib.gdn_update_varlen(B, H, d, dtype, cap, most, P(cu), P(q), P(k), P(v), P(beta), P(alpha), P(state),
                                      P(out), P(ws), n, P(st), None)
     assert call(B=0) == 1 and call(H=0) == 1 and call(cap=-1) == 1 and call(most=-1) == 1
+    assert call(cap=2 ** 31 - 1) == 1
     assert call(d=96) == 2 and call(dtype=2) == 2 and call(dtype=5) == 2
     for name in ("cu", "q", "k", "v", "beta", "alpha", "state", "out", "st"):
         assert call(**{name: None}) == 1, name

@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(St<D, NS>::kThreads, 1)
     uint64_t S2[8];   // this row's 16 columns, in pairs
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float4 v = r128 < D ? *reinterpret_cast<const float4*>(Sg + 4 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 v = r128 < D ? __ldcg(reinterpret_cast<const float4*>(Sg + 4 * q)) : make_float4(0.f, 0.f, 0.f, 0.f);
       S2[2 * q] = f2_pack(v.x, v.y);
       S2[2 * q + 1] = f2_pack(v.z, v.w);
     }

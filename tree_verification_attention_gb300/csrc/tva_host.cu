@@ -309,7 +309,8 @@ size_t gdn_workspace(int B, int H, int d, int dtype, int rows, int max_tokens) {
 tva_status check_gdn_update(int B, int H, int d, int dtype, int rows, const int32_t* cu, const void* q, const void* k,
                             const void* v, const float* beta, const float* alpha, const float* state, const void* out,
                             const int32_t* dev_status) {
-  if (B < 1 || H < 1 || rows < 0 || (long long)B * H > (1LL << 24) || !cu || !state || !dev_status)
+  if (B < 1 || H < 1 || rows < 0 || rows > INT32_MAX - 128 || (long long)B * H > (1LL << 24) || !cu || !state ||
+      !dev_status)
     return TVA_ERR_INVALID_ARG;
   if (rows > 0 && (!k || !v || !beta || !alpha)) return TVA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return TVA_ERR_UNSUPPORTED;
