@@ -21,7 +21,7 @@
 // sequences of 32 heads, d = 128, 272 MB: one token 41.9 us, 6.5 TB/s, without the hints 45.9; the commit of
 // 64 paths of 0 to 8 nodes 46.3 and 52.1 us, and 57.6 without a bound on the registers that lets eight
 // blocks share a SM).  Many tokens are bound by the chain from token to token (products, three shuffles,
-// update): some 330 clocks each (777 tokens of single precision 133 us).  Tried and not kept: sixteen row
+// update): some 310 clocks each (777 tokens of single precision 125 us).  Tried and not kept: sixteen row
 // groups (half the work a warp: no shorter), the state scaled lazily by the product of the decays (one
 // multiply-add an element instead of two, but a division a token: no shorter), the outputs' sums behind the
 // update.
@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(kThreadsUp, kPath ? 8 : 6) gdn_recurrent_kerne
     const bool more = j0 + kTile < n;   // uniform over the block
     if (more) fetch(j0 + kTile);
     const int cnt = min(kTile, n - j0);
-#pragma unroll 1
+    constexpr int kUnroll = kOut ? 4 : 1;   // single precision prompts 133 -> 125 us; a path's few nodes lose by it
+#pragma unroll kUnroll
     for (int j = 0; j < cnt; ++j) {
       uint64_t k2[2 * NI];
       uint64_t x2[4], y2[4], z2 = 0;   // S^T k, S^T q, q.k (0 bits: a pair of zeros)
