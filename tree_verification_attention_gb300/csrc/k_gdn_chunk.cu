@@ -12,7 +12,7 @@
 //     P = lower(G o Q K^T) T diag(beta)  [C x C]      O  = g o (Q S) + P r
 //
 // Two kernels.  The first makes W and P of every (sequence, head, chunk), all at once, one CTA of
-// four warps each (four resident per SM), and leaves them in the workspace as the second's shared
+// eight warps each (four resident per SM), and leaves them in the workspace as the second's shared
 // memory will hold them (48 KB at d = 128).  The second walks a sequence's chunks, one CTA per (sequence,
 // head, 64 columns of d_v): a producer warp fetches K, Q, W and P a chunk ahead, eight warps hold the
 // state in registers (fp32; thread = row of d_k = TMEM lane, 32 columns) and run
@@ -91,7 +91,7 @@ __device__ __forceinline__ bool sequence_ok(const GdnUpdateArgs& a, int t0, int 
 
 // ------------------------------------------------------------------ W and P of one chunk
 
-constexpr int kThreadsPr = 128;
+constexpr int kThreadsPr = 256;   // TMEM lane t % 128, columns (of 64) 32 (t / 128) ..
 constexpr uint32_t kTmWork = 64;   // TMEM: [K; Q] K^T, then G o (Q K^T) hi and lo, at 0; then W, then P
 
 template <int D>
@@ -103,8 +103,8 @@ struct Pr {
   // over T's terms for W, P over T's terms for P
   static constexpr int kTHi = kSpan, kTLo = D == 128 ? 3 * kSpan : kAOff + kChunk * kLd * 4;
   static constexpr int kXOff = kAOff + kChunk * kLd * 4 + (D == 128 ? 0 : kSpan);
-  static constexpr int kGateOff = kXOff + 32 * kLdX * 4;   // alpha, beta, G_Ci
-  static constexpr int kBarOff = kGateOff + 3 * kChunk * 4;
+  static constexpr int kGateOff = kXOff + 32 * kLdX * 4;   // alpha, beta, G_Ci, products from token 33 on
+  static constexpr int kBarOff = kGateOff + 4 * kChunk * 4;
   static constexpr int kSmem = kBarOff + 64 + 1024;
   static_assert(kChunk * kLd * 4 % 1024 == 0 && kChunk * kLd * 4 >= 2 * kSpan, "T's terms over A");
 };
@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
   float* al_s = reinterpret_cast<float*>(smem + C::kGateOff);   // alpha
   float* be_s = al_s + kChunk;                                  // beta
   float* en_s = be_s + kChunk;                                  // G_Ci
+  float* mid_s = en_s + kChunk;                                 // product of alpha over tokens 33 .. i
   // gates (rows past the sequence's end: no decay, nothing written)
   float al = 1.f, be = 0.f;
   if (t < cnt) {
@@ -214,7 +215,8 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t lane_base = (uint32_t)(w * 32) << 16;
+  const int half = t >> 7;
+  const uint32_t lane_base = (uint32_t)((w & 3) * 32) << 16;
   constexpr uint32_t idesc_a = idesc_bf16(128, 64, false);                 // [K; Q] K^T: both K-major
   constexpr uint32_t idesc_w = idesc_bf16(128, 64, true) | (1u << 15);     // K^T T: A along M, B along N
   constexpr uint32_t idesc_p = idesc_bf16(128, 64, true);                  // A in TMEM
@@ -222,13 +224,15 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
   // products of the decays from the chunk's start and to its end: 64 threads, a scan each way
   float pre = al;
   if (t < 64) {
-    float suf = t < 63 ? al_s[t + 1] : 1.f;
+    float suf = t < 63 ? al_s[t + 1] : 1.f, mid = lane == 0 ? 1.f : al;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const float x = __shfl_up_sync(0xffffffffu, pre, o), y = __shfl_down_sync(0xffffffffu, suf, o);
-      if (lane >= o) pre *= x;
+      const float z = __shfl_up_sync(0xffffffffu, mid, o);
+      if (lane >= o) { pre *= x; mid *= z; }
       if (lane + o < 32) suf *= y;
     }
+    mid_s[t] = t < 32 ? 1.f : mid;
     // across the two warps: the other one's 32 factors, multiplied by every lane's share
     float other = t < 32 ? al_s[32 + lane] : al_s[lane];
     if (t < 32 && lane == 0) other = 1.f;   // al_s[32] is already in warp 0's suffixes
@@ -258,64 +262,53 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
     }
     tc_commit_elect(P_DONE);
   }
-  const int row = t & 63;   // this lane's token row (of K for t < 64, of Q above)
+  const int row = t & 63;   // this lane's token row (of K for lanes below 64, of Q above)
+  const bool qrow = (t & 64) != 0;
   if (ok) ok = mbar_wait(P_DONE, 0, abort_flag, wait_ns);
   tc_fence_after();
   {
-    // row `row` of beta_i G_ij k_i.k_j (j < i), or of G_ij q_i.k_j (j <= i); warps of the rows below 32
-    // have none of the columns from 32 on
-    uint32_t d[64];
-    tmem_ld32(tmem + lane_base, d);
-    tmem_ld32(tmem + lane_base + 32, d + 32);
+    // this thread's half of row `row` of beta_i G_ij k_i.k_j (j < i), or of G_ij q_i.k_j (j <= i)
+    uint32_t d[32];
+    tmem_ld32(tmem + lane_base + 32 * half, d);
+    const int j0 = 32 * half, last = qrow ? row : row - 1;
+    // G_row,31 but for alpha of token 32, which the walk below multiplies in, where the walk starts there
+    float p = (qrow ? 1.f : be_s[row]) * (half == 0 ? mid_s[row] : 1.f);
     tmem_wait_ld32(d);
-    tie32(d + 32);
-    const bool qrow = t >= 64;
-    float p = qrow ? 1.f : be;
-    const int last = qrow ? row : row - 1;
-    auto decay = [&](int j0) {   // columns j0 + 31 .. j0
 #pragma unroll
-      for (int j4 = 28; j4 >= 0; j4 -= 4) {
-        const float4 a4 = *reinterpret_cast<const float4*>(al_s + j0 + j4);
-        const float next = j0 + j4 < 60 ? al_s[j0 + j4 + 4] : 1.f;
-        const float f[4] = {a4.y, a4.z, a4.w, next};   // alpha of token j + 1
+    for (int j4 = 28; j4 >= 0; j4 -= 4) {
+      const float4 a4 = *reinterpret_cast<const float4*>(al_s + j0 + j4);
+      const float next = al_s[min(j0 + j4 + 4, kChunk - 1)];
+      const float f[4] = {a4.y, a4.z, a4.w, next};   // alpha of token j + 1 (never used past token 63)
 #pragma unroll
-        for (int e = 3; e >= 0; --e) {
-          const int j = j0 + j4 + e;
-          if (j < row) p *= f[e];
-          d[j] = j <= last ? __float_as_uint(__uint_as_float(d[j]) * p) : 0u;
-        }
+      for (int e = 3; e >= 0; --e) {
+        const int j = j0 + j4 + e;
+        if (j < row) p *= f[e];
+        d[j4 + e] = j <= last ? __float_as_uint(__uint_as_float(d[j4 + e]) * p) : 0u;
       }
-    };
-    if (w & 1) {
-      decay(32);
-    } else {
-#pragma unroll
-      for (int j = 32; j < 64; ++j) d[j] = 0u;
     }
-    decay(0);
+    uint32_t lo[16];
     if (!qrow) {
 #pragma unroll
-      for (int j = 0; j < 64; j += 4)
-        *reinterpret_cast<uint4*>(As + row * kLd + j) = make_uint4(d[j], d[j + 1], d[j + 2], d[j + 3]);
+      for (int j = 0; j < 32; j += 4)
+        *reinterpret_cast<uint4*>(As + row * kLd + j0 + j) = make_uint4(d[j], d[j + 1], d[j + 2], d[j + 3]);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) d[j] = 0u;
-      tmem_st32(tmem + lane_base, d);
-      tmem_st32(tmem + lane_base + 32, d);
+      for (int j = 0; j < 16; ++j) d[j] = lo[j] = 0u;
     } else {
-      uint32_t lo[32];
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
+      for (int j = 0; j < 16; ++j)
         split2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]), d[j], lo[j]);
-      tmem_st32(tmem + lane_base, d);   // lower(G o Q K^T) in lanes 64 .. 127, zeros above
-      tmem_st32(tmem + lane_base + 32, lo);
     }
+    tc_fence_before();
+    __syncthreads();   // every column is read
+    tc_fence_after();
+    tmem_st16(tmem + lane_base + 16 * half, d);   // lower(G o Q K^T) in lanes 64 .. 127, zeros above: hi
+    tmem_st16(tmem + lane_base + 32 + 16 * half, lo);
     tmem_wait_st();
     tc_fence_before();
   }
-  __syncthreads();
   // ---- T = (I + A)^-1: 16-row diagonal blocks by substitution (a column per lane), then the
   // blocks below them, T21 = -T22 (A21 T11), at 16 and at 32 rows
-  {
+  if (w < 4) {
     const int o = 16 * w, cc = lane & 15;
     float x[16];
 #pragma unroll
@@ -340,58 +333,56 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
   __syncthreads();
   const int gq = lane >> 2, tq = 2 * (lane & 3);   // this lane's first row and columns of a 16 x 8 product
   {
-    const int o = 32 * (w >> 1), n0 = 8 * (w & 1);   // two blocks of 32 rows; columns of their 16
-    float* X = Xs + (w >> 1) * 16 * kLdX + gq * kLdX + n0 + tq;
+    const int o = 32 * ((w >> 1) & 1), n0 = 8 * (w & 1);   // two blocks of 32 rows; columns of their 16
+    float* Xb = Xs + ((w >> 1) & 1) * 16 * kLdX + n0;
     float d[4] = {0.f, 0.f, 0.f, 0.f};
-    block_product(As + (o + 16) * kLd + o, kLd, As + o * kLd + o + n0, kLd, 0, 16, lane, d);   // A21 T11
-    *reinterpret_cast<float2*>(X) = make_float2(d[0], d[1]);
-    *reinterpret_cast<float2*>(X + 8 * kLdX) = make_float2(d[2], d[3]);
-    __syncthreads();
-    d[0] = d[1] = d[2] = d[3] = 0.f;
-    block_product(As + (o + 16) * kLd + o + 16, kLd, Xs + (w >> 1) * 16 * kLdX + n0, kLdX, 0, 16, lane, d);
-    float* T21 = As + (o + 16 + gq) * kLd + o + n0 + tq;
-    *reinterpret_cast<float2*>(T21) = make_float2(-d[0], -d[1]);
-    *reinterpret_cast<float2*>(T21 + 8 * kLd) = make_float2(-d[2], -d[3]);
-  }
-  __syncthreads();
-  {
-    // 32 x 32 x 32: warp w takes 16 rows and 16 columns; T11 has nothing above, T22 nothing right of, its
-    // diagonal
-    const int m0 = 16 * (w & 1), n0 = 16 * (w >> 1);
-#pragma unroll
-    for (int nt = 0; nt < 16; nt += 8) {   // A21 T11
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      block_product(As + (32 + m0) * kLd, kLd, As + n0 + nt, kLd, n0, 32, lane, d);
-      float* X = Xs + (m0 + gq) * kLdX + n0 + nt + tq;
-      *reinterpret_cast<float2*>(X) = make_float2(d[0], d[1]);
-      *reinterpret_cast<float2*>(X + 8 * kLdX) = make_float2(d[2], d[3]);
+    if (w < 4) {
+      block_product(As + (o + 16) * kLd + o, kLd, As + o * kLd + o + n0, kLd, 0, 16, lane, d);   // A21 T11
+      *reinterpret_cast<float2*>(Xb + gq * kLdX + tq) = make_float2(d[0], d[1]);
+      *reinterpret_cast<float2*>(Xb + (gq + 8) * kLdX + tq) = make_float2(d[2], d[3]);
     }
     __syncthreads();
-#pragma unroll
-    for (int nt = 0; nt < 16; nt += 8) {   // -T22 (A21 T11)
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      block_product(As + (32 + m0) * kLd + 32, kLd, Xs + n0 + nt, kLdX, 0, m0 + 16, lane, d);
-      float* T21 = As + (32 + m0 + gq) * kLd + n0 + nt + tq;
+    if (w < 4) {
+      d[0] = d[1] = d[2] = d[3] = 0.f;
+      block_product(As + (o + 16) * kLd + o + 16, kLd, Xb, kLdX, 0, 16, lane, d);
+      float* T21 = As + (o + 16 + gq) * kLd + o + n0 + tq;
       *reinterpret_cast<float2*>(T21) = make_float2(-d[0], -d[1]);
       *reinterpret_cast<float2*>(T21 + 8 * kLd) = make_float2(-d[2], -d[3]);
     }
   }
   __syncthreads();
   {
+    // 32 x 32 x 32: warp w takes 16 rows and 8 columns; T11 has nothing above, T22 nothing right of, its
+    // diagonal
+    const int m0 = 16 * (w & 1), n0 = 8 * (w >> 1);
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    block_product(As + (32 + m0) * kLd, kLd, As + n0, kLd, n0, 32, lane, d);   // A21 T11
+    float* X = Xs + (m0 + gq) * kLdX + n0 + tq;
+    *reinterpret_cast<float2*>(X) = make_float2(d[0], d[1]);
+    *reinterpret_cast<float2*>(X + 8 * kLdX) = make_float2(d[2], d[3]);
+    __syncthreads();
+    d[0] = d[1] = d[2] = d[3] = 0.f;
+    block_product(As + (32 + m0) * kLd + 32, kLd, Xs + n0, kLdX, 0, m0 + 16, lane, d);   // -T22 (A21 T11)
+    float* T21 = As + (32 + m0 + gq) * kLd + n0 + tq;
+    *reinterpret_cast<float2*>(T21) = make_float2(-d[0], -d[1]);
+    *reinterpret_cast<float2*>(T21 + 8 * kLd) = make_float2(-d[2], -d[3]);
+  }
+  __syncthreads();
+  {
     // T diag(beta) (for P) and diag(G_Ci) T diag(beta) (for W, over A's place), two terms each:
     // row i is the products' k = i, its columns lie along N
-    const int i = t & 63, j0 = 32 * (t >> 6);
+    const int i = t & 63, j0 = 16 * (t >> 6);
     const float en = en_s[i];
-    float x[32];
+    float x[16];
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
+    for (int j = 0; j < 16; j += 4) {
       const float4 v = *reinterpret_cast<const float4*>(As + i * kLd + j0 + j);
       const float4 bb = *reinterpret_cast<const float4*>(be_s + j0 + j);
       x[j] = v.x * bb.x; x[j + 1] = v.y * bb.y; x[j + 2] = v.z * bb.z; x[j + 3] = v.w * bb.w;
     }
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 2; ++q) {
       uint32_t hi[4], lo[4];
       const int at = i * 128 + (((j0 >> 3) + q) ^ (i & 7)) * 16;
 #pragma unroll
@@ -421,11 +412,9 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
   }
   if (ok) ok = mbar_wait(P_DONE, 1, abort_flag, wait_ns);
   tc_fence_after();
-  uint32_t d[64];
-  tmem_ld32(tmem + kTmWork + lane_base, d);
-  tmem_ld32(tmem + kTmWork + lane_base + 32, d + 32);
+  uint32_t d[32];
+  tmem_ld32(tmem + kTmWork + lane_base + 32 * half, d);
   tmem_wait_ld32(d);
-  tie32(d + 32);
   tc_fence_before();
   ok = all_threads(ok);
   if (ok && w == 0) {   // P while W is written out
@@ -439,28 +428,27 @@ __global__ void __launch_bounds__(kThreadsPr, 4)
                      desc_join(plo + (((part == 1 ? C::kTLo : C::kTHi) + ks * 2048) >> 4), desc_hi), idesc_p, part > 0 || ks > 0);
     tc_commit_elect(P_DONE);
   }
-  // a row of 64 tokens in two terms
+  // this thread's 32 tokens of a row in two terms
   auto write_row = [&](uint8_t* hi_row, uint8_t* lo_row, int r) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < 4; ++q) {
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         split2(__uint_as_float(d[8 * q + 2 * e]), __uint_as_float(d[8 * q + 2 * e + 1]), hi[e], lo[e]);
-      const int at = (q ^ (r & 7)) * 16;
+      const int at = ((4 * half + q) ^ (r & 7)) * 16;
       *reinterpret_cast<uint4*>(hi_row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       *reinterpret_cast<uint4*>(lo_row + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   };
-  if (t < D) write_row(smem + (t < 64 ? 0 : 2 * kSpan) + (t & 63) * 128, smem + C::kAOff + t * 128, t);
+  const int r128 = t & 127;
+  if (r128 < D) write_row(smem + (r128 < 64 ? 0 : 2 * kSpan) + row * 128, smem + C::kAOff + r128 * 128, r128);
   if (t < kChunk) al_s[t] = pre;
   if (ok) ok = mbar_wait(P_DONE, 0, abort_flag, wait_ns);
   tc_fence_after();
-  if (t >= kChunk) {   // P is in lanes 64 .. 127
-    tmem_ld32(tmem + kTmWork + lane_base, d);
-    tmem_ld32(tmem + kTmWork + lane_base + 32, d + 32);
+  if (qrow) {   // P is in lanes 64 .. 127
+    tmem_ld32(tmem + kTmWork + lane_base + 32 * half, d);
     tmem_wait_ld32(d);
-    tie32(d + 32);
     write_row(smem + C::kTHi + row * 128, smem + C::kTLo + row * 128, row);
   }
   fence_async_shared();

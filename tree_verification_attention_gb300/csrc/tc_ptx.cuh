@@ -440,6 +440,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       TVA_W16(0), TVA_W16(16)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      TVA_W16(0)
+      : "memory");
+}
 // Waits for this thread's outstanding TMEM loads; the 32 registers are tied to the
 // wait so no use of them can be scheduled before it.
 __device__ __forceinline__ void tmem_wait_ld32(uint32_t* r) {
