@@ -754,6 +754,7 @@ def cross_attn_varlen(q, k_cache, v_cache, cu_queries, cu_keys, max_queries, max
 
 
 _GDN_DTYPES = (torch.float32, torch.bfloat16)
+_GDN_SHORT = 24  # tokens a sequence up to which no call of gdn_update_varlen needs a workspace
 
 
 def _check_gdn(q, k, v, beta, alpha, cu, state):
@@ -803,8 +804,9 @@ def gdn_update_varlen(q, k, v, beta, alpha, cu_tokens, max_tokens, state, out=No
     dev_status = _status_word(dev_status, q.device)
     lib = load_library()
     if workspace is None:
-        need = lib.tva_gdn_workspace_size(B, H, d, DTYPES[k.dtype], n, max_tokens)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        if max_tokens > _GDN_SHORT:
+            need = lib.tva_gdn_workspace_size(B, H, d, DTYPES[k.dtype], n, max_tokens)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     elif workspace.get_device() != here or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous uint8, on the tensors' device")
     code = lib.gdn_update_varlen(

@@ -10,6 +10,8 @@
 // logits); the natural-log LSE is produced here.  The maximum is subtracted before
 // exponentiating (the stable form of the same expression).
 //
+// A cross-attention query whose sequence has no keys has no partials: its output is 0, its log-sum-exp -inf.
+//
 // A warp takes one 32-row block of one row group and CG of its column groups (4
 // columns each); lane t owns row t of the block.  The kernel is bound by load latency,
 // so a warp issues the loads of up to NB partials at once; CG and NB are picked per

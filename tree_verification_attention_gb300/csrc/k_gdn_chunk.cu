@@ -14,14 +14,24 @@
 // Two kernels.  The first makes W and P of every (sequence, head, chunk), all at once, one CTA of
 // eight warps each (four resident per SM), and leaves them in the workspace as the second's shared
 // memory will hold them (48 KB at d = 128).  The second walks a sequence's chunks, one CTA per (sequence,
-// head, 64 columns of d_v): a producer warp fetches K, Q, W and P a chunk ahead, eight warps hold the
-// state in registers (fp32; thread = row of d_k = TMEM lane, 32 columns) and run
+// head, 64 or 32 columns of d_v): a producer warp fetches K, Q, W and P a chunk ahead, a warp issues the
+// products, and the others hold the state in registers (fp32; thread = row of d_k = TMEM lane, 16 columns):
 //     X = [K; Q] S (one M = 128 product: lanes 0-63 are K rows, 64-127 Q rows) -> r -> W r, P r.
 // Long prompts go in segments of chunks, a pair of launches each, so that the workspace stays bounded; a
 // segment is prepared beside the walk through the one before it.
-// One kernel that made W and P beside the walk, each CTA for its own columns, took 2.94 ms
-// for 32768 tokens of 32 heads, d = 128: four times the preparation, and 108 KB of code that ran at the
-// rate of its instruction fetches.
+//
+// What bounds it, measured at 32 heads, d = 128 (GB300, CUDA events): 4096 tokens 138 us, 32768 tokens 969 us
+// (1.12 TB/s and 106 TFLOP/s of the recurrence's own products; floor 160 us, its bytes).  The walk is a chain of
+// some 2350 clocks a chunk: X 640 (eight MMAs of 39 clocks, then their latency, commit and wake-up), r 370, W r
+// 580, the state's update and split 340, two hand-overs of 170 and 120; no unit is busy (tensor 24 %, issue 23 %).
+// The preparation of 2048 (head, chunk) pairs takes 47 us, 49 % of the issue slots, 44 % of the shared-memory
+// pipe: some 11500 warp instructions each, half of them splits and layouts.
+// Steps (4096 / 32768 tokens): one kernel that made W and P beside the walk, each CTA for its own columns,
+// 374 / 2942 us (four times the preparation, and 108 KB of code that ran at the rate of its instruction
+// fetches); two kernels 254 / 1922; the products issued by a warp of their own, no barrier among the state's
+// holders 190 / 1402; images out by bulk copies, T read without bank conflicts 181 / 1330; 16 columns a thread, 32
+// a CTA where each has an SM 148 / 1080; the inverse's blocks on mma.sync 141 / 1042; a segment prepared
+// beside the walk before it 140 / 987; eight warps a preparing CTA 138 / 969.
 //
 // Precision: K, Q and V are bf16 inputs and exact.  S, T, W, G o (Q K^T), P and r are fp32 values held
 // as two bf16 terms each, so that products have operands of 16 bits or more (a term is off by 2^-17;
@@ -30,9 +40,9 @@
 // 5e-3 with keys that repeat: there W r and P r are small sums of large terms.  Sums, decays, T and
 // the state are fp32.
 //
-// Every wait is bounded (as in the attention kernels): when one expires the abort flag is raised, the
-// warps leave their loops together at their next barrier, everything in flight is drained (again
-// bounded), TMEM is freed and TVA_ERR_TIMEOUT recorded; the state is then not written.
+// Every wait is bounded (as in the attention kernels): when one expires the abort flag is raised, every
+// warp leaves its loop at its next wait, everything in flight is drained (again bounded), TMEM is
+// freed and TVA_ERR_TIMEOUT recorded; the state is then not written.
 #include <cuda.h>
 #include <cuda_bf16.h>
 

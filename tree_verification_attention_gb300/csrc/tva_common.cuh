@@ -24,6 +24,8 @@
 // that walk the same (KV head, key tile) columns side by side, so the K/V tiles come
 // from DRAM once; a member's partials go to slots r (Q + Hkv) + k + g.
 //
+// Cross-attention (CrossProblem) has no tree tile: tile t holds prefix keys [128 t, 128 (t + 1)).
+//
 // Both the partials kernels and the combine kernel recompute this map from
 // cu_prefix / cu_nodes, so no schedule table is stored.
 #pragma once
