@@ -423,7 +423,9 @@ tva_status gdn_tree_verify(int batch, int num_heads, int head_dim, tva_dtype dty
  * token_capacity rows may be null when it is 0.  fp32 calls, and bf16 calls of at most 24 tokens a
  * sequence (40 at d = 64), run the recurrence in fp32.  Longer bf16 calls run in chunks of 64 tokens on the tensor
  * cores: fp32 sums of products whose operands are held to 16 bits or more (relative error of the
- * state some 5e-6).  bf16 outputs are rounded once.  tva_diag_set_wait_limit applies to the chunked
+ * state 4e-6 to 6e-6).  bf16 outputs are rounded once.  There a token with a value that is not finite can
+ * spoil its sequence's outputs from the start of its chunk on, in the recurrence from the token on; other
+ * sequences are not affected.  tva_diag_set_wait_limit applies to the chunked
  * form.  A sequence outside the bounds is skipped (state and output untouched) with
  * TVA_ERR_INVALID_ARG in *dev_status. */
 tva_status gdn_update_varlen(int batch, int num_heads, int head_dim, tva_dtype dtype, int token_capacity,

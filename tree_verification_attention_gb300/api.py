@@ -793,6 +793,9 @@ def gdn_update_varlen(q, k, v, beta, alpha, cu_tokens, max_tokens, state, out=No
     [B, H, d, d] float32.  The state is updated in place, the outputs [n, H, d] are returned; rows of
     no sequence are left as they were.  ``max_tokens`` bounds every sequence's tokens; one
     beyond it is skipped and reported in ``dev_status`` (int32 [1], zeroed by the caller).
+    A token with a value that is not finite spoils its own sequence alone (in bf16 calls of long
+    sequences from the start of its 64 tokens on).
+
     bf16 calls of long sequences use a ``workspace`` (uint8, gdn_workspace_size bytes, 0: none),
     allocated here when not given; calls that overlap on the GPU need one each."""
     max_tokens = _c_int("max_tokens", max_tokens)
