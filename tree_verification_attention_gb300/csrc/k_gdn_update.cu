@@ -9,9 +9,9 @@
 // o_t = alpha_t S_{t-1}^T q_t + (q_t . k_t) w, so both products read the state before the step
 // and their sums over the key rows are taken together.  Columns of S (of d_v) never meet.
 //
-// A block of two warps takes 32 columns of one head's state.  A warp's 16 columns x D rows stay in
-// its registers from the first token to the last: lane = 4 rg + c4 holds columns 4 c4 .. 4 c4 + 3 of
-// the rows 32 i + 4 rg + e (e < 4), packed in pairs of rows (e, e + 1), so that a 16-byte read of k or q
+// A block of two warps takes 32 columns of one head's state (16 with sixteen row groups).  A warp's 16
+// columns x D rows stay in its registers from the first token to the last: lane = 4 rg + c4 holds columns
+// 4 c4 .. 4 c4 + 3 of the rows 32 i + 4 rg + e (e < 4), packed in pairs of rows (e, e + 1), so that a 16-byte read of k or q
 // from shared memory is two such pairs and the products and the update run on packed fp32 pairs.
 // The eight row groups are summed by a butterfly of shuffles.  Tokens are staged kTile at a time; the
 // next tile's rows are on their way from memory while the current one is computed.  All
@@ -21,8 +21,8 @@
 // sequences of 32 heads, d = 128, 272 MB: one token 41.9 us, 6.5 TB/s, without the hints 45.9; the commit of
 // 64 paths of 0 to 8 nodes 46.3 and 52.1 us, and 57.6 without a bound on the registers that lets eight
 // blocks share a SM).  Many tokens are bound by the chain from token to token (products, three shuffles,
-// update): some 310 clocks each (777 tokens of single precision 125 us).  Tried and not kept: sixteen row
-// groups (half the work a warp: no shorter), the state scaled lazily by the product of the decays (one
+// update) and the products' rate, 272 clocks of 310 on the one scheduler that a warp has (777 tokens of single
+// precision 125 us, with sixteen row groups 104).  Tried and not kept: the state scaled lazily by the product of the decays (one
 // multiply-add an element instead of two, but a division a token: no shorter), the outputs' sums behind the
 // update.
 #include <cuda_bf16.h>
@@ -38,7 +38,6 @@ namespace {
 using namespace ptx;
 
 constexpr int kThreadsUp = 64;
-constexpr int kColsUp = 32;  // columns of d_v per block, 16 per warp
 constexpr int kTile = 8;     // tokens staged together
 
 __device__ __forceinline__ float4 up_load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
@@ -51,11 +50,13 @@ __device__ __forceinline__ void up_store4(__nv_bfloat16* p, float4 v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-// kPath: the tokens are the nodes of an accepted path and there is no output.
-template <int D, typename T, bool kPath>
+// kPath: the tokens are the nodes of an accepted path and there is no output.  RG: row groups, 8 or 16.
+template <int D, typename T, bool kPath, int RG>
 __global__ void __launch_bounds__(kThreadsUp, kPath ? 8 : 6) gdn_recurrent_kernel(GdnUpdateArgs a) {
-  constexpr int CS = D / kColsUp;   // blocks per (sequence, head)
-  constexpr int NI = D / 32;        // row quadruples per lane
+  constexpr int C4 = 32 / RG;          // lanes side by side
+  constexpr int kColsUp = 8 * C4;      // columns of d_v per block, half of them per warp
+  constexpr int CS = D / kColsUp;      // blocks per (sequence, head)
+  constexpr int NI = D / (4 * RG);     // row quadruples per lane
   constexpr bool kOut = !kPath;
   __shared__ __align__(16) float sk[2][kTile][D];
   __shared__ __align__(16) float sq[2][kOut ? kTile : 1][D];
@@ -68,9 +69,9 @@ __global__ void __launch_bounds__(kThreadsUp, kPath ? 8 : 6) gdn_recurrent_kerne
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cs = blockIdx.x % CS, bh = blockIdx.x / CS;
   const int b = bh / a.H, h = bh % a.H;
-  const int rg = lane >> 2, c4 = lane & 3;
+  const int rg = lane / C4, c4 = lane % C4;
   const int c0 = cs * kColsUp;                    // this block's first column
-  const int col = c0 + 16 * warp + 4 * c4;        // this lane's
+  const int col = c0 + 4 * (C4 * warp + c4);      // this lane's
   float* S = a.state + ((size_t)b * a.H + h) * D * D + col;
 
   // which rows: checked before anything is written
@@ -99,12 +100,14 @@ __global__ void __launch_bounds__(kThreadsUp, kPath ? 8 : 6) gdn_recurrent_kerne
   for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      s4[i][e] = __ldcs(reinterpret_cast<const float4*>(S + (size_t)(32 * i + 4 * rg + e) * D));
+      s4[i][e] = __ldcs(reinterpret_cast<const float4*>(S + (size_t)(4 * (RG * i + rg) + e) * D));
 
   const size_t hs = (size_t)a.H * D;
   constexpr int kVecs = kTile * (D / 4) / kThreadsUp;   // 16-byte pieces of k (of q) per thread and tile
   float4 pk[kVecs], pq[kOut ? kVecs : 1], pv;
   float pa = 1.f, pb = 0.f;
+  constexpr int kVPieces = kTile * (kColsUp / 4);   // of v per tile, at most one a thread
+  static_assert(kVPieces <= kThreadsUp, "v");
   auto row_of = [&](int j) -> size_t { return (size_t)t0 + (kPath ? s_path[j] : j); };
   auto fetch = [&](int j0) {
 #pragma unroll
@@ -117,7 +120,8 @@ __global__ void __launch_bounds__(kThreadsUp, kPath ? 8 : 6) gdn_recurrent_kerne
       }
     }
     const int j = j0 + tid / (kColsUp / 4);
-    if (j < n) pv = up_load4(static_cast<const T*>(a.v) + row_of(j) * hs + (size_t)h * D + c0 + 4 * (tid % (kColsUp / 4)));
+    if (tid < kVPieces && j < n)
+      pv = up_load4(static_cast<const T*>(a.v) + row_of(j) * hs + (size_t)h * D + c0 + 4 * (tid % (kColsUp / 4)));
     if (tid < kTile && j0 + tid < n) {
       pa = __ldg(a.alpha + row_of(j0 + tid) * a.H + h);
       pb = __ldg(a.beta + row_of(j0 + tid) * a.H + h);
@@ -130,10 +134,9 @@ __global__ void __launch_bounds__(kThreadsUp, kPath ? 8 : 6) gdn_recurrent_kerne
       *reinterpret_cast<float4*>(&sk[buf][e / (D / 4)][4 * (e % (D / 4))]) = pk[x];
       if constexpr (kOut) *reinterpret_cast<float4*>(&sq[buf][e / (D / 4)][4 * (e % (D / 4))]) = pq[x];
     }
-    *reinterpret_cast<float4*>(&sv[buf][tid / (kColsUp / 4)][4 * (tid % (kColsUp / 4))]) = pv;
+    if (tid < kVPieces) *reinterpret_cast<float4*>(&sv[buf][tid / (kColsUp / 4)][4 * (tid % (kColsUp / 4))]) = pv;
     if (tid < kTile) { s_alpha[buf][tid] = pa; s_beta[buf][tid] = pb; }
   };
-  static_assert(kTile * (kColsUp / 4) == kThreadsUp, "one piece of v per thread");
   fetch(0);
   stage(0);
   __syncthreads();
@@ -162,7 +165,7 @@ __global__ void __launch_bounds__(kThreadsUp, kPath ? 8 : 6) gdn_recurrent_kerne
       for (int c = 0; c < 4; ++c) x2[c] = y2[c] = 0;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const ulonglong2 kv = *reinterpret_cast<const ulonglong2*>(&sk[buf][j][32 * i + 4 * rg]);
+        const ulonglong2 kv = *reinterpret_cast<const ulonglong2*>(&sk[buf][j][4 * (RG * i + rg)]);
         k2[2 * i] = kv.x;
         k2[2 * i + 1] = kv.y;
 #pragma unroll
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kThreadsUp, kPath ? 8 : 6) gdn_recurrent_kerne
           x2[c] = f2_fma(s2[2 * i + 1][c], kv.y, x2[c]);
         }
         if constexpr (kOut) {
-          const ulonglong2 qv = *reinterpret_cast<const ulonglong2*>(&sq[buf][j][32 * i + 4 * rg]);
+          const ulonglong2 qv = *reinterpret_cast<const ulonglong2*>(&sq[buf][j][4 * (RG * i + rg)]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             y2[c] = f2_fma(s2[2 * i][c], qv.x, y2[c]);
@@ -198,7 +201,7 @@ __global__ void __launch_bounds__(kThreadsUp, kPath ? 8 : 6) gdn_recurrent_kerne
         z = lo + hi;
       }
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
+      for (int o = C4; o < 32; o <<= 1) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) x[c] += __shfl_xor_sync(0xffffffffu, x[c], o);
         if constexpr (kOut) {
@@ -208,7 +211,7 @@ __global__ void __launch_bounds__(kThreadsUp, kPath ? 8 : 6) gdn_recurrent_kerne
         }
       }
       const float al = s_alpha[buf][j], be = s_beta[buf][j];
-      const float4 vv = *reinterpret_cast<const float4*>(&sv[buf][j][16 * warp + 4 * c4]);
+      const float4 vv = *reinterpret_cast<const float4*>(&sv[buf][j][4 * (C4 * warp + c4)]);
       float w[4];
       w[0] = be * (vv.x - al * x[0]);
       w[1] = be * (vv.y - al * x[1]);
@@ -239,20 +242,31 @@ __global__ void __launch_bounds__(kThreadsUp, kPath ? 8 : 6) gdn_recurrent_kerne
       float lo[4], hi[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) f2_unpack(s2[2 * i + p][c], lo[c], hi[c]);
-      float* at = S + (size_t)(32 * i + 4 * rg + 2 * p) * D;
+      float* at = S + (size_t)(4 * (RG * i + rg) + 2 * p) * D;
       __stcs(reinterpret_cast<float4*>(at), make_float4(lo[0], lo[1], lo[2], lo[3]));
       __stcs(reinterpret_cast<float4*>(at + D), make_float4(hi[0], hi[1], hi[2], hi[3]));
     }
 }
 
+template <int D, typename T, bool kPath, int RG>
+cudaError_t launch_recurrent_rows(const GdnUpdateArgs& a, cudaStream_t s) {
+  return check_cuda(launch_pdl(gdn_recurrent_kernel<D, T, kPath, RG>, dim3((unsigned)((long long)a.B * a.H * (D * RG / 256))),
+                               dim3(kThreadsUp), 0, s, a),
+                    "launch gdn_recurrent_kernel");
+}
+
+// Sixteen row groups: twice the warps, each with half of a token's products and a fourth shuffle.  They pay when
+// there is a scheduler for every warp and more than a few tokens (fp32, 5 sequences of up to 777 tokens, 6
+// heads: 104 us against 125), not otherwise (one token of 1 sequence 2.7 against 2.4 us, of 64 57 against 42).
+constexpr int kSchedulers = 608;
+constexpr int kFewTokens = 8;
+
 template <int D, typename T>
 cudaError_t launch_recurrent_typed(const GdnUpdateArgs& a, cudaStream_t s) {
-  const dim3 grid((unsigned)((long long)a.B * a.H * (D / kColsUp)));
-  if (a.accept_len != nullptr)
-    return check_cuda(launch_pdl(gdn_recurrent_kernel<D, T, true>, grid, dim3(kThreadsUp), 0, s, a),
-                      "launch gdn_recurrent_kernel");
-  return check_cuda(launch_pdl(gdn_recurrent_kernel<D, T, false>, grid, dim3(kThreadsUp), 0, s, a),
-                    "launch gdn_recurrent_kernel");
+  if (a.accept_len != nullptr) return launch_recurrent_rows<D, T, true, 8>(a, s);
+  if (a.max_tokens > kFewTokens && (long long)a.B * a.H * (D / 8) <= kSchedulers)
+    return launch_recurrent_rows<D, T, false, 16>(a, s);
+  return launch_recurrent_rows<D, T, false, 8>(a, s);
 }
 
 }  // namespace
