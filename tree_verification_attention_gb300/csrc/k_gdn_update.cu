@@ -9,22 +9,23 @@
 // o_t = alpha_t S_{t-1}^T q_t + (q_t . k_t) w, so both products read the state before the step
 // and their sums over the key rows are taken together.  Columns of S (of d_v) never meet.
 //
-// A block of two warps takes 32 columns of one head's state (16 with sixteen row groups).  A warp's 16
-// columns x D rows stay in its registers from the first token to the last: lane = 4 rg + c4 holds columns
-// 4 c4 .. 4 c4 + 3 of the rows 32 i + 4 rg + e (e < 4), packed in pairs of rows (e, e + 1), so that a 16-byte read of k or q
-// from shared memory is two such pairs and the products and the update run on packed fp32 pairs.
-// The eight row groups are summed by a butterfly of shuffles.  Tokens are staged kTile at a time; the
-// next tile's rows are on their way from memory while the current one is computed.  All
-// arithmetic is fp32 (bf16 rows are widened as they are staged, the output rounded once).
+// A block of two warps takes 32 columns of one head's state (16 with sixteen row groups).  A warp's columns
+// x D rows stay in its registers from the first token to the last: lane = 4 rg + c4 holds columns 4 c4 ..
+// 4 c4 + 3 of the rows 32 i + 4 rg + e (e < 4), packed in pairs of rows (e, e + 1), so that a 16-byte read
+// of k or q from shared memory is two such pairs and the products and the update run on packed fp32
+// pairs.  The eight row groups are summed by a butterfly of shuffles.  (With sixteen: lane = 2 rg + c4, rows
+// 64 i + 4 rg + e.)  Tokens are staged kTile at a time; the next tile's rows are on their way from memory
+// while the current one is computed.  All arithmetic is fp32 (bf16 rows are widened as they are staged, the
+// output rounded once).
 //
 // Few tokens are bound by the state's traffic: it is read and written once, with streaming hints (64
 // sequences of 32 heads, d = 128, 272 MB: one token 41.9 us, 6.5 TB/s, without the hints 45.9; the commit of
 // 64 paths of 0 to 8 nodes 46.3 and 52.1 us, and 57.6 without a bound on the registers that lets eight
-// blocks share a SM).  Many tokens are bound by the chain from token to token (products, three shuffles,
-// update) and the products' rate, 272 clocks of 310 on the one scheduler that a warp has (777 tokens of single
-// precision 125 us, with sixteen row groups 104).  Tried and not kept: the state scaled lazily by the product of the decays (one
-// multiply-add an element instead of two, but a division a token: no shorter), the outputs' sums behind the
-// update.
+// blocks share a SM).  Many tokens are bound by the chain from token to token: the products and the update
+// (136 packed multiply-adds of two clocks each, on the one scheduler that a warp has), three shuffles, the
+// correction; some 310 clocks (777 tokens of single precision 125 us, with sixteen row groups 104).  Tried
+// and not kept: the state scaled lazily by the product of the decays (one multiply-add an element instead of
+// two, but a division a token: no shorter), the outputs' sums behind the update.
 #include <cuda_bf16.h>
 
 #include <type_traits>
