@@ -64,7 +64,7 @@ CASES = [
     ([300], [333], (6, 2), 64), ([257], [1000], (8, 8), 128), ([0, 5, 0, 300, 128], [3, 1, 2, 0, 40], (12, 4), 64),
     ([513, 0, 1], [9, 300, 1], (8, 2), 128), ([40] * 20, [1] * 20, (32, 8), 128), ([0] * 17 + [9], [2] * 18, (4, 4), 64),
     ([640, 641, 5], [40, 40, 40], (32, 2), 128), ([0, 0], [5, 1], (4, 1), 128), ([90], [2500], (4, 1), 64),
-    ([70, 71], [129, 500], (64, 2), 64),
+    ([70, 71], [129, 500], (64, 2), 64), ([700], [400], (32, 8), 128), ([500], [2001], (8, 2), 128), ([260], [640], (8, 2), 64),
 ]
 
 

@@ -835,7 +835,8 @@ cudaError_t launch_chunk_typed(const GdnUpdateArgs& a, void* workspace, cudaStre
   if (e != cudaSuccess) return e;
   const int all = (a.max_tokens + kChunk - 1) / kChunk, segment = segment_chunks(a.B, a.H, a.max_tokens);
   // A chunk takes a CTA of 32 columns less time than one of 64, but not half of it: 32 columns while
-  // every CTA then has an SM of its own.
+  // every CTA then has an SM of its own (32 heads, d = 128, 32 / 64 columns: 1 prompt of 2048 tokens 75 / 93 us, 2 of
+  // 1024 78 / 63, 8 266 / 234; d = 64, 1 of 2048 61 / 79, 3 of 1024 79 / 64).
   const bool narrow = (long long)a.B * a.H * (D / 32) <= kSms;
   ChunkArgs ca{a, nullptr, 0, 0, segment, 0, 0};
   tc_wait_settings(&ca.wait_ns, &ca.stall);

@@ -37,8 +37,8 @@
 // partials; the rest is their epilogues and the combine).
 // Cross-attention (CrossProblem) is the same without a tree tile: 16 fp16 queries over 32768 keys 30 us with the
 // combine (134 MB at 3.9 TB/s in the partials; then two launches' latency), one query of each of 8 sequences
-// of 4k to 32k keys 86 us (468 MB at 5.4 TB/s), 2001 queries over 8190 keys 236 us (partials 198 us, 61 % tensor
-// cycles, bound by the softmax between the products; the combine of 256 row groups 31 us).
+// of 4k to 32k keys 86 us (468 MB at 5.4 TB/s), 2001 queries over 8190 keys 222 us (partials 191 us, 63 % tensor
+// cycles, bound by the softmax between the products; the combine of 256 row groups 33 us).
 // TMEM columns: S/P buffers at 0 and 128, O accumulators at 256 and 384 (512 total).
 //
 // Every wait is bounded (2 s by default; the main-loop limit is a launch argument): on

@@ -75,10 +75,11 @@ tva_status check_shape(int B, int Hq, int Hkv, int d, int dtype, int max_prefix,
 // workspace takes (a partial row for each query row).
 constexpr int kMaxQueries = 65536;
 
-// Row groups of one KV head up to which cross-attention forms teams (Problem::share).  U / S
-// teams of S leave up to S - 1 workers without work, and with more row groups the products
-// bound the call, not DRAM: beyond, the workers take equal ranges.
-constexpr int kMaxCrossTeam = 8;
+// Whether cross-attention with S row groups a KV head forms teams (Problem::share): where U / S teams
+// leave no more than a sixteenth of the U workers without work; otherwise the workers take equal ranges.
+// Measured on 152 workers (Hq 32, Hkv 8, d = 128, teams / ranges): 13 groups (143 at work) 162 / 219 us, 8 (152)
+// 180 / 199, 10 (150) 125 / 130, 16 (144) 192 / 200, 63 (126) 234 / 219.
+bool cross_teams(int U, int S) { return U >= S && U % S * 16 <= U; }
 
 struct Layout {
   Problem pr;
@@ -114,7 +115,8 @@ tva_status make_layout(int B, int Hq, int Hkv, int d, int dtype, int max_prefix,
   if (B == 1 && W == 2) {
     const int mt1 = (max_nodes + npt - 1) / npt;
     const int mt2 = 2 * ((max_nodes + 2 * npt - 1) / (2 * npt));
-    if (mt1 < mt2) W = 1;
+    // (Cross-attention: where teams are formed.  Workers on ranges want the larger groups.)
+    if (mt1 < mt2 && (!cross || cross_teams(dtype == TVA_FP32 ? sms * tva::simt_workers_per_sm() : sms, mt1))) W = 1;
   }
   L->npt = npt;
   L->W = W;
@@ -136,7 +138,7 @@ tva_status make_layout(int B, int Hq, int Hkv, int d, int dtype, int max_prefix,
   const long long groups = (long long)B * Hkv * mp_max;
   // One sequence whose KV heads have several row groups: teams of workers, one member per
   // row group, stream the same K/V tiles together, so each is read from DRAM once.
-  pr.share = (B == 1 && mp_max >= 2 && pr.U >= mp_max && (!cross || mp_max <= kMaxCrossTeam)) ? mp_max : 0;
+  pr.share = (B == 1 && mp_max >= 2 && pr.U >= mp_max && (!cross || cross_teams(pr.U, mp_max))) ? mp_max : 0;
   // One sequence with one row group per KV head: split each head's tiles over its own
   // U / Hkv workers when Hkv divides U (see Problem::align).
   pr.align = (B == 1 && mp_max == 1 && pr.U % Hkv == 0) ? pr.U / Hkv : 0;
